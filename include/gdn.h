@@ -81,6 +81,8 @@ typedef enum {
  * gdn_status_from_device() maps it to a gdn_status_t. */
 #define GDN_DEV_BAD_SLOT 0x1 /* a slot index was >= num_slots; the row/sequence was skipped */
 #define GDN_DEV_TIMEOUT 0x2  /* a bounded wait expired inside a kernel; its outputs are invalid */
+#define GDN_DEV_BAD_LENGTH 0x4 /* paged calls: a request's lengths are negative or exceed a stated bound; it was skipped */
+#define GDN_DEV_NO_PAGES 0x8   /* gdn_paged_maps: the free list ran out; the requests it could not serve were refused */
 
 typedef struct {
     int32_t h_k;  /* query/key heads */
@@ -352,6 +354,144 @@ gdn_status_t gdn_mixed_step_colaunch(const gdn_dims_t *dims, int32_t num_decodes
                                      void *workspace, size_t workspace_bytes,
                                      int32_t *dev_status, void *stream,
                                      void *aux_stream, void *fork_event, void *join_event);
+
+/* ---- full-attention layers over a paged K/V cache ------------------------
+ *
+ * The layers that a hybrid decoder interleaves with its Gated DeltaNet layers
+ * attend over all cached tokens.  Their keys and values live in fixed-size
+ * pages (the cache blocks of the prefix-cache grid, e.g. 1088 tokens, or
+ * smaller ones) that a block table assigns to requests.  A step is three
+ * calls: gdn_paged_maps (once per step), then per layer gdn_paged_kv_write
+ * and gdn_paged_attention.  All three read the step's lengths on the device,
+ * so a step captured once in a CUDA graph replays for other lengths.
+ */
+
+typedef enum { GDN_BF16 = 0, GDN_FP16 = 1 } gdn_dtype_t;
+
+/* A paged cache: element (page, row, head, i) of K is at
+ * k[page * k_page_stride + row * k_slot_stride + head * k_head_stride + i]
+ * and the same for V; strides are in elements, so [pages][page_size][h][d],
+ * [pages][h][page_size][d] and the K and V halves of one tensor are all
+ * served.  Slot s is row s % page_size of page s / page_size.
+ *   - d in {64, 128, 256}; page_size a multiple of 16;
+ *     num_pages * page_size <= INT32_MAX (slots are int32; offsets into the
+ *     cache are 64-bit);
+ *   - base addresses 16-byte aligned, strides multiples of 8 elements, and
+ *     positive wherever the dimension has more than one entry. */
+typedef struct {
+    void *k, *v;
+    int32_t dtype; /* gdn_dtype_t */
+    int32_t page_size;
+    int32_t h_kv;
+    int32_t d;
+    int64_t num_pages;
+    int64_t k_page_stride, k_slot_stride, k_head_stride;
+    int64_t v_page_stride, v_slot_stride, v_head_stride;
+} gdn_paged_cache_t;
+
+/*
+ * The step's maps from its request lengths: takes the pages that the new
+ * tokens need from a free list into the block table, and gives every new
+ * token its position and its cache slot.
+ *
+ * Request i has c = context_lens[i] cached tokens and m = new_lens[i] new
+ * ones; have = ceil(c / page_size), total = ceil((c + m) / page_size).  Its
+ * total - have new pages are the next entries of the free list, in request
+ * order, and become block_table[i][have .. total).  For its new token u:
+ * position p = c + u, slot = block_table[i][p / page_size] * page_size
+ * + p % page_size.
+ *
+ *   num_reqs       n >= 0.
+ *   context_lens, new_lens  [n] int32.
+ *   block_table    [n] rows of table_width int32 entries, table_stride apart.
+ *   free_pages     [num_free] int32 page ids, or NULL: no page is taken and
+ *                  the table already covers the new tokens.
+ *   free_head      device int32: entries of the list already taken (>= 0).
+ *   free_head_out  device int32: the same after this call; may be free_head.
+ *                  Both are ignored when free_pages is NULL.
+ *   cu_seqlens     [n + 1] int32 out: first token of each request.
+ *   kv_lens        [n] int32 out: c + m, or 0 for a refused request.
+ *   slot_map, positions  [token_capacity] int32 out; tokens past
+ *                  cu_seqlens[n] and tokens of refused requests get slot -1
+ *                  and position 0.
+ * Refusals (the request takes no page, its kv_len is 0, its slots are -1;
+ * the others are served):
+ *   GDN_DEV_BAD_LENGTH  a negative length (a negative new_len counts as no
+ *                tokens), c + m over the table's width or INT32_MAX, or
+ *                tokens past token_capacity (cu_seqlens stops there); a
+ *                negative free_head offers no page.
+ *   GDN_DEV_NO_PAGES  the free list is too short for it; so it is then for
+ *                every later request that needs a page.
+ * A page id outside [0, num_pages) gives its tokens slot -1 (their positions
+ * stay) and sets GDN_DEV_BAD_SLOT.
+ */
+gdn_status_t gdn_paged_maps(int32_t num_reqs, int32_t page_size, int64_t num_pages,
+                            const int32_t *context_lens, const int32_t *new_lens,
+                            int32_t *block_table, int32_t table_width, int64_t table_stride,
+                            const int32_t *free_pages, int32_t num_free,
+                            const int32_t *free_head, int32_t *free_head_out,
+                            int32_t *cu_seqlens, int32_t *kv_lens, int64_t token_capacity,
+                            int32_t *slot_map, int32_t *positions, int32_t *dev_status, void *stream);
+
+/*
+ * Keys and values of the new tokens into the cache: row t of k and v goes to
+ * slot slot_map[t]; a negative slot is skipped (padded token), one past the
+ * cache is skipped with GDN_DEV_BAD_SLOT.  No slot may be given twice.
+ *   k, v      num_tokens rows of [h_kv][d] in the cache's dtype: element
+ *             (t, h, i) at t * token_stride + h * head_stride + i (elements;
+ *             16-byte aligned, strides multiples of 8).
+ */
+gdn_status_t gdn_paged_kv_write(const gdn_paged_cache_t *cache, int64_t num_tokens,
+                                const void *k, int64_t k_token_stride, int64_t k_head_stride,
+                                const void *v, int64_t v_token_stride, int64_t v_head_stride,
+                                const int32_t *slot_map, int32_t *dev_status, void *stream);
+
+/*
+ * Attention of each request's new tokens over its cached ones (the new
+ * tokens' own keys and values written before).  Query token u of request r
+ * (tokens cu_seqlens[r] .. cu_seqlens[r + 1], m of them) stands at position
+ * p = kv_lens[r] - m + u and sees the keys j <= p (with window > 0 only the
+ * last `window` of them, j > p - window); query head h reads K/V head
+ * h / (h_q / h_kv):
+ *     o[t][h] = sum_j softmax_j(scale * q[t][h] . K[j]) V[j]
+ * A token that sees no key (p < 0) gets zeros, as do the tokens from
+ * cu_seqlens[num_reqs] up to num_tokens (a captured step's padding).
+ *
+ *   num_tokens   rows of q and o; cu_seqlens[num_reqs] <= num_tokens.
+ *   h_q          query heads, a multiple of cache->h_kv; h_q / h_kv <= 128.
+ *   q, o         rows of [h_q][d] in the cache's dtype, q rows
+ *                q_token_stride elements apart (a multiple of 8, at least
+ *                h_q * d), o dense; 16-byte aligned.
+ *   block_table  [num_reqs] rows of table_width entries, table_stride apart;
+ *                only the pages of visible keys are looked at.
+ *   max_kv_len   bound on kv_lens that the caller promises (at most
+ *                table_width * page_size, which 0 stands for); it sizes the
+ *                workspace.
+ *   scale        finite, >= 0.
+ *   workspace    gdn_paged_attention_workspace_bytes() bytes for the same
+ *                sizes, 256-byte aligned; needs no initial value.
+ * GDN_DEV_BAD_LENGTH: a request whose kv_len is negative or over max_kv_len
+ * gets zero outputs; one whose cu_seqlens run backwards or past num_tokens is
+ * skipped.  A page id outside [0, num_pages) reads as zero keys
+ * and values (GDN_DEV_BAD_SLOT).
+ * Rows of the cache that no token of the request sees (the rest of its last
+ * page, what the window has left behind) may hold anything, NaN included.
+ * A NaN or infinity in a value that some token of the request sees reaches
+ * that token's output and may reach those of the request's other new tokens.
+ * A request's outputs depend on its own tokens, lengths and cache alone, bit
+ * for bit: not on the batch, the pages it lies in, or the padding.
+ */
+gdn_status_t gdn_paged_attention(const gdn_paged_cache_t *cache, int32_t num_reqs, int64_t num_tokens,
+                                 int32_t h_q, float scale, int32_t window, int64_t max_kv_len,
+                                 const void *q, int64_t q_token_stride, const int32_t *block_table,
+                                 int32_t table_width, int64_t table_stride, const int32_t *cu_seqlens,
+                                 const int32_t *kv_lens, void *o, void *workspace,
+                                 size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/* Device scratch (bytes) of gdn_paged_attention for these sizes;
+ * (size_t)-1 on a bad argument. */
+size_t gdn_paged_attention_workspace_bytes(int32_t h_q, int32_t h_kv, int32_t d, int32_t num_reqs,
+                                           int64_t num_tokens, int64_t max_kv_len);
 
 /* ---- host-only helpers (no device work) ------------------------------- */
 

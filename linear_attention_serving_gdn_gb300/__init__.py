@@ -29,18 +29,21 @@ __all__ = [
     "gdn_prefill_varlen", "gdn_prefill_varlen_apc", "gdn_mixed_step", "gdn_mixed_step_colaunch", "gdn_prefill_num_emits", "gdn_prefill_emit_offsets", "gdn_align_block_size",
     "gdn_floor_prefix_hit", "gdn_grid_emit_every_chunks", "gdn_status_string",
     "gdn_prefill_workspace_bytes", "gdn_status_from_device",
-    "EXPORTED_SYMBOLS", "GDN_DEV_BAD_SLOT", "GDN_DEV_TIMEOUT",
+    "gdn_paged_maps", "gdn_paged_kv_write", "gdn_paged_attention", "gdn_paged_attention_workspace_bytes",
+    "EXPORTED_SYMBOLS", "GDN_DEV_BAD_SLOT", "GDN_DEV_TIMEOUT", "GDN_DEV_BAD_LENGTH", "GDN_DEV_NO_PAGES",
 ]
 
 GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED, GDN_ERR_CUDA = 0, 1, 2, 3
 GDN_ERR_WORKSPACE, GDN_ERR_TIMEOUT = 4, 5
-GDN_DEV_BAD_SLOT, GDN_DEV_TIMEOUT = 0x1, 0x2
+GDN_DEV_BAD_SLOT, GDN_DEV_TIMEOUT, GDN_DEV_BAD_LENGTH, GDN_DEV_NO_PAGES = 0x1, 0x2, 0x4, 0x8
+GDN_BF16, GDN_FP16 = 0, 1
 
 EXPORTED_SYMBOLS = (
     "gdn_decode_packed", "gdn_decode_packed_raw", "gdn_prep_inputs", "gdn_decode_multi",
     "gdn_prefill_varlen", "gdn_prefill_varlen_apc", "gdn_mixed_step", "gdn_mixed_step_colaunch", "gdn_prefill_num_emits", "gdn_prefill_emit_offsets", "gdn_align_block_size",
     "gdn_floor_prefix_hit", "gdn_grid_emit_every_chunks", "gdn_status_string",
     "gdn_prefill_workspace_bytes", "gdn_status_from_device",
+    "gdn_paged_maps", "gdn_paged_kv_write", "gdn_paged_attention", "gdn_paged_attention_workspace_bytes",
 )
 
 
@@ -53,6 +56,13 @@ class GdnError(RuntimeError):
 class Dims(ctypes.Structure):
     _fields_ = [("h_k", ctypes.c_int32), ("h_v", ctypes.c_int32), ("d_k", ctypes.c_int32),
                 ("d_v", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class PagedCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("h_kv", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("num_pages", ctypes.c_int64)] + [
+                    (f"{s}_{n}_stride", ctypes.c_int64) for s in "kv" for n in ("page", "slot", "head")]
 
 
 _P = ctypes.c_void_p
@@ -106,6 +116,18 @@ def _configure(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.gdn_prefill_workspace_bytes.argtypes = [ctypes.POINTER(Dims), _I32, _I64]
     lib.gdn_status_from_device.restype = ctypes.c_int
     lib.gdn_status_from_device.argtypes = [_I32]
+    _F32 = ctypes.c_float
+    lib.gdn_paged_maps.restype = ctypes.c_int
+    lib.gdn_paged_maps.argtypes = [_I32, _I32, _I64, _P, _P, _P, _I32, _I64, _P, _I32, _P, _P, _P, _P, _I64,
+                                   _P, _P, _P, _P]
+    lib.gdn_paged_kv_write.restype = ctypes.c_int
+    lib.gdn_paged_kv_write.argtypes = [ctypes.POINTER(PagedCache), _I64, _P, _I64, _I64, _P, _I64, _I64,
+                                       _P, _P, _P]
+    lib.gdn_paged_attention.restype = ctypes.c_int
+    lib.gdn_paged_attention.argtypes = [ctypes.POINTER(PagedCache), _I32, _I64, _I32, _F32, _I32, _I64,
+                                        _P, _I64, _P, _I32, _I64, _P, _P, _P, _P, _SZ, _P, _P]
+    lib.gdn_paged_attention_workspace_bytes.restype = _SZ
+    lib.gdn_paged_attention_workspace_bytes.argtypes = [_I32, _I32, _I32, _I32, _I64, _I64]
     lib.gdn_prefill_num_emits.restype = _I64
     lib.gdn_prefill_num_emits.argtypes = [_P, _I32, _I32]
     lib.gdn_prefill_emit_offsets.restype = ctypes.c_int
@@ -502,6 +524,134 @@ def gdn_mixed_step_colaunch(num_decodes: int, q, k, v, g, beta, cu_seqlens_p, cu
         extra = [ctypes.c_void_p(aux_stream.cuda_stream), _event_handle(fork_event, stream),
                  _event_handle(join_event, stream)]
     _check(lib.gdn_mixed_step_colaunch(*args, *extra), "gdn_mixed_step_colaunch")
+
+
+# ---------------------------------------------------------------------------
+# full-attention layers over a paged K/V cache
+# ---------------------------------------------------------------------------
+
+_PAGED_DTYPES = {torch.bfloat16: GDN_BF16, torch.float16: GDN_FP16}
+
+
+def _strided(t, name, dtype, ndim):
+    """A CUDA tensor whose last dimension is contiguous; its other strides are free."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dims, got {tuple(t.shape)}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return t
+
+
+def _paged_cache(k_cache, v_cache):
+    dtype = getattr(k_cache, "dtype", None)
+    if dtype not in _PAGED_DTYPES:
+        raise TypeError(f"k_cache must be bfloat16 or float16, got {dtype}")
+    _strided(k_cache, "k_cache", dtype, 4), _strided(v_cache, "v_cache", dtype, 4)
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must have the same shape")
+    pages, page_size, h_kv, d = k_cache.shape
+    return PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), _PAGED_DTYPES[dtype], page_size, h_kv, d, pages,
+                      *k_cache.stride()[:3], *v_cache.stride()[:3])
+
+
+def _block_table(t):
+    """The checked table and its row stride (one row's stride says nothing: its width stands for it)."""
+    t = _strided(t, "block_table", torch.int32, 2)
+    return t, t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def gdn_paged_maps(context_lens, new_lens, block_table, page_size: int, num_pages: int, cu_seqlens, kv_lens,
+                   slot_map, positions, free_pages=None, free_head=None, free_head_out=None, dev_status=None,
+                   stream=None) -> None:
+    """Maps of a step from its request lengths: pages from the free list into
+    ``block_table`` (in place), ``cu_seqlens``, ``kv_lens``, and the slot and
+    position of every new token (see gdn.h).  ``free_head_out`` defaults to
+    ``free_head``, which then advances in place."""
+    lib = load_library()
+    i32 = torch.int32
+    context_lens, new_lens = _dev(context_lens, "context_lens", i32, 1), _dev(new_lens, "new_lens", i32, 1)
+    block_table, table_stride = _block_table(block_table)
+    cu_seqlens, kv_lens = _dev(cu_seqlens, "cu_seqlens", i32, 1), _dev(kv_lens, "kv_lens", i32, 1)
+    slot_map, positions = _dev(slot_map, "slot_map", i32, 1), _dev(positions, "positions", i32, 1)
+    free_pages = _dev(free_pages, "free_pages", i32, 1, optional=True)
+    free_head = _dev(free_head, "free_head", i32, optional=free_pages is None)
+    free_head_out = free_head if free_head_out is None else _dev(free_head_out, "free_head_out", i32)
+    dev_status = _dev(dev_status, "dev_status", i32, optional=True)
+    n = context_lens.shape[0]
+    if not (new_lens.shape[0] == n and block_table.shape[0] == n and cu_seqlens.shape[0] == n + 1
+            and kv_lens.shape[0] == n and positions.shape == slot_map.shape):
+        raise ValueError("inconsistent paged-maps shapes")
+    # an empty list serves no page, unlike no list at all: any non-null pointer stands for it
+    pages = None if free_pages is None else (free_pages.data_ptr() or cu_seqlens.data_ptr())
+    _check(lib.gdn_paged_maps(n, int(page_size), int(num_pages), _ptr(context_lens), _ptr(new_lens),
+                              _ptr(block_table), block_table.shape[1], table_stride,
+                              pages, 0 if free_pages is None else free_pages.shape[0], _ptr(free_head),
+                              _ptr(free_head_out), _ptr(cu_seqlens), _ptr(kv_lens), slot_map.shape[0],
+                              _ptr(slot_map), _ptr(positions), _ptr(dev_status), _stream(stream)),
+           "gdn_paged_maps")
+
+
+def gdn_paged_kv_write(k, v, k_cache, v_cache, slot_map, dev_status=None, stream=None) -> None:
+    """Rows of ``k`` and ``v`` ([T][h_kv][d]) into the caches' slots
+    ``slot_map`` (see gdn.h).  The caches are viewed as
+    [pages][page_size][h_kv][d]; any strides with a contiguous last dimension."""
+    lib = load_library()
+    cache = _paged_cache(k_cache, v_cache)
+    k, v = _strided(k, "k", k_cache.dtype, 3), _strided(v, "v", k_cache.dtype, 3)
+    slot_map = _dev(slot_map, "slot_map", torch.int32, 1)
+    dev_status = _dev(dev_status, "dev_status", torch.int32, optional=True)
+    if not (k.shape == v.shape and k.shape[1:] == k_cache.shape[2:] and slot_map.shape[0] == k.shape[0]):
+        raise ValueError("inconsistent K/V write shapes")
+    _check(lib.gdn_paged_kv_write(ctypes.byref(cache), k.shape[0], _ptr(k), k.stride(0), k.stride(1), _ptr(v),
+                                  v.stride(0), v.stride(1), _ptr(slot_map), _ptr(dev_status), _stream(stream)),
+           "gdn_paged_kv_write")
+
+
+def gdn_paged_attention_workspace_bytes(h_q: int, h_kv: int, d: int, num_reqs: int, num_tokens: int,
+                                        max_kv_len: int) -> int:
+    """Device scratch (bytes) of a ``gdn_paged_attention`` call of these sizes."""
+    n = load_library().gdn_paged_attention_workspace_bytes(int(h_q), int(h_kv), int(d), int(num_reqs),
+                                                           int(num_tokens), int(max_kv_len))
+    if n == ctypes.c_size_t(-1).value:
+        raise ValueError("invalid paged-attention sizes")
+    return int(n)
+
+
+def gdn_paged_attention(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, o, scale=None, window: int = 0,
+                        max_kv_len: int = 0, workspace=None, dev_status=None, stream=None) -> None:
+    """Attention of each request's new tokens over its cached ones (see
+    gdn.h).  ``q`` is [T][h_q][d] (rows may be slices of a wider tensor), ``o``
+    dense; ``scale`` defaults to d ** -0.5; ``max_kv_len`` bounds ``kv_lens``
+    (0: what the block table can hold); ``workspace`` is a uint8 tensor of
+    ``gdn_paged_attention_workspace_bytes`` for that bound."""
+    lib = load_library()
+    i32 = torch.int32
+    cache = _paged_cache(k_cache, v_cache)
+    q = _strided(q, "q", k_cache.dtype, 3)
+    o = _dev(o, "o", k_cache.dtype, 3)
+    block_table, table_stride = _block_table(block_table)
+    cu_seqlens, kv_lens = _dev(cu_seqlens, "cu_seqlens", i32, 1), _dev(kv_lens, "kv_lens", i32, 1)
+    workspace = _dev(workspace, "workspace", torch.uint8, optional=True)
+    dev_status = _dev(dev_status, "dev_status", i32, optional=True)
+    T, h_q, d = q.shape
+    n = kv_lens.shape[0]
+    if not (o.shape == q.shape and d == cache.d and cu_seqlens.shape[0] == n + 1 and block_table.shape[0] == n):
+        raise ValueError("inconsistent paged-attention shapes")
+    if q.stride(1) != d and h_q > 1:
+        raise ValueError("q's heads must be adjacent")
+    _check(lib.gdn_paged_attention(ctypes.byref(cache), n, T, h_q, d ** -0.5 if scale is None else scale,
+                                   int(window), int(max_kv_len), _ptr(q), q.stride(0), _ptr(block_table),
+                                   block_table.shape[1], table_stride,
+                                   _ptr(cu_seqlens), _ptr(kv_lens), _ptr(o), _ptr(workspace),
+                                   0 if workspace is None else workspace.numel(), _ptr(dev_status),
+                                   _stream(stream)),
+           "gdn_paged_attention")
 
 
 # ---------------------------------------------------------------------------
