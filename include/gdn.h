@@ -373,7 +373,7 @@ typedef enum { GDN_BF16 = 0, GDN_FP16 = 1 } gdn_dtype_t;
  * and the same for V; strides are in elements, so [pages][page_size][h][d],
  * [pages][h][page_size][d] and the K and V halves of one tensor are all
  * served.  Slot s is row s % page_size of page s / page_size.
- *   - d in {64, 128, 256}; page_size a multiple of 16;
+ *   - d in {64, 128, 256}; page_size a multiple of 16; num_pages >= 1;
  *     num_pages * page_size <= INT32_MAX (slots are int32; offsets into the
  *     cache are 64-bit);
  *   - base addresses 16-byte aligned, strides multiples of 8 elements, and
@@ -465,8 +465,8 @@ gdn_status_t gdn_paged_kv_write(const gdn_paged_cache_t *cache, int64_t num_toke
  *   block_table  [num_reqs] rows of table_width entries, table_stride apart;
  *                only the pages of visible keys are looked at.
  *   max_kv_len   bound on kv_lens that the caller promises (at most
- *                table_width * page_size, which 0 stands for); it sizes the
- *                workspace.
+ *                table_width * page_size, which 0 stands for, and 2^30); it
+ *                sizes the workspace.
  *   scale        finite, >= 0.
  *   workspace    gdn_paged_attention_workspace_bytes() bytes for the same
  *                sizes, 256-byte aligned; needs no initial value.

@@ -7,6 +7,8 @@
 
 namespace {
 
+constexpr int64_t kMaxStride = int64_t{1} << 39;  // elements: a tensor map's strides are under 2^40 bytes
+constexpr int64_t kMaxKeys = int64_t{1} << 30;    // keys of a request: key indices stay inside int32
 constexpr int32_t kMaxGroup = 128;  // query heads per K/V head: one token's heads fit a 128-row tile
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -15,19 +17,19 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // one is replaced by the row length, so that tensor maps always see a valid value.
 bool stride_ok(int64_t *stride, int64_t entries, int64_t row) {
     if (entries <= 1) *stride = row;
-    return *stride > 0 && *stride % 8 == 0 && *stride <= (INT64_MAX >> 4) / (entries > 1 ? entries : 1);
+    return *stride > 0 && *stride % 8 == 0 && *stride < kMaxStride;
 }
 
 // Checks a cache description and fills unused strides of the copy.
 gdn_status_t cache_ok(const gdn_paged_cache_t *in, gdn_paged_cache_t *c) {
     if (!in) return GDN_ERR_INVALID_ARG;
     *c = *in;
-    if (c->h_kv <= 0 || c->d <= 0 || c->page_size <= 0 || c->num_pages < 0) return GDN_ERR_INVALID_ARG;
+    if (c->h_kv <= 0 || c->d <= 0 || c->page_size <= 0 || c->num_pages <= 0) return GDN_ERR_INVALID_ARG;
     if (c->dtype != GDN_BF16 && c->dtype != GDN_FP16) return GDN_ERR_UNSUPPORTED;
     if (c->d != 64 && c->d != 128 && c->d != 256) return GDN_ERR_UNSUPPORTED;
     if (c->page_size % 16 != 0) return GDN_ERR_UNSUPPORTED;
     if (c->num_pages > INT_MAX / c->page_size) return GDN_ERR_UNSUPPORTED;
-    if (c->num_pages > 0 && (!c->k || !c->v)) return GDN_ERR_INVALID_ARG;
+    if (!c->k || !c->v) return GDN_ERR_INVALID_ARG;
     if (!aligned16(c->k) || !aligned16(c->v)) return GDN_ERR_INVALID_ARG;
     if (!stride_ok(&c->k_page_stride, c->num_pages, c->d) || !stride_ok(&c->v_page_stride, c->num_pages, c->d) ||
         !stride_ok(&c->k_slot_stride, c->page_size, c->d) || !stride_ok(&c->v_slot_stride, c->page_size, c->d) ||
@@ -107,7 +109,7 @@ gdn_status_t gdn_paged_kv_write(const gdn_paged_cache_t *cache, int64_t num_toke
 size_t gdn_paged_attention_workspace_bytes(int32_t h_q, int32_t h_kv, int32_t d, int32_t num_reqs,
                                            int64_t num_tokens, int64_t max_kv_len) {
     if (h_q <= 0 || h_kv <= 0 || h_q % h_kv != 0 || h_q / h_kv > kMaxGroup || (d != 64 && d != 128 && d != 256) ||
-        num_reqs < 0 || num_tokens < 0 || num_tokens > INT_MAX || max_kv_len < 0 || max_kv_len > INT_MAX)
+        num_reqs < 0 || num_tokens < 0 || num_tokens > INT_MAX || max_kv_len < 0 || max_kv_len > kMaxKeys)
         return static_cast<size_t>(-1);
     return gdn::paged_attention_workspace(h_q, h_kv, d, num_reqs, num_tokens, max_kv_len);
 }
@@ -127,8 +129,8 @@ gdn_status_t gdn_paged_attention(const gdn_paged_cache_t *cache, int32_t num_req
     if (h_q / c.h_kv > kMaxGroup || num_tokens > INT_MAX || num_tokens > INT_MAX / h_q) return GDN_ERR_UNSUPPORTED;
     const int64_t table_tokens = static_cast<int64_t>(table_width) * c.page_size;
     if (max_kv_len < 0 || max_kv_len > table_tokens) return GDN_ERR_INVALID_ARG;
-    if (max_kv_len == 0) max_kv_len = table_tokens < INT_MAX ? table_tokens : INT_MAX;
-    if (max_kv_len > INT_MAX) return GDN_ERR_UNSUPPORTED;
+    if (max_kv_len == 0) max_kv_len = table_tokens < kMaxKeys ? table_tokens : kMaxKeys;
+    if (max_kv_len > kMaxKeys) return GDN_ERR_UNSUPPORTED;
     if (num_tokens == 0) return GDN_OK;
     if (!q || !o || !cu_seqlens || !aligned16(q) || !aligned16(o)) return GDN_ERR_INVALID_ARG;
     if (num_reqs > 0 && (!kv_lens || (table_width > 0 && (!block_table || table_stride < table_width))))

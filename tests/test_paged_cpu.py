@@ -31,7 +31,7 @@ def cache(gdn, **kw):
 
 BAD_CACHES = [
     (dict(d=96), UNSUPPORTED), (dict(d=0), INVALID), (dict(page_size=24), UNSUPPORTED), (dict(page_size=0), INVALID),
-    (dict(dtype=2), UNSUPPORTED), (dict(h_kv=0), INVALID), (dict(num_pages=-1), INVALID),
+    (dict(dtype=2), UNSUPPORTED), (dict(h_kv=0), INVALID), (dict(num_pages=-1), INVALID), (dict(num_pages=0), INVALID),
     (dict(num_pages=1 << 27), UNSUPPORTED), (dict(k=None), INVALID), (dict(v=0x10008), INVALID),
     (dict(k_slot_stride=260), INVALID), (dict(v_page_stride=0), INVALID), (dict(k_head_stride=-128), INVALID),
     (dict(v_page_stride=1 << 60), INVALID),
