@@ -43,6 +43,7 @@
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
 #include <limits.h>
+#include <stddef.h>
 
 #ifndef GDN_WAIT_CYCLES
 #define GDN_WAIT_CYCLES 2000000000LL
@@ -67,11 +68,10 @@ bool encode_tiles(CUtensorMap *m, const void *base, int dtype, int rank, const c
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr int kThreads = 256;
-constexpr int kRows = 128;   // query rows of a tile (TMEM lanes)
-constexpr int kKeys = 128;   // keys of a tile
+constexpr int kRows = 128;     // query rows of a tile (TMEM lanes)
+constexpr int kKeys = 128;     // keys of a tile
 constexpr int kPanel = 16384;  // 128 rows of 64 16-bit elements
-constexpr int kItems = 4;    // items between the scheduler and the other warps
+constexpr int kItems = 2;      // items between the scheduler and the other warps
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 256;  // O after the two S buffers
 
@@ -81,9 +81,12 @@ constexpr int kSplitUnits = 152;
 constexpr int kMaxSplits = 64;
 constexpr int kMinSplitTiles = 2;
 
+// Row tiles that a block works on at once: two where two accumulators fit TMEM.
+__host__ __device__ constexpr int streams_of(int d) { return d <= 128 ? 2 : 1; }
+
 struct Plan {
-    int32_t row_tiles;    // tiles of query rows
-    int32_t tile_tokens;  // tokens of one
+    int32_t row_items;    // pieces of the new tokens
+    int32_t item_tokens;  // tokens of one
     int32_t split_tiles;  // key tiles of a split
     int32_t split0, splits;
     int64_t items;
@@ -102,16 +105,17 @@ __device__ __forceinline__ void key_tiles(int32_t kv, int32_t m, int32_t u, int3
 }
 
 // How a request of m new tokens and kv keys is cut; depends on nothing else of the batch.
-__device__ __forceinline__ Plan plan_request(int32_t kv, int32_t m, int32_t group, int32_t h_kv, int32_t window) {
+__device__ __forceinline__ Plan plan_request(int32_t kv, int32_t m, int32_t group, int32_t streams, int32_t h_kv,
+                                             int32_t window) {
     Plan p;
-    p.tile_tokens = kRows / group;
-    p.row_tiles = ceil_div(m, p.tile_tokens);
+    p.item_tokens = kRows / group * streams;
+    p.row_items = ceil_div(m, p.item_tokens);
     int32_t lo, hi;
     key_tiles(kv, m, 0, m, window, &lo, &hi);
     p.split_tiles = INT_MAX;
     p.split0 = 0;
     p.splits = 1;
-    const int64_t units = static_cast<int64_t>(p.row_tiles) * h_kv;
+    const int64_t units = static_cast<int64_t>(p.row_items) * h_kv;
     if (m > 0 && units * 2 <= kSplitUnits) {
         int32_t want = kSplitUnits / static_cast<int32_t>(units);
         if (want > kMaxSplits) want = kMaxSplits;
@@ -128,36 +132,55 @@ __device__ __forceinline__ Plan plan_request(int32_t kv, int32_t m, int32_t grou
 // Bound of `partials` over the requests of a call: at most `want` splits and
 // one more where a window starts inside one, and never more than the longest
 // context has.
-int64_t partials_bound(int32_t group, int32_t h_kv, int32_t num_reqs, int64_t num_tokens, int64_t max_kv_len) {
+int64_t partials_bound(int32_t group, int32_t streams, int32_t h_kv, int32_t num_reqs, int64_t num_tokens, int64_t max_kv_len) {
     const int64_t tiles = (max_kv_len + kKeys - 1) / kKeys;
     if (h_kv * 2 > kSplitUnits || tiles <= kMinSplitTiles || num_tokens == 0 || num_reqs == 0) return 0;
     const int32_t want = kSplitUnits / h_kv < kMaxSplits ? kSplitUnits / h_kv : kMaxSplits;
     const int64_t by_length = (tiles + kMinSplitTiles - 1) / kMinSplitTiles;
     const int64_t splits = want < by_length ? want : by_length;
-    // m tokens make at least m / tile_tokens row tiles, so m * want <= tile_tokens * kSplitUnits / h_kv
-    const int64_t by_request = static_cast<int64_t>(num_reqs) * (kRows / group) * ceil_div(kSplitUnits, h_kv);
+    // m tokens make at least m / item_tokens row items, so m * want <= item_tokens * kSplitUnits / h_kv
+    const int64_t by_request = static_cast<int64_t>(num_reqs) * (kRows / group * streams) * ceil_div(kSplitUnits, h_kv);
     const int64_t by_token = num_tokens * splits;
     return (by_token < by_request ? by_token : by_request) + num_tokens;
 }
 
-// Workspace: first partial of each request, then (m, l) and O of the partials.
+// Bound of the items of a call.
+int64_t items_bound(int32_t group, int32_t streams, int32_t h_kv, int32_t num_reqs, int64_t num_tokens, bool split) {
+    const int64_t rows = num_tokens / (kRows / group * streams) + num_reqs;
+    return (rows < num_tokens ? rows : num_tokens) * h_kv * (split ? kMaxSplits + 1 : 1);
+}
+
+// Workspace: the item counter, the first partial of each request, then (m, l)
+// and O of the partials.
 struct Workspace {
+    unsigned long long *counter;  // null: items are dealt round robin
     int64_t *base;
     float2 *ml;
-    float *o;
+    float *o;  // null: no request of this call can be split
+    int64_t partials;
     size_t bytes;
 };
-Workspace workspace_at(void *ws, int32_t num_reqs, int64_t partials, int32_t h_q, int32_t d) {
+Workspace workspace_at(void *ws, int32_t h_q, int32_t h_kv, int32_t d, int32_t num_reqs, int64_t num_tokens,
+                       int64_t max_kv_len) {
     auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
-    Workspace w;
+    const int32_t group = h_q / h_kv, streams = streams_of(d);
+    Workspace w = {};
     char *p = static_cast<char *>(ws);
-    const size_t rows = static_cast<size_t>(partials) * h_q;
-    w.base = reinterpret_cast<int64_t *>(p);
-    size_t at = up(static_cast<size_t>(num_reqs) * sizeof(int64_t));
-    w.ml = reinterpret_cast<float2 *>(p + at);
-    at += up(rows * sizeof(float2));
-    w.o = reinterpret_cast<float *>(p + at);
-    w.bytes = at + rows * d * sizeof(float);
+    w.partials = partials_bound(group, streams, h_kv, num_reqs, num_tokens, max_kv_len);
+    // One item per block at most: nothing to balance.
+    if (items_bound(group, streams, h_kv, num_reqs, num_tokens, w.partials > 0) > kSplitUnits) {
+        w.counter = reinterpret_cast<unsigned long long *>(p);
+        w.bytes = 256;
+    }
+    if (w.partials > 0) {
+        const size_t rows = static_cast<size_t>(w.partials) * h_q;
+        w.base = reinterpret_cast<int64_t *>(p + w.bytes);
+        w.bytes += up(static_cast<size_t>(num_reqs) * sizeof(int64_t));
+        w.ml = reinterpret_cast<float2 *>(p + w.bytes);
+        w.bytes += up(rows * sizeof(float2));
+        w.o = reinterpret_cast<float *>(p + w.bytes);
+        w.bytes += rows * d * sizeof(float);
+    }
     return w;
 }
 
@@ -166,8 +189,7 @@ struct AttentionLaunch {
     CUtensorMap tm_q_one;  // the same, one token
     CUtensorMap tm_k, tm_v;  // [page][head][row][d]: boxes of box_rows x 64
     PagedAttentionArgs a;
-    Workspace ws;       // o null: no request of this call can be split
-    int64_t partials;   // that the workspace holds
+    Workspace ws;
     int32_t group, box_rows;
     float c;  // scale * log2(e)
 };
@@ -175,7 +197,7 @@ struct AttentionLaunch {
 struct Item {
     int32_t stop;
     int32_t req, head;  // request, K/V head
-    int32_t tok, n;     // first token (row of q) and tokens of the row tile
+    int32_t tok, n;     // first token (row of q) and tokens
     int32_t pos;        // position of the first token
     int32_t lo, hi;     // key tiles
     int32_t splits;     // of the request
@@ -184,54 +206,95 @@ struct Item {
 
 template <int D>
 struct Shape {
+    static constexpr int kStreams = streams_of(D);
+    static constexpr int kThreads = 128 + 128 * kStreams;
     static constexpr int kCols = D < 128 ? D : 128;  // columns of a stage
     static constexpr int kHalves = D / kCols;        // stages of a K or V tile
     static constexpr int kPanels = kCols / 64;
     static constexpr uint32_t kStage = kPanels * kPanel;
-    static constexpr uint32_t kQ = D / 64 * kPanel;
-    // As many stages as 227 KB hold beside Q and 1.5 KB of barriers and items.
-    static constexpr int kStages = (227 * 1024 - 1024 - 1536 - static_cast<int>(kQ)) / static_cast<int>(kStage);
-    static constexpr uint32_t kSmem = 1024 + kQ + kStages * kStage + 1536;
+    static constexpr uint32_t kQTile = D / 64 * kPanel;
+    static constexpr uint32_t kQ = kStreams * kQTile;
+    // Q of an item while the next one's loads: with two streams each single tile has its own half, else few rows
+    // (kSmallRows) lie at row 0 or 64 of the tile (a product reads the 128 rows from there; the rest is not used).
+    static constexpr int kSmallRows = 64;
+    static constexpr uint32_t kQSlot = kStreams == 2 ? kQTile : kSmallRows * 128;
+    // As many stages as 227 KB hold beside Q and the control block.
+    static constexpr int kControl = 2048;
+    static constexpr int kStages = (227 * 1024 - 1024 - kControl - static_cast<int>(kQ)) / static_cast<int>(kStage);
+    static constexpr uint32_t kSmem = 1024 + kQ + kStages * kStage + kControl;
 };
 
 template <int D>
 struct Control {
     uint64_t kv_full[Shape<D>::kStages], kv_empty[Shape<D>::kStages];
-    uint64_t q_full, q_empty;
+    uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2], p_full[2];
-    uint64_t o_done, o_free;
+    uint64_t o_done[2], o_free[2], ml_full[2];
     uint64_t item_full[kItems], item_empty[kItems];
     uint64_t drain;
     Item items[kItems];
     uint32_t tmem;
     int fail;
+    // (m, l) of one warpgroup for the other; row r is only touched by the two threads of row r, in turn.
+    float2 ml[Shape<D>::kStreams == 2 ? kRows : 1];
+};
+
+// Units.  The work of an item is a sequence of units, each one S = Q K^T and
+// one O += P V over a tile of keys; units of all items are numbered on, and
+// unit g uses S/P buffer g % 2.  With one stream (d = 256) unit j of an item
+// is key tile j and there is one O.  With two streams buffer, O and softmax
+// warpgroup go together (w = g % 2): an item of two row tiles ("dual") takes
+// each key tile twice, once per row tile; an item of one row tile gives its
+// even key tiles to one warpgroup and its odd ones to the other, each with its
+// own m, l and O, joined at the end.  The tensor core gets
+// QK(g), PV(g - 1), QK(g + 1), ..., so the scores of one unit are computed
+// while the weights of the one before are.
+//
+// The ring holds K and V tiles in the order of their first use.  V of the last
+// tile of an item of one row tile is used after the next item's first K and
+// lies behind it.  `first` is the item's first stage, `late` whether such a V
+// of the item before lies behind its first K.
+struct Ring {
+    uint32_t first = 0, late = 0;
+    // in tiles from `first`:
+    __device__ __forceinline__ uint32_t k_at(uint32_t t, bool dual) const {
+        return t == 0 ? 0 : dual ? late + 2 * t : late + 2 * t - 1;
+    }
+    __device__ __forceinline__ uint32_t v_at(uint32_t t, bool dual) const {
+        return dual ? 1 + late + 2 * t : 2 + late + 2 * t;
+    }
+    __device__ __forceinline__ void next(uint32_t tiles, bool dual, uint32_t halves) {
+        first += halves * (late + 2 * tiles - (dual ? 0 : 1));
+        late = dual ? 0 : 1;
+    }
 };
 
 constexpr long long kWaitCycles = GDN_WAIT_CYCLES;
 constexpr long long kDrainCycles = 2000000000LL;
 
 // Bounded wait for the phase of `bar` with the given parity; gives up as soon
-// as any thread has flagged a failure, and flags one when it runs out.
+// as any thread has flagged a failure, and flags one when it runs out (the
+// block reports it at its end).
 struct Waiter {
-    int *fail;
-    int32_t *status;
-    __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity) const {
+    volatile int *fail;
+    // bar: shared-memory address
+    __device__ __forceinline__ bool at(uint32_t bar, uint32_t parity) const {
         if (tc::mbar_try_wait(bar, parity)) return true;
         const long long start = clock64();
         while (!tc::mbar_try_wait(bar, parity)) {
-            if (*reinterpret_cast<volatile int *>(fail)) return false;
+            if (*fail) return false;
             if (clock64() - start > kWaitCycles) {
-                atomicExch(fail, 1);
-                report(status, GDN_DEV_TIMEOUT);
+                *fail = 1;
                 return false;
             }
         }
         return true;
     }
-    // The same for a whole warp: true for all lanes or for none.
-    __device__ __forceinline__ bool all(uint64_t *bar, uint32_t parity) const {
-        return __all_sync(0xffffffffu, (*this)(bar, parity));
+    // For a whole warp: true for all lanes or for none.
+    __device__ __forceinline__ bool all(uint32_t bar, uint32_t parity) const {
+        return __all_sync(0xffffffffu, at(bar, parity));
     }
+    __device__ __forceinline__ bool all(uint64_t *bar, uint32_t parity) const { return all(tc::smem_u32(bar), parity); }
 };
 __device__ __forceinline__ void drain_bar(uint64_t *bar, uint32_t parity) {
     const long long start = clock64();
@@ -263,7 +326,7 @@ struct Request {
 // Lengths of request r; m = 0 (nothing to do) where its token range is bad, kv = 0 (no keys) where its length is.
 __device__ __forceinline__ Request load_request(const PagedAttentionArgs &a, int64_t r, bool tell) {
     Request q = {0, 0, 0};
-    if (r < a.num_reqs) {
+    if (r >= 0 && r < a.num_reqs) {
         const int32_t b = a.cu_seqlens[r], e = a.cu_seqlens[r + 1], kv = a.kv_lens[r];
         const bool range = b >= 0 && b <= e && e <= a.num_tokens, len = kv >= 0 && kv <= a.max_kv_len;
         if (range) q = {b, e - b, len ? kv : 0};
@@ -272,27 +335,50 @@ __device__ __forceinline__ Request load_request(const PagedAttentionArgs &a, int
     return q;
 }
 
+// Tokens that see no key: zeros, by the scheduler itself.
+template <int D>
+__device__ __forceinline__ void zero_rows(const PagedAttentionArgs &a, const Item &it, int32_t group, int lane) {
+    const int32_t pieces = group * (D / 8);
+    for (int32_t i = lane; i < it.n * pieces; i += 32)
+        reinterpret_cast<uint4 *>(a.o + ((static_cast<int64_t>(it.tok) + i / pieces) * a.h_q + it.head * group) * D)[i % pieces] =
+            make_uint4(0, 0, 0, 0);
+}
+
 template <int D>
 __device__ void schedule(const AttentionLaunch &L, Control<D> *ctl, const Waiter &wait) {
     const PagedAttentionArgs &a = L.a;
     const int lane = threadIdx.x & 31;
     const bool first_block = blockIdx.x == 0;
     uint32_t n = 0;
+    int64_t next = -1;
+    // The next item's number, taken when there is room for the item.
+    auto advance = [&]() {
+        if (!wait.all(ctl->item_empty + n % kItems, (n / kItems & 1) ^ 1)) return false;
+        if (!L.ws.counter) {
+            next = next < 0 ? blockIdx.x : next + gridDim.x;
+        } else {
+            unsigned long long x = 0;
+            if (lane == 0) x = atomicAdd(L.ws.counter, 1ull);
+            next = static_cast<int64_t>(__shfl_sync(0xffffffffu, x, 0));
+        }
+        return true;
+    };
     auto publish = [&](const Item &it) {
         const uint32_t s = n % kItems;
-        if (!wait.all(ctl->item_empty + s, (n / kItems & 1) ^ 1)) return false;
         if (lane == 0) {
             ctl->items[s] = it;
             tc::mbar_arrive(ctl->item_full + s);
         }
         ++n;
         __syncwarp();
-        return true;
     };
-    int64_t next = blockIdx.x, items0 = 0, partials0 = 0;
+    if (!advance()) return;
+    int64_t items0 = 0, partials0 = 0;
+    // From the last request to the first: long prompts stand behind the decode rows and should start first.
     for (int64_t base = 0; base < a.num_reqs; base += 32) {
-        const Request q = load_request(a, base + lane, first_block);
-        const Plan p = plan_request(q.kv, q.m, L.group, a.cache.h_kv, a.window);
+        const int64_t r = a.num_reqs - 1 - base - lane;
+        const Request q = load_request(a, r, first_block);
+        const Plan p = plan_request(q.kv, q.m, L.group, streams_of(D), a.cache.h_kv, a.window);
         int64_t items = p.items, partials = p.partials;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -302,28 +388,29 @@ __device__ void schedule(const AttentionLaunch &L, Control<D> *ctl, const Waiter
                 partials += y;
             }
         }
-        if (first_block && L.ws.o && base + lane < a.num_reqs) L.ws.base[base + lane] = partials0 + partials - p.partials;
+        if (first_block && L.ws.o && r >= 0) L.ws.base[r] = partials0 + partials - p.partials;
         const int64_t group_items = __shfl_sync(0xffffffffu, items, 31);
         while (next < items0 + group_items) {
             const int src = __ffs(__ballot_sync(0xffffffffu, items0 + items > next)) - 1;
-            // Items of a request: row tiles of one (split, head) next to each other, longest first.
-            const int64_t local = next - items0 - __shfl_sync(0xffffffffu, items - p.items, src);
+            // Items of a request: the row items of one (split, head) next to each other, longest first.
+            // (at most h_kv times the row items, or few splits of few: 32 bits)
+            const uint32_t local = static_cast<uint32_t>(next - items0 - __shfl_sync(0xffffffffu, items - p.items, src));
             const int32_t m = __shfl_sync(0xffffffffu, q.m, src), kv = __shfl_sync(0xffffffffu, q.kv, src);
-            const int32_t row_tiles = __shfl_sync(0xffffffffu, p.row_tiles, src);
+            const int32_t row_items = __shfl_sync(0xffffffffu, p.row_items, src);
             const int32_t split_tiles = __shfl_sync(0xffffffffu, p.split_tiles, src);
             const int32_t split0 = __shfl_sync(0xffffffffu, p.split0, src);
             const int32_t splits = __shfl_sync(0xffffffffu, p.splits, src);
             const int32_t first = __shfl_sync(0xffffffffu, q.first, src);
             const int64_t pbase = partials0 + __shfl_sync(0xffffffffu, partials - p.partials, src);
-            const int32_t tile = row_tiles - 1 - static_cast<int32_t>(local % row_tiles);
-            const int32_t rest = static_cast<int32_t>(local / row_tiles);
-            const int32_t head = rest % a.cache.h_kv, split = split0 + rest / a.cache.h_kv;
+            const int32_t rest = static_cast<int32_t>(local / static_cast<uint32_t>(row_items));
+            const int32_t piece = row_items - 1 - static_cast<int32_t>(local - static_cast<uint32_t>(rest) * row_items);
+            const int32_t split = split0 + rest / a.cache.h_kv;
             Item it;
             it.stop = 0;
-            it.req = static_cast<int32_t>(base) + src;
-            it.head = head;
-            const int32_t u = tile * p.tile_tokens;
-            it.n = m - u < p.tile_tokens ? m - u : p.tile_tokens;
+            it.req = static_cast<int32_t>(a.num_reqs - 1 - base) - src;
+            it.head = rest % a.cache.h_kv;
+            const int32_t u = piece * p.item_tokens;
+            it.n = m - u < p.item_tokens ? m - u : p.item_tokens;
             it.tok = first + u;
             it.pos = kv - m + u;
             it.splits = splits;
@@ -334,18 +421,18 @@ __device__ void schedule(const AttentionLaunch &L, Control<D> *ctl, const Waiter
             it.lo = s_lo > lo ? static_cast<int32_t>(s_lo) : lo;
             it.hi = s_hi < hi ? static_cast<int32_t>(s_hi) : hi;
             it.partial = whole ? -1 : pbase + static_cast<int64_t>(u) * splits + (split - split0);
+            // A split past what the tokens see has nothing to do; tokens that see nothing are written by the first.
+            bool run = it.lo < it.hi || (lo == hi && split == split0);
             // Token ranges that overlap can ask for more partials than there are tokens for.
-            if (!whole && pbase + static_cast<int64_t>(m) * splits > L.partials) {
+            if (run && !whole && pbase + static_cast<int64_t>(m) * splits > L.ws.partials) {
                 if (lane == 0) report(a.dev_status, GDN_DEV_BAD_LENGTH);
-                next += gridDim.x;
-                continue;
+                run = false;
             }
-            // A split past what the tile sees has nothing to do; a tile that sees nothing is written by the first.
-            if (it.lo < it.hi || (lo == hi && split == split0)) {
-                if (it.lo >= it.hi) it.lo = it.hi = 0;
-                if (!publish(it)) return;
-            }
-            next += gridDim.x;
+            if (run && it.lo < it.hi)
+                publish(it);
+            else if (run)
+                zero_rows<D>(a, it, L.group, lane);
+            if (!advance()) return;
         }
         items0 += group_items;
         partials0 += __shfl_sync(0xffffffffu, partials, 31);
@@ -361,257 +448,454 @@ __device__ __forceinline__ void visible_rows(const Item &it, int32_t window, int
     *lo = window > 0 && it.pos >= window ? it.pos - window + 1 : 0;
 }
 
-// ---- the load warp -------------------------------------------------------------------
+// ---- the load warps -----------------------------------------------------------------
 
-template <int D>
+// Page and row of this lane's box of a key tile.  A box that no token sees, or
+// whose page id is bad, is loaded from past the last page: TMA fills zeros.
+struct Boxes {
+    const PagedAttentionArgs &a;
+    int32_t box_rows, box;  // this lane's box of a tile
+    int32_t row_lo, row_hi, hi;
+    const int32_t *table;
+    __device__ __forceinline__ void start(const Item &it) {
+        visible_rows(it, a.window, &row_lo, &row_hi);
+        hi = it.hi;
+        table = a.block_table + it.req * a.table_stride;
+    }
+    __device__ __forceinline__ bool seen(int32_t tile) const {
+        const int32_t key = tile * kKeys + box * box_rows;
+        return tile < hi && key < row_hi && key + box_rows > row_lo;
+    }
+    // The table's entry, asked for one tile ahead of its use.
+    __device__ __forceinline__ int32_t fetch(int32_t tile) const {
+        return seen(tile) ? table[(tile * kKeys + box * box_rows) / a.cache.page_size] : 0;
+    }
+    __device__ __forceinline__ void place(int32_t tile, int32_t id, int32_t *page, int32_t *row) const {
+        *page = static_cast<int32_t>(a.cache.num_pages);
+        *row = 0;
+        if (seen(tile)) {
+            if (id >= 0 && id < *page) {
+                *page = id;
+                *row = (tile * kKeys + box * box_rows) % a.cache.page_size;
+            } else {
+                report(a.dev_status, GDN_DEV_BAD_SLOT);
+            }
+        }
+    }
+};
+
+// Warp 0 loads Q and the K tiles, warp 3 the V tiles: issuing one box takes a
+// warp some tens of cycles, which pages of 16 rows (16 boxes per 32 KB) would
+// make the bound of a single load warp.
+template <int D, bool kIsK>
 __device__ void load_tiles(const AttentionLaunch &L, Control<D> *ctl, uint32_t q_smem, uint32_t ring, const Waiter &wait) {
     using Sh = Shape<D>;
     const PagedAttentionArgs &a = L.a;
     const int lane = threadIdx.x & 31;
     const int boxes = kKeys / L.box_rows;
-    const int box = lane % boxes, panel = lane / boxes;
-    const uint32_t dst = panel * kPanel + box * L.box_rows * 128;
-    uint32_t stage = 0, phase = 0, filled = 0, q_loads = 0;
-    // One stage: columns [half * kCols, + kCols) of a tile, one box per lane.
-    auto fill = [&](const CUtensorMap *map, int32_t page, int32_t row, int32_t head, int half) {
-        if (!wait.all(ctl->kv_empty + stage, phase ^ 1)) return false;
-        if (lane == 0) tc::mbar_expect_tx(ctl->kv_full + stage, Sh::kStage);
-        __syncwarp();
-        if (panel < Sh::kPanels)
-            tc::tma_load_4d(ring + stage * Sh::kStage + dst, map, half * Sh::kCols + panel * 64, row, head, page,
-                            ctl->kv_full + stage);
-        ++filled;
-        if (++stage == Sh::kStages) {
-            stage = 0;
-            phase ^= 1;
-        }
-        return true;
-    };
-    bool ok = true;
+    Boxes where = {a, L.box_rows, lane % boxes, 0, 0, 0, nullptr};
+    const CUtensorMap *map = kIsK ? &L.tm_k : &L.tm_v;
+    Ring pos;
+    uint32_t n_items = 0;
+    bool ok = true, wide_before = false;
+    int32_t filled = -1;  // of stage `lane`: this warp's last fill
     for (uint32_t n = 0; ok; ++n) {
         const uint32_t s = n % kItems;
-        if (!wait.all(ctl->item_full + s, n / kItems & 1)) break;
+        ok = wait.all(ctl->item_full + s, n / kItems & 1);
+        if (!ok) break;
         const Item it = ctl->items[s];
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(ctl->item_empty + s);
         if (it.stop) break;
-        if (it.lo >= it.hi) continue;
-        if (!wait.all(&ctl->q_empty, (q_loads & 1) ^ 1)) break;
-        // Few tokens: a box per token and panel, one per lane, instead of the full tile's.
-        constexpr int kQPanels = D / 64;
-        const bool few = it.n * kQPanels <= 32 && it.n < kRows / L.group;
-        const uint32_t token_bytes = L.group * 128u;
-        if (lane == 0)
-            tc::mbar_expect_tx(&ctl->q_full, kQPanels * token_bytes * static_cast<uint32_t>(few ? it.n : kRows / L.group));
-        __syncwarp();
-        if (few) {
-            if (lane < it.n * kQPanels)
-                tc::tma_load_3d(q_smem + lane % kQPanels * kPanel + lane / kQPanels * token_bytes, &L.tm_q_one,
-                                lane % kQPanels * 64, it.head * L.group, it.tok + lane / kQPanels, &ctl->q_full);
-        } else if (lane < kQPanels) {
-            tc::tma_load_3d(q_smem + lane * kPanel, &L.tm_q, lane * 64, it.head * L.group, it.tok, &ctl->q_full);
-        }
-        ++q_loads;
-        int32_t row_lo, row_hi;
-        visible_rows(it, a.window, &row_lo, &row_hi);
-        // Page and row of this lane's box of a tile.  A box that no token sees, or whose page id is bad, is loaded
-        // from past the last page: TMA fills it with zeros.
-        const int32_t none = static_cast<int32_t>(a.cache.num_pages);
-        auto lookup = [&](int32_t tile, int32_t *page, int32_t *row) {
-            const int32_t key = tile * kKeys + box * L.box_rows;
-            *page = none;
-            *row = 0;
-            if (tile < it.hi && key < row_hi && key + L.box_rows > row_lo) {
-                const int32_t idx = key / a.cache.page_size;
-                const int32_t id = a.block_table[it.req * a.table_stride + idx];
-                if (id >= 0 && id < none) {
-                    *page = id;
-                    *row = key - idx * a.cache.page_size;
-                } else {
-                    report(a.dev_status, GDN_DEV_BAD_SLOT);
-                }
+        const int32_t tiles = it.hi - it.lo;
+        where.start(it);
+        int32_t id = where.fetch(it.lo);
+        const int32_t tile_tokens = kRows / L.group;
+        const bool dual = Sh::kStreams == 2 && it.n > tile_tokens;
+        if (kIsK) {
+            // Few tokens: a box per token and panel, one per lane, instead of the full tile's.
+            constexpr int kQPanels = D / 64;
+            const bool few = it.n < tile_tokens && it.n * kQPanels <= 32;
+            const bool wide = Sh::kStreams == 2 ? dual : !(few && it.n * L.group <= Sh::kSmallRows);
+            const uint32_t slot = n_items & 1;
+            ok = wait.all(ctl->q_empty + slot, (n_items >> 1 & 1) ^ 1);
+            if (ok && (wide || wide_before) && n_items > 0)
+                ok = wait.all(ctl->q_empty + (slot ^ 1), (n_items - 1) >> 1 & 1);
+            if (!ok) break;
+            wide_before = wide;
+            const uint32_t token_bytes = L.group * 128u;
+            const uint32_t q_at = q_smem + (wide ? 0 : slot * Sh::kQSlot);
+            if (lane == 0)
+                tc::mbar_expect_tx(ctl->q_full + slot,
+                                   kQPanels * token_bytes * static_cast<uint32_t>(few ? it.n : (dual ? 2 : 1) * tile_tokens));
+            __syncwarp();
+            if (few) {
+                if (lane < it.n * kQPanels)
+                    tc::tma_load_3d(q_at + lane % kQPanels * kPanel + lane / kQPanels * token_bytes, &L.tm_q_one,
+                                    lane % kQPanels * 64, it.head * L.group, it.tok + lane / kQPanels, ctl->q_full + slot);
+            } else if (lane < kQPanels * (dual ? 2 : 1)) {
+                tc::tma_load_3d(q_at + lane * kPanel, &L.tm_q, lane % kQPanels * 64, it.head * L.group,
+                                it.tok + lane / kQPanels * tile_tokens, ctl->q_full + slot);
             }
-        };
-        int32_t k_page, k_row, v_page = none, v_row = 0;
-        lookup(it.lo, &k_page, &k_row);
-        for (int32_t t = it.lo; ok && t <= it.hi; ++t) {  // K of tile t, then V of tile t - 1
-            int32_t next_page, next_row;
-            lookup(t + 1, &next_page, &next_row);
-            if (t < it.hi)
-                for (int h = 0; ok && h < Sh::kHalves; ++h) ok = fill(&L.tm_k, k_page, k_row, it.head, h);
-            if (t > it.lo)
-                for (int h = 0; ok && h < Sh::kHalves; ++h) ok = fill(&L.tm_v, v_page, v_row, it.head, h);
-            v_page = k_page;
-            v_row = k_row;
-            k_page = next_page;
-            k_row = next_row;
+        }
+        ++n_items;
+        for (int32_t t = 0; ok && t < tiles; ++t) {
+            int32_t page, row;
+            where.place(it.lo + t, id, &page, &row);
+            id = where.fetch(it.lo + t + 1);
+            const uint32_t at = pos.first + Sh::kHalves * (kIsK ? pos.k_at(t, dual) : pos.v_at(t, dual));
+#pragma unroll 1
+            for (int h = 0; h < Sh::kHalves; ++h) {
+                const uint32_t st = (at + h) % Sh::kStages;
+                ok = wait.all(ctl->kv_empty + st, ((at + h) / Sh::kStages & 1) ^ 1);
+                if (!ok) break;
+                if (lane == 0) tc::mbar_expect_tx(ctl->kv_full + st, Sh::kStage);
+#pragma unroll 1
+                for (int b = 0; b < boxes; ++b) {
+                    const int32_t bp = __shfl_sync(0xffffffffu, page, b), br = __shfl_sync(0xffffffffu, row, b);
+                    if (lane == 0)
+#pragma unroll
+                        for (int p = 0; p < Sh::kPanels; ++p)
+                            tc::tma_load_4d(ring + st * Sh::kStage + p * kPanel + b * L.box_rows * 128, map,
+                                            h * Sh::kCols + p * 64, br, it.head, bp, ctl->kv_full + st);
+                }
+                if (lane == static_cast<int>(st)) filled = static_cast<int32_t>((at + h) / Sh::kStages & 1);
+            }
+        }
+        pos.next(tiles, dual, Sh::kHalves);
+    }
+    // After a failure: copies in flight land before the block may leave (else every copy has been consumed).
+    if (!ok) {
+        if (lane < Sh::kStages && filled >= 0) drain_bar(ctl->kv_full + lane, filled);
+        if (kIsK && lane < 2 && n_items > static_cast<uint32_t>(lane)) {
+            const uint32_t i = n_items - 1 - lane;
+            drain_bar(ctl->q_full + (i & 1), i >> 1 & 1);
         }
     }
-    // Copies still in flight land before the block may leave.
-    if (q_loads > 0) drain_bar(&ctl->q_full, (q_loads - 1) & 1);
-    for (uint32_t i = 0; i < Sh::kStages && i < filled; ++i) {
-        const uint32_t f = filled - 1 - i;
-        drain_bar(ctl->kv_full + f % Sh::kStages, f / Sh::kStages & 1);
-    }
+    __syncwarp();
 }
 
-// ---- the MMA warp (one thread) -----------------------------------------------------------
+// ---- the MMA warp -----------------------------------------------------------
+//
+// The whole warp runs the code and one elected lane issues: operands then stay
+// in uniform registers.  The tensor pipe holds about three products (64 cycles each) beyond the one
+// it runs, so the way from one batch's last product to the next one's first
+// has to be short: a stage pointer that only steps (stages are used in ring
+// order), barriers by shared address, descriptors by their low words, the
+// batch's V waited for before its weights.
 
 template <int D, bool kHalf>
-__device__ void issue_products(Control<D> *ctl, uint32_t q_smem, uint32_t ring, uint32_t tmem, const Waiter &wait) {
+struct Issuer {
     using Sh = Shape<D>;
-    constexpr uint32_t kType = kHalf ? 0u : tc::kIdescBf16;
-    constexpr uint32_t kIdescS = tc::idesc_f16_f32acc(kRows, kKeys) | kType;
-    constexpr uint32_t kIdescO = tc::idesc_f16_f32acc(kRows, Sh::kCols) | kType | tc::kIdescBmn;
-    uint32_t stage = 0, phase = 0, tile = 0, n_items = 0;
-    auto next_stage = [&]() {
-        tc::mma_commit(ctl->kv_empty + stage);
+    static constexpr uint32_t kType = kHalf ? 0u : tc::kIdescBf16;
+    static constexpr uint32_t kIdescS = tc::idesc_f16_f32acc(kRows, kKeys) | kType;
+    static constexpr uint32_t kIdescO = tc::idesc_f16_f32acc(kRows, Sh::kCols) | kType | tc::kIdescBmn;
+    const Waiter &wait;
+    uint32_t bars;  // address of the control block
+    uint32_t ring, tmem;
+    uint32_t stage, phase;  // next stage of the ring
+    uint32_t used;          // per O: parity of the items that used it
+    // The unit whose product with P is still to be issued.
+    uint32_t left, left_stage;  // its number; V's stage where `left_loaded`
+    bool any, left_fresh, left_loaded;
+
+#define GDN_BAR(name, i) (bars + static_cast<uint32_t>(offsetof(Control<D>, name)) + (i) * 8u)
+
+    __device__ __forceinline__ void step() {
         if (++stage == Sh::kStages) {
             stage = 0;
             phase ^= 1;
         }
-    };
-    // O (+)= P V of the tile whose number is g
-    auto weights = [&](uint32_t g, bool first) {
-        if (!wait(ctl->p_full + (g & 1), g >> 1 & 1)) return false;
-        if (first && !wait(&ctl->o_free, (n_items & 1) ^ 1)) return false;
-        for (int h = 0; h < Sh::kHalves; ++h) {
-            if (!wait(ctl->kv_full + stage, phase)) return false;
-            tc::fence_after_sync();
-#pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k)
-                tc::mma_f16_ta(tmem + kTmemO + h * Sh::kCols, tmem + (g & 1) * kKeys + k * 8,
-                               tc::desc_mn_sw128(ring + stage * Sh::kStage + k * 2048, kPanel), kIdescO,
-                               !first || k > 0);
-            next_stage();
-        }
-        tc::mma_commit(&ctl->o_done);
-        return true;
-    };
-    for (uint32_t n = 0;; ++n) {
-        const uint32_t s = n % kItems;
-        if (!wait(ctl->item_full + s, n / kItems & 1)) break;
-        const int32_t stop = ctl->items[s].stop, tiles = ctl->items[s].hi - ctl->items[s].lo;
-        tc::mbar_arrive(ctl->item_empty + s);
-        if (stop) break;
-        if (tiles <= 0) continue;
-        bool ok = wait(&ctl->q_full, n_items & 1);
-        for (int32_t i = 0; ok && i < tiles; ++i, ++tile) {
-            // S of tile i; its buffer's last reader, the product with P of tile i - 2, is ahead in the queue
-            for (int h = 0; ok && h < Sh::kHalves; ++h) {
-                ok = wait(ctl->kv_full + stage, phase);
-                if (!ok) break;
-                tc::fence_after_sync();
-#pragma unroll
-                for (int k = 0; k < Sh::kCols / 16; ++k)
-                    tc::mma_f16(tmem + (tile & 1) * kKeys,
-                                tc::desc_k_sw128(q_smem + (h * Sh::kPanels + k / 4) * kPanel) + (k % 4) * 2,
-                                tc::desc_k_sw128(ring + stage * Sh::kStage + k / 4 * kPanel) + (k % 4) * 2, kIdescS,
-                                h > 0 || k > 0);
-                next_stage();
-            }
-            if (!ok) break;
-            tc::mma_commit(ctl->s_full + (tile & 1));
-            if (i + 1 == tiles) tc::mma_commit(&ctl->q_empty);
-            if (i > 0) ok = weights(tile - 1, i == 1);
-        }
-        if (!ok || !weights(tile - 1, tiles == 1)) break;
-        ++n_items;
     }
-    tc::mma_commit(&ctl->drain);
-    drain_bar(&ctl->drain, 0);
-}
+    // S of unit g from Q at q (low descriptor word), the item's `last`: Q is free after it.  kTake: K is the ring's next tile (else stage *at); kFree: its last use.
+    template <bool kTake, bool kFree>
+    __device__ __forceinline__ bool scores(uint32_t g, uint32_t q, uint32_t *at, bool last, uint32_t q_bar) {
+        for (int h = 0; h < Sh::kHalves; ++h) {
+            if (kTake) {
+                if (!wait.all(GDN_BAR(kv_full, stage), phase)) return false;
+                *at = stage;
+            }
+            tc::fence_after_sync();
+            const uint32_t k = tc::desc_lo(ring + *at * Sh::kStage, 16);
+            if (tc::elect_lane()) {
+#pragma unroll
+                for (int i = 0; i < Sh::kCols / 16; ++i)
+                    tc::mma_f16_lo(tmem + (g & 1) * kKeys, q + (h * Sh::kPanels + i / 4) * (kPanel >> 4) + (i % 4) * 2,
+                                   k + i / 4 * (kPanel >> 4) + (i % 4) * 2, kIdescS, h > 0 || i > 0);
+                if (kFree) tc::mma_commit(GDN_BAR(kv_empty, *at));
+                if (h + 1 == Sh::kHalves) {
+                    tc::mma_commit(GDN_BAR(s_full, g & 1));
+                    if (last) tc::mma_commit(q_bar);
+                }
+            }
+            if (kTake) step();
+        }
+        return true;
+    }
+    // O (+)= P V of unit g.  kTake, kFree as above for V.
+    template <bool kTake, bool kFree>
+    __device__ __forceinline__ bool weights(uint32_t g, bool fresh, uint32_t *at) {
+        const uint32_t b = g & 1, w = Sh::kStreams == 2 ? b : 0;
+        if (kTake && !wait.all(GDN_BAR(kv_full, stage), phase)) return false;
+        if (fresh) {
+            if (!wait.all(GDN_BAR(o_free, w), (used >> w & 1) ^ 1)) return false;
+            used ^= 1u << w;
+        }
+        if (!wait.all(GDN_BAR(p_full, b), g >> 1 & 1)) return false;
+        for (int h = 0; h < Sh::kHalves; ++h) {
+            if (kTake) {
+                if (h > 0 && !wait.all(GDN_BAR(kv_full, stage), phase)) return false;
+                *at = stage;
+            }
+            tc::fence_after_sync();
+            const uint32_t v = tc::desc_lo(ring + *at * Sh::kStage, kPanel);
+            if (tc::elect_lane()) {
+#pragma unroll
+                for (int i = 0; i < kKeys / 16; ++i)
+                    tc::mma_f16_ta_lo(tmem + kTmemO + w * D + h * Sh::kCols, tmem + b * kKeys + i * 8, v + i * (2048 >> 4), kIdescO,
+                                      !fresh || i > 0);
+                if (kFree) tc::mma_commit(GDN_BAR(kv_empty, *at));
+                if (h + 1 == Sh::kHalves) tc::mma_commit(GDN_BAR(o_done, w));
+            }
+            if (kTake) step();
+        }
+        return true;
+    }
+    __device__ __forceinline__ bool weights_left() {
+        any = false;
+        return left_loaded ? weights<false, true>(left, left_fresh, &left_stage) : weights<true, true>(left, left_fresh, &left_stage);
+    }
+    // An item of one row tile: unit g + t is key tile t.  Ring order K, V of the tile before, K, V, ...
+    __device__ __forceinline__ bool single(uint32_t g, int32_t tiles, uint32_t q, uint32_t q_bar) {
+        for (int32_t t = 0; t < tiles; ++t, ++g) {
+            uint32_t at;
+            if (!scores<true, true>(g, q, &at, t + 1 == tiles, q_bar)) return false;
+            if (any && !weights_left()) return false;
+            any = true;
+            left = g;
+            left_fresh = t < Sh::kStreams;
+            left_loaded = false;
+        }
+        return true;
+    }
+    // An item of two row tiles: units g + 2t and g + 2t + 1 are key tile t.  Ring order K, V, K, V, ...
+    __device__ __forceinline__ bool dual(uint32_t g, int32_t tiles, uint32_t q, uint32_t q_bar) {
+        for (int32_t t = 0; t < tiles; ++t, g += 2) {
+            uint32_t at;
+            if (!scores<true, false>(g, q, &at, false, q_bar)) return false;
+            if (any && !weights_left()) return false;
+            if (!scores<false, true>(g + 1, q + (Sh::kQTile >> 4), &at, t + 1 == tiles, q_bar)) return false;
+            if (!weights<true, false>(g, t == 0, &left_stage)) return false;
+            any = true;
+            left = g + 1;
+            left_fresh = t == 0;
+            left_loaded = true;
+        }
+        return true;
+    }
+    __device__ __forceinline__ void run(Control<D> *ctl, const AttentionLaunch &L, uint32_t q_smem) {
+        const int32_t tile_tokens = kRows / L.group;
+        uint32_t unit = 0, n_items = 0;
+        for (uint32_t n = 0;; ++n) {
+            const uint32_t s = n % kItems;
+            if (!wait.all(GDN_BAR(item_full, s), n / kItems & 1)) break;
+            // (through a warp reduction: what the compiler knows to be uniform it keeps in uniform registers)
+            const int32_t stop = __reduce_max_sync(0xffffffffu, ctl->items[s].stop);
+            const int32_t tokens = __reduce_max_sync(0xffffffffu, ctl->items[s].n);
+            const int32_t tiles = __reduce_max_sync(0xffffffffu, ctl->items[s].hi - ctl->items[s].lo);
+            if (tc::elect_lane()) tc::mbar_arrive(ctl->item_empty + s);
+            if (stop) {
+                if (any && !left_loaded)  // V of the last tile lies behind the place of a next item's first K
+                    for (int h = 0; h < Sh::kHalves; ++h) step();
+                if (any) weights_left();
+                break;
+            }
+            const bool two = Sh::kStreams == 2 && tokens > tile_tokens;
+            const bool few = tokens < tile_tokens && tokens * (D / 64) <= 32;
+            const bool wide = Sh::kStreams == 2 ? two : !(few && tokens * L.group <= Sh::kSmallRows);
+            const uint32_t slot = n_items & 1;
+            if (!wait.all(GDN_BAR(q_full, slot), n_items >> 1 & 1)) break;
+            const uint32_t q = tc::desc_lo(q_smem + (wide ? 0 : slot * Sh::kQSlot), 16);
+            if (!(two ? dual(unit, tiles, q, GDN_BAR(q_empty, slot)) : single(unit, tiles, q, GDN_BAR(q_empty, slot)))) break;
+            unit += two ? 2 * tiles : tiles;
+            ++n_items;
+        }
+        if (tc::elect_lane()) tc::mma_commit(GDN_BAR(drain, 0));
+        __syncwarp();
+        drain_bar(&ctl->drain, 0);
+    }
+#undef GDN_BAR
+};
 
 // ---- the softmax warps ----------------------------------------------------------------------
+
+// Instruction fetch bounds this code before arithmetic does: a pass over 128
+// scores unrolled with compares, selects and scalar arithmetic is ~1200
+// instructions, and ncu showed the softmax warps stalled on `no_instruction`
+// most of the time (issue slots 19 % used, tensor pipe 44 %).  So masks are
+// applied in a rolled pass of their own through TMEM, only on tiles that need
+// one, and the rest uses three-input maxima and packed pairs.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ void unpair(uint64_t d, float *lo, float *hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(d));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// Scores outside columns [lo, hi) of this thread's row become minus infinity.
+__device__ __forceinline__ void mask_scores(uint32_t t_s, int32_t lo, int32_t hi) {
+#pragma unroll 1
+    for (int q = 0; q < kKeys; q += 32) {
+        uint32_t x[32];
+        tc::tmem_ld32(t_s + q, x);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (q + i < lo || q + i >= hi) x[i] = 0xff800000u;
+        tc::tmem_st32(t_s + q, x);
+    }
+}
+
+// Moves the running maximum m where the scores x make it; the factor for l and
+// O (1 where it stayed) comes back in *f.  True if any row of the warp moved.
+__device__ __forceinline__ bool move_max(const uint32_t (&x)[kKeys], bool valid, float c, float &m, float *f) {
+    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int j = 0; j < kKeys; j += 2)
+        top[j / 2 & 3] = max3(top[j / 2 & 3], __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+    float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+    mx = valid ? fmaxf(m, mx) : -INFINITY;
+    const bool move = (m == -INFINITY && mx > -INFINITY) || (mx - m) * c > 8.f;
+    *f = move ? ex2((m - mx) * c) : 1.f;  // 0 from the empty maximum
+    if (move) m = mx;
+    return __any_sync(0xffffffffu, move);
+}
+
+// P = exp2(c S - mc) over S in TMEM; the sum of the row's weights.
+template <bool kHalf>
+__device__ __forceinline__ float store_weights(uint32_t t_s, const uint32_t (&x)[kKeys], float c, float mc) {
+    const uint64_t c2 = pair(c, c), mc2 = pair(-mc, -mc);
+    uint64_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        uint32_t pw[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const int j = q * 64 + 2 * i;
+            float p0, p1;
+            unpair(fma2(pair(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), c2, mc2), &p0, &p1);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
+            sum[i & 3] = add2(sum[i & 3], pair(p0, p1));
+            pw[i] = pack2<kHalf>(p0, p1);
+        }
+        tc::tmem_st32(t_s + q * 32, pw);
+    }
+    float lo, hi;
+    unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), &lo, &hi);
+    return lo + hi;
+}
+
+// O of `cols` columns times f, in TMEM.
+template <int kCount>
+__device__ __forceinline__ void scale_o(uint32_t t_o, float f) {
+#pragma unroll 1
+    for (int q = 0; q < kCount / 16; ++q) {
+        uint32_t o[16];
+        tc::tmem_ld16(t_o + q * 16, o);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+        tc::tmem_st16(t_o + q * 16, o);
+    }
+}
 
 template <int D, bool kHalf>
 __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t *ring, uint32_t tmem, const Waiter &wait) {
     using Sh = Shape<D>;
     const PagedAttentionArgs &a = L.a;
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
+    const uint32_t w = Sh::kStreams == 2 ? (threadIdx.x >> 7) - 1 : 0;  // warpgroup = buffer = O, with two streams
     const int row = warp * 32 + lane;
-    const int32_t u = row / L.group, g = row - u * L.group;
+    const int32_t u_tile = row / L.group, g = row - u_tile * L.group;
+    const int32_t tile_tokens = kRows / L.group;
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;  // this warp's TMEM lanes
     const uint32_t t_o = tmem + kTmemO + lanes;
     const float c = L.c;
-    uint32_t tile = 0, stages = 0;  // tiles and stages of the items before
+    Ring pos;
+    uint32_t unit0 = 0;              // first unit of the item
+    uint32_t ml_sent = 0, ml_got = 0;
     for (uint32_t n = 0;; ++n) {
-        const uint32_t s = n % kItems;
-        if (!wait.all(ctl->item_full + s, n / kItems & 1)) return;
-        const Item it = ctl->items[s];
+        const uint32_t sl = n % kItems;
+        if (!wait.all(ctl->item_full + sl, n / kItems & 1)) return;
+        const Item it = ctl->items[sl];
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(ctl->item_empty + s);
+        if (lane == 0) tc::mbar_arrive(ctl->item_empty + sl);
         if (it.stop) return;
-        const bool valid = u < it.n;
-        const bool any_row = warp * 32 < it.n * L.group;
         const int32_t tiles = it.hi - it.lo;
+        const bool dual = Sh::kStreams == 2 && it.n > tile_tokens;
+        // Which part of the item is this warpgroup's: row tile of a dual one, even or odd key tiles of another.
+        const int32_t part = Sh::kStreams == 2 ? static_cast<int32_t>((w ^ unit0) & 1) : 0;
+        const int32_t u = u_tile + (dual ? part * tile_tokens : 0);
+        const int32_t rows = (dual ? (part ? it.n - tile_tokens : tile_tokens) : it.n) * L.group;
+        const bool valid = row < rows && u_tile < tile_tokens;
+        const bool any_row = warp * 32 < rows;
         const int32_t key_hi = it.pos + u + 1;
         const int32_t key_lo = a.window > 0 && key_hi > a.window ? key_hi - a.window : 0;
         int32_t row_lo, row_hi;
         visible_rows(it, a.window, &row_lo, &row_hi);
+        const int32_t units = dual ? 2 * tiles : tiles;
         float m = -INFINITY, l = 0.f;
-        for (int32_t i = 0; i < tiles; ++i, ++tile) {
-            const int32_t k0 = (it.lo + i) * kKeys;
-            if (!wait.all(ctl->s_full + (tile & 1), tile >> 1 & 1)) return;
+        for (int32_t j = part; j < units; j += Sh::kStreams) {
+            const uint32_t unit = unit0 + j, b = unit & 1;
+            const int32_t t = dual ? j >> 1 : j;
+            const int32_t k0 = (it.lo + t) * kKeys;
+            if (!wait.all(ctl->s_full + b, unit >> 1 & 1)) return;
             tc::fence_after_sync();
             if (any_row) {
-                const uint32_t t_s = tmem + (tile & 1) * kKeys + lanes;
-                uint32_t sb[kKeys];
-                tc::tmem_ld128(t_s, sb);
-                float x[kKeys];
-#pragma unroll
-                for (int j = 0; j < kKeys; ++j) x[j] = __uint_as_float(sb[j]);
-                if (__any_sync(0xffffffffu, valid && (k0 + kKeys > key_hi || k0 < key_lo))) {
-                    const int32_t hi = key_hi - k0, lo = key_lo - k0;
-#pragma unroll
-                    for (int j = 0; j < kKeys; ++j) x[j] = (j < hi && j >= lo) ? x[j] : -INFINITY;
-                }
-                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int j = 0; j < kKeys; ++j) top[j & 3] = fmaxf(top[j & 3], x[j]);
-                float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                mx = valid ? fmaxf(m, mx) : -INFINITY;
-                const bool move = (m == -INFINITY && mx > -INFINITY) || (mx - m) * c > 8.f;
-                if (__any_sync(0xffffffffu, move)) {
-                    const float f = move ? ex2((m - mx) * c) : 1.f;  // 0 from the empty maximum
-                    if (move) m = mx;
+                const uint32_t t_s = tmem + b * kKeys + lanes;
+                if (__any_sync(0xffffffffu, valid && (k0 + kKeys > key_hi || k0 < key_lo)))
+                    mask_scores(t_s, key_lo - k0, key_hi - k0);
+                uint32_t x[kKeys];
+                tc::tmem_ld128(t_s, x);
+                float f;
+                if (move_max(x, valid, c, m, &f)) {
                     l *= f;
-                    if (i > 0) {
-                        if (!wait.all(&ctl->o_done, (tile - 1) & 1)) return;
-                        tc::fence_after_sync();
-#pragma unroll 1
-                        for (int q = 0; q < D / 16; ++q) {
-                            uint32_t o[16];
-                            tc::tmem_ld16(t_o + q * 16, o);
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                            tc::tmem_st16(t_o + q * 16, o);
+                    if (j >= Sh::kStreams) {
+                        // With two streams S of this unit told that O is done: both are this warpgroup's buffers.
+                        if (Sh::kStreams == 1) {
+                            if (!wait.all(ctl->o_done, (unit - 1) & 1)) return;
+                            tc::fence_after_sync();
                         }
+                        scale_o<D>(t_o + w * D, f);
                     }
                 }
-                const float mc = m == -INFINITY ? 0.f : m * c;
-                float sum[4] = {};
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t pw[32];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const float p0 = ex2(fmaf(x[q * 64 + 2 * j], c, -mc)), p1 = ex2(fmaf(x[q * 64 + 2 * j + 1], c, -mc));
-                        sum[j & 1] += p0;
-                        sum[2 + (j & 1)] += p1;
-                        pw[j] = pack2<kHalf>(p0, p1);
-                    }
-                    tc::tmem_st32(t_s + q * 32, pw);
-                }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                l += store_weights<kHalf>(t_s, x, c, m == -INFINITY ? 0.f : m * c);
             }
             // Value rows that no token sees may hold anything (0 x NaN): zero them before the product.
             if (k0 + kKeys > row_hi || k0 < row_lo) {
-                const uint32_t before = stages + Sh::kHalves * static_cast<uint32_t>((i + 2 < tiles ? i + 2 : tiles) + i);
+                const uint32_t at = pos.first + Sh::kHalves * pos.v_at(t, dual);
                 const bool dead = k0 + row >= row_hi || k0 + row < row_lo;
-                for (uint32_t v = before; v < before + Sh::kHalves; ++v) {
-                    const uint32_t st = v % Sh::kStages;
-                    if (!wait.all(ctl->kv_full + st, v / Sh::kStages & 1)) return;
+#pragma unroll 1
+                for (uint32_t v = at; v < at + Sh::kHalves; ++v) {
+                    // Two waits: a parity tells this fill from the one before only once that one has been consumed.
+                    const uint32_t st = v % Sh::kStages, parity = v / Sh::kStages & 1;
+                    if (!wait.all(ctl->kv_empty + st, parity ^ 1) || !wait.all(ctl->kv_full + st, parity)) return;
                     if (dead) {
 #pragma unroll
                         for (int p = 0; p < Sh::kPanels * 8; ++p)
@@ -623,66 +907,104 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
             }
             tc::fence_before_sync();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(ctl->p_full + (tile & 1));
+            if (lane == 0) tc::mbar_arrive(ctl->p_full + b);
         }
-        stages += 2 * Sh::kHalves * static_cast<uint32_t>(tiles > 0 ? tiles : 0);
         // O to memory: the result, or this split's part of it.
-        // (the last two products in turn: S of the last tile only told that the third-last is done, and a parity
-        // tells two phases apart)
-        if (tiles > 0) {
-            if (tiles > 1 && !wait.all(&ctl->o_done, tile & 1)) return;
-            if (!wait.all(&ctl->o_done, (tile - 1) & 1)) return;
+        const bool pair = Sh::kStreams == 2 && !dual && tiles > 1;  // two warpgroups hold one row tile's parts
+        if (dual || part < tiles) {
+            if (Sh::kStreams == 2) {
+                const uint32_t last = unit0 + units - 1 - ((units - 1 - part) & 1);
+                if (!wait.all(ctl->o_done + w, last >> 1 & 1)) return;
+            } else {
+                // The last two products in turn: S of the last unit only told that the third-last is done, and a
+                // parity tells two phases apart.
+                if (tiles > 1 && !wait.all(ctl->o_done, (unit0 + units) & 1)) return;
+                if (!wait.all(ctl->o_done, (unit0 + units - 1) & 1)) return;
+            }
             tc::fence_after_sync();
         }
-        if (any_row) {
+        float f0 = 1.f, f1 = 0.f;  // factors of this warpgroup's O and the other's
+        bool writer = dual || part == 0;
+        if (pair && part == 1) {
+            ctl->ml[Sh::kStreams == 2 ? row : 0] = make_float2(m, l);
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(ctl->ml_full + w);
+            ++ml_sent;
+        } else if (pair) {
+            if (!wait.all(ctl->ml_full + (w ^ 1), ml_got++ & 1)) return;
+            tc::fence_after_sync();
+            const float2 other = ctl->ml[Sh::kStreams == 2 ? row : 0];
+            const float top = fmaxf(m, other.x);
+            if (top > -INFINITY) {
+                f0 = ex2((m - top) * c);
+                f1 = ex2((other.x - top) * c);
+                m = top;
+                l = l * f0 + other.y * f1;
+            }
+        }
+        if (writer && any_row) {
             const int64_t head = static_cast<int64_t>(it.head) * L.group + g;
-            const bool part = it.partial >= 0;
+            const bool split = it.partial >= 0;
             const int64_t prow = (it.partial + static_cast<int64_t>(u) * it.splits) * a.h_q + head;
-            const float f = part ? 1.f : l == 0.f ? 0.f : 1.f / l;
+            const bool none = l == 0.f;  // no key seen, or all weights zero
+            if (!split) {
+                const float inv = none ? 0.f : 1.f / l;
+                f0 *= inv;
+                f1 *= inv;
+            } else if (valid) {
+                L.ws.ml[prow] = make_float2(m * c, l);
+            }
             uint16_t *out = a.o + ((static_cast<int64_t>(it.tok) + u) * a.h_q + head) * D;
             float *pout = L.ws.o + prow * D;
-            if (part && valid) L.ws.ml[prow] = make_float2(m * c, l);
 #pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
+                float y[32];
                 uint32_t o[32];
-                if (tiles > 0)
-                    tc::tmem_ld32(t_o + q * 32, o);
+                tc::tmem_ld32(t_o + w * D + q * 32, o);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) y[j] = none ? 0.f : __uint_as_float(o[j]) * f0;
+                if (pair) {
+                    tc::tmem_ld32(t_o + (w ^ 1) * D + q * 32, o);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) y[j] = none ? 0.f : fmaf(__uint_as_float(o[j]), f1, y[j]);
+                }
                 if (valid) {
-                    if (part) {
+                    if (split) {
 #pragma unroll
                         for (int j = 0; j < 32; j += 4)
-                            *reinterpret_cast<uint4 *>(pout + q * 32 + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                            *reinterpret_cast<float4 *>(pout + q * 32 + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
                     } else {
-                        uint32_t w[16];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const float y0 = l == 0.f ? 0.f : __uint_as_float(o[2 * j]) * f;
-                            const float y1 = l == 0.f ? 0.f : __uint_as_float(o[2 * j + 1]) * f;
-                            w[j] = pack2<kHalf>(y0, y1);
-                        }
-#pragma unroll
-                        for (int j = 0; j < 16; j += 4)
-                            *reinterpret_cast<uint4 *>(out + q * 32 + j * 2) = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+                        for (int j = 0; j < 32; j += 8)
+                            *reinterpret_cast<uint4 *>(out + q * 32 + j) =
+                                make_uint4(pack2<kHalf>(y[j], y[j + 1]), pack2<kHalf>(y[j + 2], y[j + 3]),
+                                           pack2<kHalf>(y[j + 4], y[j + 5]), pack2<kHalf>(y[j + 6], y[j + 7]));
                     }
                 }
             }
         }
-        if (tiles > 0) {
+        if (writer) {
             tc::fence_before_sync();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&ctl->o_free);
+            if (lane == 0) {
+                tc::mbar_arrive(ctl->o_free + w);
+                if (pair) tc::mbar_arrive(ctl->o_free + (w ^ 1));
+            }
         }
+        pos.next(tiles, dual, Sh::kHalves);
+        unit0 += units;
     }
 }
 
 template <int D, bool kHalf>
-__global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ AttentionLaunch L) {
+__global__ void __launch_bounds__(Shape<D>::kThreads, 1) attention_kernel(const __grid_constant__ AttentionLaunch L) {
     using Sh = Shape<D>;
     extern __shared__ uint8_t raw[];
     uint8_t *base = raw + ((1024u - (tc::smem_u32(raw) & 1023u)) & 1023u);
     uint8_t *ring = base + Sh::kQ;
     Control<D> *ctl = reinterpret_cast<Control<D> *>(ring + Sh::kStages * Sh::kStage);
-    static_assert(sizeof(Control<D>) <= 1536, "control block");
+    static_assert(sizeof(Control<D>) <= Sh::kControl && Sh::kSmem <= 227 * 1024, "shared memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
@@ -690,17 +1012,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             tc::mbar_init(ctl->kv_full + i, 1);
             tc::mbar_init(ctl->kv_empty + i, 1);
         }
-        tc::mbar_init(&ctl->q_full, 1);
-        tc::mbar_init(&ctl->q_empty, 1);
         for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(ctl->q_full + i, 1);
+            tc::mbar_init(ctl->q_empty + i, 1);
             tc::mbar_init(ctl->s_full + i, 1);
             tc::mbar_init(ctl->p_full + i, 4);
+            tc::mbar_init(ctl->o_done + i, 1);
+            tc::mbar_init(ctl->o_free + i, 4);
+            tc::mbar_init(ctl->ml_full + i, 4);
         }
-        tc::mbar_init(&ctl->o_done, 1);
-        tc::mbar_init(&ctl->o_free, 4);
         for (int i = 0; i < kItems; ++i) {
             tc::mbar_init(ctl->item_full + i, 1);
-            tc::mbar_init(ctl->item_empty + i, 6);  // load, mma, four softmax warps
+            tc::mbar_init(ctl->item_empty + i, 3 + 4 * Sh::kStreams);  // two load warps, MMA, softmax warps
         }
         tc::mbar_init(&ctl->drain, 1);
         ctl->fail = 0;
@@ -712,27 +1035,35 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = ctl->tmem;
-    const Waiter wait = {&ctl->fail, L.a.dev_status};
-    if (warp == 0) {
-        load_tiles<D>(L, ctl, tc::smem_u32(base), tc::smem_u32(ring), wait);
-    } else if (warp == 1) {
-        if (lane == 0) issue_products<D, kHalf>(ctl, tc::smem_u32(base), tc::smem_u32(ring), tmem, wait);
-    } else if (warp == 2) {
-        schedule<D>(L, ctl, wait);
-    } else if (warp == 3) {
-        // Tokens of no request: zeros.
-        const PagedAttentionArgs &a = L.a;
-        const int32_t end = a.num_reqs > 0 ? a.cu_seqlens[a.num_reqs] : 0;
-        const int64_t chunk = static_cast<int64_t>(a.h_q) * D / 8;
-        for (int64_t i = (end > 0 ? end : 0) * chunk + blockIdx.x * 32 + lane; i < a.num_tokens * chunk; i += gridDim.x * 32)
-            reinterpret_cast<uint4 *>(a.o)[i] = make_uint4(0, 0, 0, 0);
+    const Waiter wait = {&ctl->fail};
+    // 384 threads are launched with 168 registers each: 128 x 72 + 256 x 216 is the same sum.
+    if (warp < 4) {
+        if (Sh::kStreams == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == 0) {
+            load_tiles<D, true>(L, ctl, tc::smem_u32(base), tc::smem_u32(ring), wait);
+        } else if (warp == 1) {
+            Issuer<D, kHalf> issuer = {wait, tc::smem_u32(ctl), tc::smem_u32(ring), __reduce_max_sync(0xffffffffu, tmem)};
+            issuer.run(ctl, L, tc::smem_u32(base));
+        } else if (warp == 2) {
+            schedule<D>(L, ctl, wait);
+            // Tokens of no request: zeros.
+            const PagedAttentionArgs &a = L.a;
+            const int32_t end = a.num_reqs > 0 ? a.cu_seqlens[a.num_reqs] : 0;
+            const int64_t chunk = static_cast<int64_t>(a.h_q) * D / 8;
+            for (int64_t i = (end > 0 ? end : 0) * chunk + blockIdx.x * 32 + lane; i < a.num_tokens * chunk; i += gridDim.x * 32)
+                reinterpret_cast<uint4 *>(a.o)[i] = make_uint4(0, 0, 0, 0);
+        } else {
+            load_tiles<D, false>(L, ctl, tc::smem_u32(base), tc::smem_u32(ring), wait);
+        }
     } else {
+        if (Sh::kStreams == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         softmax_rows<D, kHalf>(L, ctl, ring, tmem, wait);
     }
     __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
+    if (threadIdx.x == 0 && ctl->fail) report(L.a.dev_status, GDN_DEV_TIMEOUT);
     if (warp == 3) {
         tc::tmem_relinquish();
         tc::tmem_dealloc(tmem, kTmemCols);
@@ -765,14 +1096,14 @@ template <int D, bool kHalf>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ AttentionLaunch L) {
     const PagedAttentionArgs &a = L.a;
     const int lane = threadIdx.x & 31;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
+    const uint32_t row = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);  // under 2^31 + kJoinWarps
     const bool any = row < a.num_tokens * a.h_q;
-    const int32_t t = any ? static_cast<int32_t>(row / a.h_q) : 0;
+    const int32_t t = any ? static_cast<int32_t>(row / static_cast<uint32_t>(a.h_q)) : 0;
     const int32_t r = find_request(a.cu_seqlens, a.num_reqs, t, lane);
     const Request q = load_request(a, r, false);
-    const Plan p = plan_request(q.kv, q.m, L.group, a.cache.h_kv, a.window);
-    const int32_t u = t - q.first, u0 = u / p.tile_tokens * p.tile_tokens;
-    const int32_t n = q.m - u0 < p.tile_tokens ? q.m - u0 : p.tile_tokens;
+    const Plan p = plan_request(q.kv, q.m, L.group, streams_of(D), a.cache.h_kv, a.window);
+    const int32_t u = t - q.first, u0 = u / p.item_tokens * p.item_tokens;
+    const int32_t n = q.m - u0 < p.item_tokens ? q.m - u0 : p.item_tokens;
     int32_t lo, hi;
     key_tiles(q.kv, q.m, u0, n, a.window, &lo, &hi);
     const int32_t s0 = lo / p.split_tiles, s1 = hi > lo ? (hi - 1) / p.split_tiles + 1 : s0;
@@ -782,8 +1113,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     // One split wrote the row itself.
     if (!any || t < q.first || t >= q.first + q.m || s1 - s0 < 2) return;
     const int64_t base = L.ws.base[r];
-    if (base < 0 || base + p.partials > L.partials) return;  // not written: the call timed out or its ranges overlap
-    const int64_t first = (base + static_cast<int64_t>(u) * p.splits + (s0 - p.split0)) * a.h_q + row % a.h_q;
+    if (base < 0 || base + p.partials > L.ws.partials) return;  // not written: the call timed out or its ranges overlap
+    const int64_t first = (base + static_cast<int64_t>(u) * p.splits + (s0 - p.split0)) * a.h_q +
+                          (row - static_cast<uint32_t>(t) * a.h_q);
     float top = -INFINITY;
     for (int32_t s = lane; s < s1 - s0; s += 32) top = fmaxf(top, L.ws.ml[first + static_cast<int64_t>(s) * a.h_q].x);
 #pragma unroll
@@ -807,7 +1139,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     const float f = 1.f / l;
 #pragma unroll
     for (int v = 0; v < kVec; ++v)
-        *reinterpret_cast<uint32_t *>(a.o + row * D + v * 64 + lane * 2) =
+        *reinterpret_cast<uint32_t *>(a.o + static_cast<int64_t>(row) * D + v * 64 + lane * 2) =
             pack2<kHalf>(l == 0.f ? 0.f : acc[v][0] * f, l == 0.f ? 0.f : acc[v][1] * f);
 }
 
@@ -823,8 +1155,12 @@ cudaError_t launch_d(const AttentionLaunch &L, int64_t items, cudaStream_t strea
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < kMaxDevices) __atomic_store_n(&set[dev], 1, __ATOMIC_RELEASE);
     }
+    if (L.ws.counter) {
+        e = cudaMemsetAsync(L.ws.counter, 0, sizeof(*L.ws.counter), stream);
+        if (e != cudaSuccess) return e;
+    }
     const unsigned blocks = static_cast<unsigned>(items < sms ? (items > 0 ? items : 1) : sms);
-    attention_kernel<D, kHalf><<<blocks, kThreads, Shape<D>::kSmem, stream>>>(L);
+    attention_kernel<D, kHalf><<<blocks, Shape<D>::kThreads, Shape<D>::kSmem, stream>>>(L);
     e = cudaGetLastError();
     if (e != cudaSuccess || !L.ws.o) return e;
     cudaLaunchConfig_t cfg = {};
@@ -844,8 +1180,7 @@ cudaError_t launch_d(const AttentionLaunch &L, int64_t items, cudaStream_t strea
 
 size_t paged_attention_workspace(int32_t h_q, int32_t h_kv, int32_t d, int32_t num_reqs, int64_t num_tokens,
                                  int64_t max_kv_len) {
-    const int64_t partials = partials_bound(h_q / h_kv, h_kv, num_reqs, num_tokens, max_kv_len);
-    return partials > 0 ? workspace_at(nullptr, num_reqs, partials, h_q, d).bytes : 0;
+    return workspace_at(nullptr, h_q, h_kv, d, num_reqs, num_tokens, max_kv_len).bytes;
 }
 
 cudaError_t launch_paged_attention(const PagedAttentionArgs &a, cudaStream_t stream) {
@@ -857,8 +1192,7 @@ cudaError_t launch_paged_attention(const PagedAttentionArgs &a, cudaStream_t str
     while (c.page_size % L.box_rows != 0) L.box_rows /= 2;
     // A scale of zero weighs all keys alike; the least one keeps masked scores at minus infinity (0 x inf is NaN).
     L.c = fmaxf(a.scale * 1.4426950408889634f, 1e-30f);
-    const int64_t partials = L.partials = partials_bound(L.group, c.h_kv, a.num_reqs, a.num_tokens, a.max_kv_len);
-    if (partials > 0) L.ws = workspace_at(a.workspace, a.num_reqs, partials, a.h_q, c.d);
+    L.ws = workspace_at(a.workspace, a.h_q, c.h_kv, c.d, a.num_reqs, a.num_tokens, a.max_kv_len);
     const cuuint64_t d = static_cast<cuuint64_t>(c.d);
     const cuuint64_t q_dims[3] = {d, static_cast<cuuint64_t>(a.h_q), static_cast<cuuint64_t>(a.num_tokens)};
     const cuuint64_t q_strides[2] = {d * 2, static_cast<cuuint64_t>(a.q_token_stride) * 2};
@@ -875,9 +1209,7 @@ cudaError_t launch_paged_attention(const PagedAttentionArgs &a, cudaStream_t str
         !encode_tiles(&L.tm_k, c.k, c.dtype, 4, dims, k_strides, box) ||
         !encode_tiles(&L.tm_v, c.v, c.dtype, 4, dims, v_strides, box))
         return cudaErrorNotSupported;
-    // Bound of the item count: row tiles times heads times splits.
-    const int64_t tiles = a.num_tokens / tile_tokens + a.num_reqs;
-    const int64_t items = (tiles < a.num_tokens ? tiles : a.num_tokens) * c.h_kv * (partials > 0 ? kMaxSplits + 1 : 1);
+    const int64_t items = items_bound(L.group, streams_of(c.d), c.h_kv, a.num_reqs, a.num_tokens, L.ws.partials > 0);
     const bool half = c.dtype == GDN_FP16;
     switch (c.d) {
         case 64: return half ? launch_d<64, true>(L, items, stream) : launch_d<64, false>(L, items, stream);
