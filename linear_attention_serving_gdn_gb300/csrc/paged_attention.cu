@@ -71,7 +71,8 @@ bool encode_tiles(CUtensorMap *m, const void *base, int dtype, int rank, const c
 constexpr int kRows = 128;     // query rows of a tile (TMEM lanes)
 constexpr int kKeys = 128;     // keys of a tile
 constexpr int kPanel = 16384;  // 128 rows of 64 16-bit elements
-constexpr int kItems = 2;      // items between the scheduler and the other warps
+constexpr int kItems = 4;      // items between the scheduler and the other warps
+constexpr int kLongItem = 16;  // key tiles: behind such an item no further one is taken until it has begun
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 256;  // O after the two S buffers
 
@@ -80,6 +81,15 @@ constexpr uint32_t kTmemO = 256;  // O after the two S buffers
 constexpr int kSplitUnits = 152;
 constexpr int kMaxSplits = 64;
 constexpr int kMinSplitTiles = 2;
+// The least key tiles of a split of `tiles` by an item of `rows` query rows.  A
+// part's cost beside its keys is its partial result, in proportion to its rows:
+// a full tile's is that of two key tiles.  And each part costs the joining
+// kernel as the others do, so their number grows with the root of the keys.
+__host__ __device__ __forceinline__ int32_t least_split_tiles(int32_t tiles, int32_t rows) {
+    int32_t n = rows / 8 > kMinSplitTiles ? rows / 8 : kMinSplitTiles;
+    while (n * n * 2 < tiles) ++n;
+    return n;
+}
 
 // Row tiles that a block works on at once: two where two accumulators fit TMEM.
 __host__ __device__ constexpr int streams_of(int d) { return d <= 128 ? 2 : 1; }
@@ -90,7 +100,7 @@ struct Plan {
     int32_t split_tiles;  // key tiles of a split
     int32_t split0, splits;
     int64_t items;
-    int64_t partials;  // (token, split) pairs that leave partial results
+    int64_t partials;  // (token, split) pairs that may leave partial results
 };
 
 __host__ __device__ __forceinline__ int32_t ceil_div(int32_t a, int32_t b) { return (a + b - 1) / b; }
@@ -105,9 +115,10 @@ __device__ __forceinline__ void key_tiles(int32_t kv, int32_t m, int32_t u, int3
 }
 
 // How a request of m new tokens and kv keys is cut; depends on nothing else of the batch.
-__device__ __forceinline__ Plan plan_request(int32_t kv, int32_t m, int32_t group, int32_t streams, int32_t h_kv,
+__device__ __forceinline__ Plan plan_request(int32_t kv, int32_t m, int32_t group, int32_t d, int32_t h_kv,
                                              int32_t window) {
     Plan p;
+    const int32_t streams = streams_of(d);
     p.item_tokens = kRows / group * streams;
     p.row_items = ceil_div(m, p.item_tokens);
     int32_t lo, hi;
@@ -120,7 +131,8 @@ __device__ __forceinline__ Plan plan_request(int32_t kv, int32_t m, int32_t grou
         int32_t want = kSplitUnits / static_cast<int32_t>(units);
         if (want > kMaxSplits) want = kMaxSplits;
         const int32_t even = ceil_div(hi - lo, want);
-        p.split_tiles = even > kMinSplitTiles ? even : kMinSplitTiles;
+        const int32_t least = least_split_tiles(hi - lo, (m < p.item_tokens ? m : p.item_tokens) * group);
+        p.split_tiles = even > least ? even : least;
         p.split0 = lo / p.split_tiles;
         p.splits = hi > lo ? (hi - 1) / p.split_tiles - p.split0 + 1 : 1;
     }
@@ -132,11 +144,13 @@ __device__ __forceinline__ Plan plan_request(int32_t kv, int32_t m, int32_t grou
 // Bound of `partials` over the requests of a call: at most `want` splits and
 // one more where a window starts inside one, and never more than the longest
 // context has.
-int64_t partials_bound(int32_t group, int32_t streams, int32_t h_kv, int32_t num_reqs, int64_t num_tokens, int64_t max_kv_len) {
+int64_t partials_bound(int32_t group, int32_t d, int32_t h_kv, int32_t num_reqs, int64_t num_tokens, int64_t max_kv_len) {
+    const int32_t streams = streams_of(d);
     const int64_t tiles = (max_kv_len + kKeys - 1) / kKeys;
     if (h_kv * 2 > kSplitUnits || tiles <= kMinSplitTiles || num_tokens == 0 || num_reqs == 0) return 0;
     const int32_t want = kSplitUnits / h_kv < kMaxSplits ? kSplitUnits / h_kv : kMaxSplits;
-    const int64_t by_length = (tiles + kMinSplitTiles - 1) / kMinSplitTiles;
+    int64_t by_length = 1;  // least_split_tiles(s) >= sqrt(s / 2), so s tiles make at most sqrt(2 s) splits
+    while (by_length * by_length < 2 * tiles && by_length < want) ++by_length;
     const int64_t splits = want < by_length ? want : by_length;
     // m tokens make at least m / item_tokens row items, so m * want <= item_tokens * kSplitUnits / h_kv
     const int64_t by_request = static_cast<int64_t>(num_reqs) * (kRows / group * streams) * ceil_div(kSplitUnits, h_kv);
@@ -150,14 +164,23 @@ int64_t items_bound(int32_t group, int32_t streams, int32_t h_kv, int32_t num_re
     return (rows < num_tokens ? rows : num_tokens) * h_kv * (split ? kMaxSplits + 1 : 1);
 }
 
-// Workspace: the item counter, the first partial of each request, then (m, l)
-// and O of the partials.
+// What the joining kernel needs of a row (token and query head) of a request
+// that was split: its place in o, its first partial and how many there are (0:
+// the row is in o already).
+struct JoinRow {
+    int32_t out, parts;
+    int64_t first;
+};
+
+// Workspace: the item counter (zeroed by each call), the number of rows of
+// split requests and those rows, then (m, l) and O of the partials.
 struct Workspace {
     unsigned long long *counter;  // null: items are dealt round robin
-    int64_t *base;
+    int64_t *num_rows;
+    JoinRow *rows;
     float2 *ml;
     float *o;  // null: no request of this call can be split
-    int64_t partials;
+    int64_t partials, max_rows;
     size_t bytes;
 };
 Workspace workspace_at(void *ws, int32_t h_q, int32_t h_kv, int32_t d, int32_t num_reqs, int64_t num_tokens,
@@ -166,7 +189,7 @@ Workspace workspace_at(void *ws, int32_t h_q, int32_t h_kv, int32_t d, int32_t n
     const int32_t group = h_q / h_kv, streams = streams_of(d);
     Workspace w = {};
     char *p = static_cast<char *>(ws);
-    w.partials = partials_bound(group, streams, h_kv, num_reqs, num_tokens, max_kv_len);
+    w.partials = partials_bound(group, d, h_kv, num_reqs, num_tokens, max_kv_len);
     // One item per block at most: nothing to balance.
     if (items_bound(group, streams, h_kv, num_reqs, num_tokens, w.partials > 0) > kSplitUnits) {
         w.counter = reinterpret_cast<unsigned long long *>(p);
@@ -174,8 +197,10 @@ Workspace workspace_at(void *ws, int32_t h_q, int32_t h_kv, int32_t d, int32_t n
     }
     if (w.partials > 0) {
         const size_t rows = static_cast<size_t>(w.partials) * h_q;
-        w.base = reinterpret_cast<int64_t *>(p + w.bytes);
-        w.bytes += up(static_cast<size_t>(num_reqs) * sizeof(int64_t));
+        w.num_rows = reinterpret_cast<int64_t *>(p + w.bytes);
+        w.rows = reinterpret_cast<JoinRow *>(p + w.bytes + 256);
+        w.max_rows = num_tokens * h_q;
+        w.bytes += up(256 + static_cast<size_t>(w.max_rows) * sizeof(JoinRow));
         w.ml = reinterpret_cast<float2 *>(p + w.bytes);
         w.bytes += up(rows * sizeof(float2));
         w.o = reinterpret_cast<float *>(p + w.bytes);
@@ -200,8 +225,10 @@ struct Item {
     int32_t tok, n;     // first token (row of q) and tokens
     int32_t pos;        // position of the first token
     int32_t lo, hi;     // key tiles
-    int32_t splits;     // of the request
-    int64_t partial;    // first token's partial, or -1: the item gives the final result
+    // Of a request that is split (rows >= 0): its row items' places among the rows to join (first token, head 0); the
+    // first token's first partial, partials from one token to the next, parts of the row item, which one this is.
+    int64_t rows, partial;
+    int32_t splits, parts, part;
 };
 
 template <int D>
@@ -337,23 +364,29 @@ __device__ __forceinline__ Request load_request(const PagedAttentionArgs &a, int
 
 // Tokens that see no key: zeros, by the scheduler itself.
 template <int D>
-__device__ __forceinline__ void zero_rows(const PagedAttentionArgs &a, const Item &it, int32_t group, int lane) {
-    const int32_t pieces = group * (D / 8);
-    for (int32_t i = lane; i < it.n * pieces; i += 32)
-        reinterpret_cast<uint4 *>(a.o + ((static_cast<int64_t>(it.tok) + i / pieces) * a.h_q + it.head * group) * D)[i % pieces] =
-            make_uint4(0, 0, 0, 0);
+__device__ __forceinline__ void zero_rows(const AttentionLaunch &L, const Item &it, int lane) {
+    const PagedAttentionArgs &a = L.a;
+    const int32_t pieces = L.group * (D / 8);
+    for (int32_t i = lane; i < it.n * pieces; i += 32) {
+        const int32_t u = i / pieces, k = i - u * pieces;
+        uint16_t *out = a.o + ((static_cast<int64_t>(it.tok) + u) * a.h_q + it.head * L.group) * D;
+        reinterpret_cast<uint4 *>(out)[k] = make_uint4(0, 0, 0, 0);
+        if (it.rows >= 0 && k < L.group)
+            L.ws.rows[it.rows + static_cast<int64_t>(u) * a.h_q + it.head * L.group + k] = {0, 0, 0};
+    }
 }
 
 template <int D>
 __device__ void schedule(const AttentionLaunch &L, Control<D> *ctl, const Waiter &wait) {
     const PagedAttentionArgs &a = L.a;
     const int lane = threadIdx.x & 31;
-    const bool first_block = blockIdx.x == 0;
     uint32_t n = 0;
+    bool long_before = false;
     int64_t next = -1;
     // The next item's number, taken when there is room for the item.
     auto advance = [&]() {
         if (!wait.all(ctl->item_empty + n % kItems, (n / kItems & 1) ^ 1)) return false;
+        if (long_before && !wait.all(ctl->item_empty + (n - 1) % kItems, (n - 1) / kItems & 1)) return false;
         if (!L.ws.counter) {
             next = next < 0 ? blockIdx.x : next + gridDim.x;
         } else {
@@ -370,25 +403,29 @@ __device__ void schedule(const AttentionLaunch &L, Control<D> *ctl, const Waiter
             tc::mbar_arrive(ctl->item_full + s);
         }
         ++n;
+        long_before = it.hi - it.lo >= kLongItem;
         __syncwarp();
     };
     if (!advance()) return;
-    int64_t items0 = 0, partials0 = 0;
+    int64_t items0 = 0, partials0 = 0, rows0 = 0;
     // From the last request to the first: long prompts stand behind the decode rows and should start first.
     for (int64_t base = 0; base < a.num_reqs; base += 32) {
         const int64_t r = a.num_reqs - 1 - base - lane;
-        const Request q = load_request(a, r, first_block);
-        const Plan p = plan_request(q.kv, q.m, L.group, streams_of(D), a.cache.h_kv, a.window);
-        int64_t items = p.items, partials = p.partials;
+        const Request q = load_request(a, r, blockIdx.x == 0);
+        const Plan p = plan_request(q.kv, q.m, L.group, D, a.cache.h_kv, a.window);
+        const int64_t split_rows = p.splits > 1 ? static_cast<int64_t>(q.m) * a.h_q : 0;
+        int64_t items = p.items, partials = p.partials, rows = split_rows;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t x = __shfl_up_sync(0xffffffffu, items, o), y = __shfl_up_sync(0xffffffffu, partials, o);
+            const int64_t z = __shfl_up_sync(0xffffffffu, rows, o);
             if (lane >= o) {
                 items += x;
                 partials += y;
+                rows += z;
             }
         }
-        if (first_block && L.ws.o && r >= 0) L.ws.base[r] = partials0 + partials - p.partials;
+        if (blockIdx.x == 0 && L.ws.o && r == 0) *L.ws.num_rows = rows0 + rows;
         const int64_t group_items = __shfl_sync(0xffffffffu, items, 31);
         while (next < items0 + group_items) {
             const int src = __ffs(__ballot_sync(0xffffffffu, items0 + items > next)) - 1;
@@ -403,6 +440,7 @@ __device__ void schedule(const AttentionLaunch &L, Control<D> *ctl, const Waiter
             const int32_t first = __shfl_sync(0xffffffffu, q.first, src);
             const int64_t pbase = partials0 + __shfl_sync(0xffffffffu, partials - p.partials, src);
             const int32_t rest = static_cast<int32_t>(local / static_cast<uint32_t>(row_items));
+            const int64_t rbase = rows0 + __shfl_sync(0xffffffffu, rows - split_rows, src);
             const int32_t piece = row_items - 1 - static_cast<int32_t>(local - static_cast<uint32_t>(rest) * row_items);
             const int32_t split = split0 + rest / a.cache.h_kv;
             Item it;
@@ -413,29 +451,34 @@ __device__ void schedule(const AttentionLaunch &L, Control<D> *ctl, const Waiter
             it.n = m - u < p.item_tokens ? m - u : p.item_tokens;
             it.tok = first + u;
             it.pos = kv - m + u;
-            it.splits = splits;
             int32_t lo, hi;
             key_tiles(kv, m, u, it.n, a.window, &lo, &hi);
-            const bool whole = hi == lo || lo / split_tiles == (hi - 1) / split_tiles;
+            const int32_t split_lo = lo / split_tiles, split_hi = hi > lo ? (hi - 1) / split_tiles : split_lo;
             const int64_t s_lo = static_cast<int64_t>(split) * split_tiles, s_hi = s_lo + split_tiles;
             it.lo = s_lo > lo ? static_cast<int32_t>(s_lo) : lo;
             it.hi = s_hi < hi ? static_cast<int32_t>(s_hi) : hi;
-            it.partial = whole ? -1 : pbase + static_cast<int64_t>(u) * splits + (split - split0);
+            it.parts = split_hi - split_lo + 1;
+            it.part = split - split_lo;
+            it.splits = splits;
+            it.partial = pbase + static_cast<int64_t>(u) * splits + (split_lo - split0);
+            it.rows = splits > 1 ? rbase + static_cast<int64_t>(u) * a.h_q : -1;
             // A split past what the tokens see has nothing to do; tokens that see nothing are written by the first.
             bool run = it.lo < it.hi || (lo == hi && split == split0);
-            // Token ranges that overlap can ask for more partials than there are tokens for.
-            if (run && !whole && pbase + static_cast<int64_t>(m) * splits > L.ws.partials) {
+            // Token ranges that overlap can ask for more partials and rows than there are tokens for.
+            if (run && splits > 1 &&
+                (pbase + static_cast<int64_t>(m) * splits > L.ws.partials || rbase + static_cast<int64_t>(m) * a.h_q > L.ws.max_rows)) {
                 if (lane == 0) report(a.dev_status, GDN_DEV_BAD_LENGTH);
                 run = false;
             }
             if (run && it.lo < it.hi)
                 publish(it);
             else if (run)
-                zero_rows<D>(a, it, L.group, lane);
+                zero_rows<D>(L, it, lane);
             if (!advance()) return;
         }
         items0 += group_items;
         partials0 += __shfl_sync(0xffffffffu, partials, 31);
+        rows0 += __shfl_sync(0xffffffffu, rows, 31);
     }
     Item end = {};
     end.stop = 1;
@@ -575,14 +618,14 @@ __device__ void load_tiles(const AttentionLaunch &L, Control<D> *ctl, uint32_t q
     __syncwarp();
 }
 
-// ---- the MMA warp -----------------------------------------------------------
+// ---- the MMA warp ------------------------------------------------------------------------
 //
 // The whole warp runs the code and one elected lane issues: operands then stay
-// in uniform registers.  The tensor pipe holds about three products (64 cycles each) beyond the one
-// it runs, so the way from one batch's last product to the next one's first
-// has to be short: a stage pointer that only steps (stages are used in ring
-// order), barriers by shared address, descriptors by their low words, the
-// batch's V waited for before its weights.
+// in uniform registers.  The tensor pipe holds about three products (64 cycles
+// each) beyond the one it runs, so the way from one batch's last product to
+// the next one's first has to be short: a stage pointer that only steps
+// (stages are used in ring order), barriers by shared address, descriptors by
+// their low words.
 
 template <int D, bool kHalf>
 struct Issuer {
@@ -590,106 +633,79 @@ struct Issuer {
     static constexpr uint32_t kType = kHalf ? 0u : tc::kIdescBf16;
     static constexpr uint32_t kIdescS = tc::idesc_f16_f32acc(kRows, kKeys) | kType;
     static constexpr uint32_t kIdescO = tc::idesc_f16_f32acc(kRows, Sh::kCols) | kType | tc::kIdescBmn;
+    // A place in the ring: stage and the parity of its filling.
+    struct Place {
+        uint32_t stage, phase;
+        __device__ __forceinline__ void step(uint32_t n) {
+            stage += n;
+            if (stage >= Sh::kStages) {
+                stage -= Sh::kStages;
+                phase ^= 1;
+            }
+        }
+    };
     const Waiter &wait;
     uint32_t bars;  // address of the control block
     uint32_t ring, tmem;
-    uint32_t stage, phase;  // next stage of the ring
-    uint32_t used;          // per O: parity of the items that used it
-    // The unit whose product with P is still to be issued.
-    uint32_t left, left_stage;  // its number; V's stage where `left_loaded`
-    bool any, left_fresh, left_loaded;
+    Place next;     // of the next first use
+    uint32_t used;  // per O: parity of the items that used it
+    // The unit whose product with P is still to be issued: its number, whether it starts O, whether its V is the next
+    // in the ring (else it is at `v`), whether this is V's last use.
+    uint32_t left;
+    bool any, fresh, take, last_use;
+    Place v;
+    bool early;  // the V behind the next K has been used already
 
 #define GDN_BAR(name, i) (bars + static_cast<uint32_t>(offsetof(Control<D>, name)) + (i) * 8u)
 
-    __device__ __forceinline__ void step() {
-        if (++stage == Sh::kStages) {
-            stage = 0;
-            phase ^= 1;
-        }
-    }
-    // S of unit g from Q at q (low descriptor word), the item's `last`: Q is free after it.  kTake: K is the ring's next tile (else stage *at); kFree: its last use.
-    template <bool kTake, bool kFree>
-    __device__ __forceinline__ bool scores(uint32_t g, uint32_t q, uint32_t *at, bool last, uint32_t q_bar) {
+    // S of unit g from Q at q (low descriptor word) and the K tile at `k`.
+    __device__ __forceinline__ bool scores(uint32_t g, uint32_t q, Place k, bool k_free, bool q_free, uint32_t q_bar) {
+#pragma unroll
         for (int h = 0; h < Sh::kHalves; ++h) {
-            if (kTake) {
-                if (!wait.all(GDN_BAR(kv_full, stage), phase)) return false;
-                *at = stage;
-            }
+            if (h > 0 && !wait.all(GDN_BAR(kv_full, k.stage), k.phase)) return false;
             tc::fence_after_sync();
-            const uint32_t k = tc::desc_lo(ring + *at * Sh::kStage, 16);
+            const uint32_t kd = tc::desc_lo(ring + k.stage * Sh::kStage, 16);
             if (tc::elect_lane()) {
 #pragma unroll
                 for (int i = 0; i < Sh::kCols / 16; ++i)
                     tc::mma_f16_lo(tmem + (g & 1) * kKeys, q + (h * Sh::kPanels + i / 4) * (kPanel >> 4) + (i % 4) * 2,
-                                   k + i / 4 * (kPanel >> 4) + (i % 4) * 2, kIdescS, h > 0 || i > 0);
-                if (kFree) tc::mma_commit(GDN_BAR(kv_empty, *at));
+                                   kd + i / 4 * (kPanel >> 4) + (i % 4) * 2, kIdescS, h > 0 || i > 0);
+                if (k_free) tc::mma_commit(GDN_BAR(kv_empty, k.stage));
                 if (h + 1 == Sh::kHalves) {
                     tc::mma_commit(GDN_BAR(s_full, g & 1));
-                    if (last) tc::mma_commit(q_bar);
+                    if (q_free) tc::mma_commit(q_bar);
                 }
             }
-            if (kTake) step();
+            __syncwarp();
+            k.step(1);
         }
         return true;
     }
-    // O (+)= P V of unit g.  kTake, kFree as above for V.
-    template <bool kTake, bool kFree>
-    __device__ __forceinline__ bool weights(uint32_t g, bool fresh, uint32_t *at) {
-        const uint32_t b = g & 1, w = Sh::kStreams == 2 ? b : 0;
-        if (kTake && !wait.all(GDN_BAR(kv_full, stage), phase)) return false;
+    // O (+)= P V of the unit left over, V at `at`.
+    __device__ __forceinline__ bool weights(Place at) {
+        const uint32_t b = left & 1, w = Sh::kStreams == 2 ? b : 0;
+        any = false;
+        if (take && !wait.all(GDN_BAR(kv_full, at.stage), at.phase)) return false;
         if (fresh) {
             if (!wait.all(GDN_BAR(o_free, w), (used >> w & 1) ^ 1)) return false;
             used ^= 1u << w;
         }
-        if (!wait.all(GDN_BAR(p_full, b), g >> 1 & 1)) return false;
+        if (!wait.all(GDN_BAR(p_full, b), left >> 1 & 1)) return false;
+#pragma unroll
         for (int h = 0; h < Sh::kHalves; ++h) {
-            if (kTake) {
-                if (h > 0 && !wait.all(GDN_BAR(kv_full, stage), phase)) return false;
-                *at = stage;
-            }
+            if (h > 0 && !wait.all(GDN_BAR(kv_full, at.stage), at.phase)) return false;
             tc::fence_after_sync();
-            const uint32_t v = tc::desc_lo(ring + *at * Sh::kStage, kPanel);
+            const uint32_t vd = tc::desc_lo(ring + at.stage * Sh::kStage, kPanel);
             if (tc::elect_lane()) {
 #pragma unroll
                 for (int i = 0; i < kKeys / 16; ++i)
-                    tc::mma_f16_ta_lo(tmem + kTmemO + w * D + h * Sh::kCols, tmem + b * kKeys + i * 8, v + i * (2048 >> 4), kIdescO,
-                                      !fresh || i > 0);
-                if (kFree) tc::mma_commit(GDN_BAR(kv_empty, *at));
+                    tc::mma_f16_ta_lo(tmem + kTmemO + w * D + h * Sh::kCols, tmem + b * kKeys + i * 8, vd + i * (2048 >> 4),
+                                      kIdescO, !fresh || i > 0);
+                if (last_use) tc::mma_commit(GDN_BAR(kv_empty, at.stage));
                 if (h + 1 == Sh::kHalves) tc::mma_commit(GDN_BAR(o_done, w));
             }
-            if (kTake) step();
-        }
-        return true;
-    }
-    __device__ __forceinline__ bool weights_left() {
-        any = false;
-        return left_loaded ? weights<false, true>(left, left_fresh, &left_stage) : weights<true, true>(left, left_fresh, &left_stage);
-    }
-    // An item of one row tile: unit g + t is key tile t.  Ring order K, V of the tile before, K, V, ...
-    __device__ __forceinline__ bool single(uint32_t g, int32_t tiles, uint32_t q, uint32_t q_bar) {
-        for (int32_t t = 0; t < tiles; ++t, ++g) {
-            uint32_t at;
-            if (!scores<true, true>(g, q, &at, t + 1 == tiles, q_bar)) return false;
-            if (any && !weights_left()) return false;
-            any = true;
-            left = g;
-            left_fresh = t < Sh::kStreams;
-            left_loaded = false;
-        }
-        return true;
-    }
-    // An item of two row tiles: units g + 2t and g + 2t + 1 are key tile t.  Ring order K, V, K, V, ...
-    __device__ __forceinline__ bool dual(uint32_t g, int32_t tiles, uint32_t q, uint32_t q_bar) {
-        for (int32_t t = 0; t < tiles; ++t, g += 2) {
-            uint32_t at;
-            if (!scores<true, false>(g, q, &at, false, q_bar)) return false;
-            if (any && !weights_left()) return false;
-            if (!scores<false, true>(g + 1, q + (Sh::kQTile >> 4), &at, t + 1 == tiles, q_bar)) return false;
-            if (!weights<true, false>(g, t == 0, &left_stage)) return false;
-            any = true;
-            left = g + 1;
-            left_fresh = t == 0;
-            left_loaded = true;
+            __syncwarp();
+            at.step(1);
         }
         return true;
     }
@@ -697,27 +713,63 @@ struct Issuer {
         const int32_t tile_tokens = kRows / L.group;
         uint32_t unit = 0, n_items = 0;
         for (uint32_t n = 0;; ++n) {
-            const uint32_t s = n % kItems;
+            const uint32_t s = n % kItems, slot = n_items & 1;
+            // The product held back does not wait for what is late: the next item, its Q or its first K.  Its V lies
+            // behind the place of that K.
+            if (any && !__all_sync(0xffffffffu, tc::mbar_test_wait(GDN_BAR(item_full, s), n / kItems & 1) &&
+                                                    tc::mbar_test_wait(GDN_BAR(q_full, slot), n_items >> 1 & 1) &&
+                                                    tc::mbar_test_wait(GDN_BAR(kv_full, next.stage), next.phase))) {
+                Place at = v;
+                early = take;
+                if (take) {
+                    at = next;
+                    at.step(Sh::kHalves);
+                }
+                if (!weights(at)) break;
+            }
             if (!wait.all(GDN_BAR(item_full, s), n / kItems & 1)) break;
             // (through a warp reduction: what the compiler knows to be uniform it keeps in uniform registers)
             const int32_t stop = __reduce_max_sync(0xffffffffu, ctl->items[s].stop);
             const int32_t tokens = __reduce_max_sync(0xffffffffu, ctl->items[s].n);
             const int32_t tiles = __reduce_max_sync(0xffffffffu, ctl->items[s].hi - ctl->items[s].lo);
             if (tc::elect_lane()) tc::mbar_arrive(ctl->item_empty + s);
-            if (stop) {
-                if (any && !left_loaded)  // V of the last tile lies behind the place of a next item's first K
-                    for (int h = 0; h < Sh::kHalves; ++h) step();
-                if (any) weights_left();
-                break;
-            }
+            __syncwarp();
+            if (stop) break;
             const bool two = Sh::kStreams == 2 && tokens > tile_tokens;
             const bool few = tokens < tile_tokens && tokens * (D / 64) <= 32;
             const bool wide = Sh::kStreams == 2 ? two : !(few && tokens * L.group <= Sh::kSmallRows);
-            const uint32_t slot = n_items & 1;
             if (!wait.all(GDN_BAR(q_full, slot), n_items >> 1 & 1)) break;
             const uint32_t q = tc::desc_lo(q_smem + (wide ? 0 : slot * Sh::kQSlot), 16);
-            if (!(two ? dual(unit, tiles, q, GDN_BAR(q_empty, slot)) : single(unit, tiles, q, GDN_BAR(q_empty, slot)))) break;
-            unit += two ? 2 * tiles : tiles;
+            const int32_t units = two ? 2 * tiles : tiles;
+            Place k = next;
+            int32_t u = 0;
+            for (; u < units; ++u, ++unit) {
+                const bool second = two && (u & 1);  // of a dual item's two units of a key tile
+                if (!second) {
+                    if (!wait.all(GDN_BAR(kv_full, next.stage), next.phase)) break;
+                    k = next;
+                }
+                if (!scores(unit, second ? q + (Sh::kQTile >> 4) : q, k, !two || second, u + 1 == units, GDN_BAR(q_empty, slot)))
+                    break;
+                if (!second) {
+                    next.step(Sh::kHalves);
+                    if (early) next.step(Sh::kHalves);
+                    early = false;
+                }
+                if (any) {
+                    if (take) {
+                        v = next;
+                        next.step(Sh::kHalves);
+                    }
+                    if (!weights(v)) break;
+                }
+                any = true;
+                left = unit;
+                fresh = u < Sh::kStreams;
+                take = !second;
+                last_use = !two || second;
+            }
+            if (u < units) break;
             ++n_items;
         }
         if (tc::elect_lane()) tc::mma_commit(GDN_BAR(drain, 0));
@@ -823,6 +875,13 @@ __device__ __forceinline__ void scale_o(uint32_t t_o, float f) {
         for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
         tc::tmem_st16(t_o + q * 16, o);
     }
+}
+
+// 32 bytes at once: whole sectors from threads that each write their own row.
+__device__ __forceinline__ void store32(void *p, const uint32_t *x) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+                 "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
 }
 
 template <int D, bool kHalf>
@@ -945,8 +1004,12 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
         }
         if (writer && any_row) {
             const int64_t head = static_cast<int64_t>(it.head) * L.group + g;
-            const bool split = it.partial >= 0;
-            const int64_t prow = (it.partial + static_cast<int64_t>(u) * it.splits) * a.h_q + head;
+            const bool split = it.parts > 1;
+            const int64_t first = (it.partial + static_cast<int64_t>(u) * it.splits) * a.h_q + head;
+            const int64_t prow = first + static_cast<int64_t>(it.part) * a.h_q;
+            if (valid && it.rows >= 0 && it.part == 0)
+                L.ws.rows[it.rows + static_cast<int64_t>(u) * a.h_q + head] = {
+                    static_cast<int32_t>((it.tok + u) * a.h_q + head), split ? it.parts : 0, first};
             const bool none = l == 0.f;  // no key seen, or all weights zero
             if (!split) {
                 const float inv = none ? 0.f : 1.f / l;
@@ -959,28 +1022,26 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
             float *pout = L.ws.o + prow * D;
 #pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
-                float y[32];
                 uint32_t o[32];
                 tc::tmem_ld32(t_o + w * D + q * 32, o);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) y[j] = none ? 0.f : __uint_as_float(o[j]) * f0;
+                for (int j = 0; j < 32; ++j) o[j] = none ? 0u : __float_as_uint(__uint_as_float(o[j]) * f0);
                 if (pair) {
-                    tc::tmem_ld32(t_o + (w ^ 1) * D + q * 32, o);
+                    uint32_t o1[32];
+                    tc::tmem_ld32(t_o + (w ^ 1) * D + q * 32, o1);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) y[j] = none ? 0.f : fmaf(__uint_as_float(o[j]), f1, y[j]);
+                    for (int j = 0; j < 32; ++j)
+                        o[j] = none ? 0u : __float_as_uint(fmaf(__uint_as_float(o1[j]), f1, __uint_as_float(o[j])));
                 }
-                if (valid) {
-                    if (split) {
+                if (valid && split) {
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4)
-                            *reinterpret_cast<float4 *>(pout + q * 32 + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
-                    } else {
+                    for (int j = 0; j < 32; j += 8) store32(pout + q * 32 + j, o + j);
+                } else if (valid) {
 #pragma unroll
-                        for (int j = 0; j < 32; j += 8)
-                            *reinterpret_cast<uint4 *>(out + q * 32 + j) =
-                                make_uint4(pack2<kHalf>(y[j], y[j + 1]), pack2<kHalf>(y[j + 2], y[j + 3]),
-                                           pack2<kHalf>(y[j + 4], y[j + 5]), pack2<kHalf>(y[j + 6], y[j + 7]));
-                    }
+                    for (int j = 0; j < 16; ++j)
+                        o[j] = pack2<kHalf>(__uint_as_float(o[2 * j]), __uint_as_float(o[2 * j + 1]));
+#pragma unroll
+                    for (int j = 0; j < 16; j += 8) store32(out + q * 32 + j * 2, o + j);
                 }
             }
         }
@@ -1073,74 +1134,54 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attention_kernel(const 
 // ---- joining the splits -----------------------------------------------------------------------
 
 constexpr int kJoinWarps = 4;
+constexpr int kJoinBlocksPerSm = 8;
 
-// Last r in [0, n) with cu[r] <= t, by the warp: 32 probes a step.
-__device__ __forceinline__ int32_t find_request(const int32_t *cu, int32_t n, int32_t t, int lane) {
-    int32_t lo = 0, hi = n;  // cu[lo] <= t, and cu[hi] > t or hi == n
-    while (hi - lo > 1) {
-        const int32_t step = ceil_div(hi - lo, 32);
-        const int64_t at = lo + static_cast<int64_t>(step) * lane;
-        const bool le = at < hi && cu[at] <= t;
-        const int last = 31 - __clz(__ballot_sync(0xffffffffu, le) | 1u);
-        const int64_t top = lo + static_cast<int64_t>(step) * (last + 1);
-        lo += step * last;
-        if (top < hi) hi = static_cast<int32_t>(top);
-    }
-    return lo;
-}
-
-// o = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s over a row's splits, in
-// split order: one warp per (token, query head), lane i holding every 32nd
-// group of four columns.
+// o = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s over a row's parts, in
+// their order; one warp per row, the rows dealt over a grid that fills the GPU
+// once.  Requests that were not split have no rows here.  Bound by the latency
+// of three dependent reads (rows, row, its partials) where there are few, by
+// L2 (the partials were just written) where there are many.
 template <int D, bool kHalf>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ AttentionLaunch L) {
-    const PagedAttentionArgs &a = L.a;
     const int lane = threadIdx.x & 31;
-    const uint32_t row = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);  // under 2^31 + kJoinWarps
-    const bool any = row < a.num_tokens * a.h_q;
-    const int32_t t = any ? static_cast<int32_t>(row / static_cast<uint32_t>(a.h_q)) : 0;
-    const int32_t r = find_request(a.cu_seqlens, a.num_reqs, t, lane);
-    const Request q = load_request(a, r, false);
-    const Plan p = plan_request(q.kv, q.m, L.group, streams_of(D), a.cache.h_kv, a.window);
-    const int32_t u = t - q.first, u0 = u / p.item_tokens * p.item_tokens;
-    const int32_t n = q.m - u0 < p.item_tokens ? q.m - u0 : p.item_tokens;
-    int32_t lo, hi;
-    key_tiles(q.kv, q.m, u0, n, a.window, &lo, &hi);
-    const int32_t s0 = lo / p.split_tiles, s1 = hi > lo ? (hi - 1) / p.split_tiles + 1 : s0;
-    // Every block waits for the attention kernel's end, also one with nothing to join: what follows this kernel in
+    const int64_t h_q = L.a.h_q;
+    // Every thread waits for the attention kernel's end, also one with nothing to join: what follows this kernel in
     // the stream relies on both.
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    // One split wrote the row itself.
-    if (!any || t < q.first || t >= q.first + q.m || s1 - s0 < 2) return;
-    const int64_t base = L.ws.base[r];
-    if (base < 0 || base + p.partials > L.ws.partials) return;  // not written: the call timed out or its ranges overlap
-    const int64_t first = (base + static_cast<int64_t>(u) * p.splits + (s0 - p.split0)) * a.h_q +
-                          (row - static_cast<uint32_t>(t) * a.h_q);
-    float top = -INFINITY;
-    for (int32_t s = lane; s < s1 - s0; s += 32) top = fmaxf(top, L.ws.ml[first + static_cast<int64_t>(s) * a.h_q].x);
+    const int64_t rows = *L.ws.num_rows < L.ws.max_rows ? *L.ws.num_rows : L.ws.max_rows;
+    for (int64_t i = blockIdx.x * kJoinWarps + (threadIdx.x >> 5); i < rows; i += gridDim.x * kJoinWarps) {
+        const JoinRow row = L.ws.rows[i];
+        // (a call that timed out or was given overlapping token ranges leaves rows unwritten)
+        if (row.parts < 2 || row.parts > kMaxSplits + 1 || row.first < 0 ||
+            row.first + (row.parts - 1) * h_q >= L.ws.partials * h_q || row.out < 0 || row.out >= L.ws.max_rows)
+            continue;
+        float top = -INFINITY;
+        for (int32_t s = lane; s < row.parts; s += 32) top = fmaxf(top, L.ws.ml[row.first + s * h_q].x);
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-    if (top == -INFINITY) top = 0.f;
-    constexpr int kVec = D / 64;  // pairs of columns of a lane
-    float acc[kVec][2] = {}, l = 0.f;
-#pragma unroll 4
-    for (int32_t s = 0; s < s1 - s0; ++s) {
-        const int64_t at = first + static_cast<int64_t>(s) * a.h_q;
-        const float2 ml = L.ws.ml[at];
-        const float w = ex2(ml.x - top);
-        l = fmaf(w, ml.y, l);
+        for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        if (top == -INFINITY) top = 0.f;
+        constexpr int kVec = D / 64;  // pairs of columns of a lane
+        float acc[kVec][2] = {}, l = 0.f;
+#pragma unroll 8
+        for (int32_t s = 0; s < row.parts; ++s) {
+            const int64_t at = row.first + s * h_q;
+            const float2 ml = L.ws.ml[at];
+            const float w = ex2(ml.x - top);
+            l = fmaf(w, ml.y, l);
 #pragma unroll
-        for (int v = 0; v < kVec; ++v) {
-            const float2 o = *reinterpret_cast<const float2 *>(L.ws.o + at * D + v * 64 + lane * 2);
-            acc[v][0] = fmaf(w, o.x, acc[v][0]);
-            acc[v][1] = fmaf(w, o.y, acc[v][1]);
+            for (int v = 0; v < kVec; ++v) {
+                const float2 o = *reinterpret_cast<const float2 *>(L.ws.o + at * D + v * 64 + lane * 2);
+                acc[v][0] = fmaf(w, o.x, acc[v][0]);
+                acc[v][1] = fmaf(w, o.y, acc[v][1]);
+            }
         }
-    }
-    const float f = 1.f / l;
+        const bool none = l == 0.f;
+        const float f = none ? 0.f : 1.f / l;
+        uint16_t *out = L.a.o + static_cast<int64_t>(row.out) * D + lane * 2;
 #pragma unroll
-    for (int v = 0; v < kVec; ++v)
-        *reinterpret_cast<uint32_t *>(a.o + static_cast<int64_t>(row) * D + v * 64 + lane * 2) =
-            pack2<kHalf>(l == 0.f ? 0.f : acc[v][0] * f, l == 0.f ? 0.f : acc[v][1] * f);
+        for (int v = 0; v < kVec; ++v)
+            *reinterpret_cast<uint32_t *>(out + v * 64) = none ? 0u : pack2<kHalf>(acc[v][0] * f, acc[v][1] * f);
+    }
 }
 
 template <int D, bool kHalf>
@@ -1163,11 +1204,12 @@ cudaError_t launch_d(const AttentionLaunch &L, int64_t items, cudaStream_t strea
     attention_kernel<D, kHalf><<<blocks, Shape<D>::kThreads, Shape<D>::kSmem, stream>>>(L);
     e = cudaGetLastError();
     if (e != cudaSuccess || !L.ws.o) return e;
+    const int64_t joins = (L.a.num_tokens * L.a.h_q + kJoinWarps - 1) / kJoinWarps, most = int64_t{sms} * kJoinBlocksPerSm;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((L.a.num_tokens * L.a.h_q + kJoinWarps - 1) / kJoinWarps));
+    cfg.gridDim = dim3(static_cast<unsigned>(joins < most ? joins : most));
     cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = stream;
-    // Its blocks may come up while the last items run; they wait for them before reading a partial.
+    // Its launch overlaps the attention kernel's end; it waits for that before it reads.
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
