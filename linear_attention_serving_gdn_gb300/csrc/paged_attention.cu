@@ -72,15 +72,19 @@ constexpr int kRows = 128;     // query rows of a tile (TMEM lanes)
 constexpr int kKeys = 128;     // keys of a tile
 constexpr int kPanel = 16384;  // 128 rows of 64 16-bit elements
 constexpr int kItems = 4;      // items between the scheduler and the other warps
-constexpr int kLongItem = 16;  // key tiles: behind such an item no further one is taken until it has begun
+// Items are taken ahead of their turn while those that have not begun hold no more keys and values than this.
+constexpr int kAheadBytes = 512 * 1024;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 256;  // O after the two S buffers
 
-// Splits.  A request alone should fill kSplitUnits SMs; the constant stands in
-// for the SM count so that results do not depend on the device.
+// Splits.  A request alone should fill kSplitUnits SMs where its row tiles are
+// full, half of them where they are not: then memory is the bound, and 76 SMs
+// draw all of it.  The constant stands in for the SM count so that results do
+// not depend on the device.
 constexpr int kSplitUnits = 152;
 constexpr int kMaxSplits = 64;
 constexpr int kMinSplitTiles = 2;
+constexpr int kMaxSplitTiles = 16;  // of few rows, while kMaxSplits allow: long items balance badly over the SMs
 // The least key tiles of a split of `tiles` by an item of `rows` query rows.  A
 // part's cost beside its keys is its partial result, in proportion to its rows:
 // a full tile's is that of two key tiles.  And each part costs the joining
@@ -97,8 +101,9 @@ __host__ __device__ constexpr int streams_of(int d) { return d <= 128 ? 2 : 1; }
 struct Plan {
     int32_t row_items;    // pieces of the new tokens
     int32_t item_tokens;  // tokens of one
+    int32_t first_tile;   // that any of its tokens sees: where its splits start
     int32_t split_tiles;  // key tiles of a split
-    int32_t split0, splits;
+    int32_t splits;
     int64_t items;
     int64_t partials;  // (token, split) pairs that may leave partial results
 };
@@ -123,45 +128,50 @@ __device__ __forceinline__ Plan plan_request(int32_t kv, int32_t m, int32_t grou
     p.row_items = ceil_div(m, p.item_tokens);
     int32_t lo, hi;
     key_tiles(kv, m, 0, m, window, &lo, &hi);
+    p.first_tile = lo;
     p.split_tiles = INT_MAX;
-    p.split0 = 0;
     p.splits = 1;
     const int64_t units = static_cast<int64_t>(p.row_items) * h_kv;
-    if (m > 0 && units * 2 <= kSplitUnits) {
-        int32_t want = kSplitUnits / static_cast<int32_t>(units);
+    const int32_t rows = (m < p.item_tokens ? m : p.item_tokens) * group;
+    const bool few = rows < kRows / 2;
+    const int32_t fill = few ? kSplitUnits / 2 : kSplitUnits;
+    if (m > 0 && (few || units * 2 <= fill)) {
+        int32_t want = units < fill ? fill / static_cast<int32_t>(units) : 1;
         if (want > kMaxSplits) want = kMaxSplits;
-        const int32_t even = ceil_div(hi - lo, want);
-        const int32_t least = least_split_tiles(hi - lo, (m < p.item_tokens ? m : p.item_tokens) * group);
+        const int32_t even = ceil_div(hi - lo, want), least = least_split_tiles(hi - lo, rows);
         p.split_tiles = even > least ? even : least;
-        p.split0 = lo / p.split_tiles;
-        p.splits = hi > lo ? (hi - 1) / p.split_tiles - p.split0 + 1 : 1;
+        if (few) {
+            const int32_t most = ceil_div(hi - lo, kMaxSplits) > kMaxSplitTiles ? ceil_div(hi - lo, kMaxSplits) : kMaxSplitTiles;
+            if (p.split_tiles > most) p.split_tiles = most;
+        }
+        p.splits = hi > lo ? ceil_div(hi - lo, p.split_tiles) : 1;
     }
     p.items = units * p.splits;
     p.partials = p.splits > 1 ? static_cast<int64_t>(m) * p.splits : 0;
     return p;
 }
 
-// Bound of `partials` over the requests of a call: at most `want` splits and
-// one more where a window starts inside one, and never more than the longest
-// context has.
+// Bound of `partials` over the requests of a call: no more splits than
+// kMaxSplits or than the longest context's.
 int64_t partials_bound(int32_t group, int32_t d, int32_t h_kv, int32_t num_reqs, int64_t num_tokens, int64_t max_kv_len) {
-    const int32_t streams = streams_of(d);
     const int64_t tiles = (max_kv_len + kKeys - 1) / kKeys;
-    if (h_kv * 2 > kSplitUnits || tiles <= kMinSplitTiles || num_tokens == 0 || num_reqs == 0) return 0;
-    const int32_t want = kSplitUnits / h_kv < kMaxSplits ? kSplitUnits / h_kv : kMaxSplits;
-    int64_t by_length = 1;  // least_split_tiles(s) >= sqrt(s / 2), so s tiles make at most sqrt(2 s) splits
-    while (by_length * by_length < 2 * tiles && by_length < want) ++by_length;
-    const int64_t splits = want < by_length ? want : by_length;
-    // m tokens make at least m / item_tokens row items, so m * want <= item_tokens * kSplitUnits / h_kv
-    const int64_t by_request = static_cast<int64_t>(num_reqs) * (kRows / group * streams) * ceil_div(kSplitUnits, h_kv);
-    const int64_t by_token = num_tokens * splits;
-    return (by_token < by_request ? by_token : by_request) + num_tokens;
+    if (tiles <= kMinSplitTiles || num_tokens == 0 || num_reqs == 0) return 0;
+    // least_split_tiles(s) >= sqrt(s / 2), so s tiles make at most sqrt(2 s) splits, or as many as the cap makes of them.
+    int64_t splits = (tiles + kMaxSplitTiles - 1) / kMaxSplitTiles;
+    while (splits * splits < 2 * tiles) ++splits;
+    if (splits > kMaxSplits) splits = kMaxSplits;
+    // With full tiles m tokens make at least m / item_tokens row items and at most kSplitUnits / (h_kv * row items)
+    // splits; fewer tokens than half a tile's make at most kMaxSplits.
+    const int64_t full = static_cast<int64_t>(kRows / group * streams_of(d)) * ceil_div(kSplitUnits, h_kv);
+    const int64_t few = static_cast<int64_t>(kRows / 2 / group + 1) * kMaxSplits;
+    const int64_t by_request = num_reqs * (full > few ? full : few), by_token = num_tokens * splits;
+    return by_token < by_request ? by_token : by_request;
 }
 
 // Bound of the items of a call.
 int64_t items_bound(int32_t group, int32_t streams, int32_t h_kv, int32_t num_reqs, int64_t num_tokens, bool split) {
     const int64_t rows = num_tokens / (kRows / group * streams) + num_reqs;
-    return (rows < num_tokens ? rows : num_tokens) * h_kv * (split ? kMaxSplits + 1 : 1);
+    return (rows < num_tokens ? rows : num_tokens) * h_kv * (split ? kMaxSplits : 1);
 }
 
 // What the joining kernel needs of a row (token and query head) of a request
@@ -381,12 +391,22 @@ __device__ void schedule(const AttentionLaunch &L, Control<D> *ctl, const Waiter
     const PagedAttentionArgs &a = L.a;
     const int lane = threadIdx.x & 31;
     uint32_t n = 0;
-    bool long_before = false;
+    constexpr int32_t kAheadTiles = kAheadBytes / (kKeys * D * 4);
+    uint32_t begun = 0;  // items known to have begun
+    int32_t ahead = 0;   // key tiles of those that are not
     int64_t next = -1;
     // The next item's number, taken when there is room for the item.
     auto advance = [&]() {
         if (!wait.all(ctl->item_empty + n % kItems, (n / kItems & 1) ^ 1)) return false;
-        if (long_before && !wait.all(ctl->item_empty + (n - 1) % kItems, (n - 1) / kItems & 1)) return false;
+        auto pass = [&]() {  // the oldest item taken has begun
+            ahead -= __reduce_max_sync(0xffffffffu, lane == 0 ? ctl->items[begun % kItems].hi - ctl->items[begun % kItems].lo : 0);
+            ++begun;
+        };
+        if (n >= kItems && begun == n - kItems) pass();
+        while (ahead > kAheadTiles) {
+            if (!wait.all(ctl->item_empty + begun % kItems, begun / kItems & 1)) return false;
+            pass();
+        }
         if (!L.ws.counter) {
             next = next < 0 ? blockIdx.x : next + gridDim.x;
         } else {
@@ -403,7 +423,7 @@ __device__ void schedule(const AttentionLaunch &L, Control<D> *ctl, const Waiter
             tc::mbar_arrive(ctl->item_full + s);
         }
         ++n;
-        long_before = it.hi - it.lo >= kLongItem;
+        ahead += it.hi - it.lo;
         __syncwarp();
     };
     if (!advance()) return;
@@ -429,41 +449,43 @@ __device__ void schedule(const AttentionLaunch &L, Control<D> *ctl, const Waiter
         const int64_t group_items = __shfl_sync(0xffffffffu, items, 31);
         while (next < items0 + group_items) {
             const int src = __ffs(__ballot_sync(0xffffffffu, items0 + items > next)) - 1;
-            // Items of a request: the row items of one (split, head) next to each other, longest first.
+            // Items of a request: the last row item first (it sees the most keys), all its splits and heads.
             // (at most h_kv times the row items, or few splits of few: 32 bits)
             const uint32_t local = static_cast<uint32_t>(next - items0 - __shfl_sync(0xffffffffu, items - p.items, src));
             const int32_t m = __shfl_sync(0xffffffffu, q.m, src), kv = __shfl_sync(0xffffffffu, q.kv, src);
             const int32_t row_items = __shfl_sync(0xffffffffu, p.row_items, src);
             const int32_t split_tiles = __shfl_sync(0xffffffffu, p.split_tiles, src);
-            const int32_t split0 = __shfl_sync(0xffffffffu, p.split0, src);
+            const int32_t first_tile = __shfl_sync(0xffffffffu, p.first_tile, src);
             const int32_t splits = __shfl_sync(0xffffffffu, p.splits, src);
             const int32_t first = __shfl_sync(0xffffffffu, q.first, src);
             const int64_t pbase = partials0 + __shfl_sync(0xffffffffu, partials - p.partials, src);
-            const int32_t rest = static_cast<int32_t>(local / static_cast<uint32_t>(row_items));
+            const uint32_t heads = static_cast<uint32_t>(a.cache.h_kv), per_piece = heads * static_cast<uint32_t>(splits);
+            const uint32_t nth = local / per_piece, rest = local - nth * per_piece;
+            const int32_t piece = row_items - 1 - static_cast<int32_t>(nth);
+            const int32_t split = static_cast<int32_t>(rest / heads);
             const int64_t rbase = rows0 + __shfl_sync(0xffffffffu, rows - split_rows, src);
-            const int32_t piece = row_items - 1 - static_cast<int32_t>(local - static_cast<uint32_t>(rest) * row_items);
-            const int32_t split = split0 + rest / a.cache.h_kv;
             Item it;
             it.stop = 0;
             it.req = static_cast<int32_t>(a.num_reqs - 1 - base) - src;
-            it.head = rest % a.cache.h_kv;
+            it.head = static_cast<int32_t>(rest % heads);
             const int32_t u = piece * p.item_tokens;
             it.n = m - u < p.item_tokens ? m - u : p.item_tokens;
             it.tok = first + u;
             it.pos = kv - m + u;
             int32_t lo, hi;
             key_tiles(kv, m, u, it.n, a.window, &lo, &hi);
-            const int32_t split_lo = lo / split_tiles, split_hi = hi > lo ? (hi - 1) / split_tiles : split_lo;
-            const int64_t s_lo = static_cast<int64_t>(split) * split_tiles, s_hi = s_lo + split_tiles;
+            const int32_t split_lo = (lo - first_tile) / split_tiles;
+            const int32_t split_hi = hi > lo ? (hi - 1 - first_tile) / split_tiles : split_lo;
+            const int64_t s_lo = first_tile + static_cast<int64_t>(split) * split_tiles, s_hi = s_lo + split_tiles;
             it.lo = s_lo > lo ? static_cast<int32_t>(s_lo) : lo;
             it.hi = s_hi < hi ? static_cast<int32_t>(s_hi) : hi;
             it.parts = split_hi - split_lo + 1;
             it.part = split - split_lo;
             it.splits = splits;
-            it.partial = pbase + static_cast<int64_t>(u) * splits + (split_lo - split0);
+            it.partial = pbase + static_cast<int64_t>(u) * splits + split_lo;
             it.rows = splits > 1 ? rbase + static_cast<int64_t>(u) * a.h_q : -1;
             // A split past what the tokens see has nothing to do; tokens that see nothing are written by the first.
-            bool run = it.lo < it.hi || (lo == hi && split == split0);
+            bool run = it.lo < it.hi || (lo == hi && split == 0);
             // Token ranges that overlap can ask for more partials and rows than there are tokens for.
             if (run && splits > 1 &&
                 (pbase + static_cast<int64_t>(m) * splits > L.ws.partials || rbase + static_cast<int64_t>(m) * a.h_q > L.ws.max_rows)) {
@@ -622,10 +644,11 @@ __device__ void load_tiles(const AttentionLaunch &L, Control<D> *ctl, uint32_t q
 //
 // The whole warp runs the code and one elected lane issues: operands then stay
 // in uniform registers.  The tensor pipe holds about three products (64 cycles
-// each) beyond the one it runs, so the way from one batch's last product to
-// the next one's first has to be short: a stage pointer that only steps
-// (stages are used in ring order), barriers by shared address, descriptors by
-// their low words.
+// each) beyond the one it runs, and a wait costs 50 cycles and more even where
+// nothing is left to wait for, so what the next batch needs is looked at
+// between a batch's products, while the pipe has work; after a batch's last
+// product only its commits and the wait for the weights stand before the next
+// one.  Stages are used in ring order: the place only steps.
 
 template <int D, bool kHalf>
 struct Issuer {
@@ -633,6 +656,7 @@ struct Issuer {
     static constexpr uint32_t kType = kHalf ? 0u : tc::kIdescBf16;
     static constexpr uint32_t kIdescS = tc::idesc_f16_f32acc(kRows, kKeys) | kType;
     static constexpr uint32_t kIdescO = tc::idesc_f16_f32acc(kRows, Sh::kCols) | kType | tc::kIdescBmn;
+    static constexpr int kScoreSteps = Sh::kCols / 16, kWeightSteps = kKeys / 16;  // products of a stage
     // A place in the ring: stage and the parity of its filling.
     struct Place {
         uint32_t stage, phase;
@@ -650,31 +674,45 @@ struct Issuer {
     Place next;     // of the next first use
     uint32_t used;  // per O: parity of the items that used it
     // The unit whose product with P is still to be issued: its number, whether it starts O, whether its V is the next
-    // in the ring (else it is at `v`), whether this is V's last use.
+    // in the ring (else it is at `v`, loaded).
     uint32_t left;
-    bool any, fresh, take, last_use;
+    bool any, fresh, take;
     Place v;
-    bool early;  // the V behind the next K has been used already
+    bool early;    // the V behind the next K has been used already
+    bool k_ready;  // the next K has been seen to be there
+    bool v_ready;  // so has the V of the unit left over
 
 #define GDN_BAR(name, i) (bars + static_cast<uint32_t>(offsetof(Control<D>, name)) + (i) * 8u)
 
-    // S of unit g from Q at q (low descriptor word) and the K tile at `k`.
-    __device__ __forceinline__ bool scores(uint32_t g, uint32_t q, Place k, bool k_free, bool q_free, uint32_t q_bar) {
+    __device__ __forceinline__ bool seen(uint32_t bar, uint32_t parity) const {
+        return __all_sync(0xffffffffu, tc::mbar_test_wait(bar, parity));
+    }
+    // S of unit g from Q at q (low descriptor word) and the K tile at `k`; `between` runs after most products are issued.
+    template <bool kFree, typename Between>
+    __device__ __forceinline__ bool scores(uint32_t g, uint32_t q, Place k, bool q_free, uint32_t q_bar, Between between) {
 #pragma unroll
         for (int h = 0; h < Sh::kHalves; ++h) {
             if (h > 0 && !wait.all(GDN_BAR(kv_full, k.stage), k.phase)) return false;
             tc::fence_after_sync();
             const uint32_t kd = tc::desc_lo(ring + k.stage * Sh::kStage, 16);
+            const uint32_t qd = q + h * Sh::kPanels * (kPanel >> 4), d = tmem + (g & 1) * kKeys;
+            constexpr int kFirst = kScoreSteps - kScoreSteps / 3;
+            const bool last = h + 1 == Sh::kHalves;
             if (tc::elect_lane()) {
 #pragma unroll
-                for (int i = 0; i < Sh::kCols / 16; ++i)
-                    tc::mma_f16_lo(tmem + (g & 1) * kKeys, q + (h * Sh::kPanels + i / 4) * (kPanel >> 4) + (i % 4) * 2,
-                                   kd + i / 4 * (kPanel >> 4) + (i % 4) * 2, kIdescS, h > 0 || i > 0);
-                if (k_free) tc::mma_commit(GDN_BAR(kv_empty, k.stage));
-                if (h + 1 == Sh::kHalves) {
-                    tc::mma_commit(GDN_BAR(s_full, g & 1));
-                    if (q_free) tc::mma_commit(q_bar);
-                }
+                for (int i = 0; i < kFirst; ++i)
+                    tc::mma_f16_lo(d, qd + i / 4 * (kPanel >> 4) + (i % 4) * 2, kd + i / 4 * (kPanel >> 4) + (i % 4) * 2, kIdescS,
+                                   h > 0 || i > 0);
+            }
+            __syncwarp();
+            if (last) between();
+            if (tc::elect_lane()) {
+#pragma unroll
+                for (int i = kFirst; i < kScoreSteps; ++i)
+                    tc::mma_f16_lo(d, qd + i / 4 * (kPanel >> 4) + (i % 4) * 2, kd + i / 4 * (kPanel >> 4) + (i % 4) * 2, kIdescS, 1);
+                if (last) tc::mma_commit(GDN_BAR(s_full, g & 1));
+                if (kFree) tc::mma_commit(GDN_BAR(kv_empty, k.stage));
+                if (last && q_free) tc::mma_commit(q_bar);
             }
             __syncwarp();
             k.step(1);
@@ -682,10 +720,11 @@ struct Issuer {
         return true;
     }
     // O (+)= P V of the unit left over, V at `at`.
-    __device__ __forceinline__ bool weights(Place at) {
+    template <bool kFree, typename Between>
+    __device__ __forceinline__ bool weights(Place at, Between between) {
         const uint32_t b = left & 1, w = Sh::kStreams == 2 ? b : 0;
         any = false;
-        if (take && !wait.all(GDN_BAR(kv_full, at.stage), at.phase)) return false;
+        if (!v_ready && !wait.all(GDN_BAR(kv_full, at.stage), at.phase)) return false;
         if (fresh) {
             if (!wait.all(GDN_BAR(o_free, w), (used >> w & 1) ^ 1)) return false;
             used ^= 1u << w;
@@ -696,16 +735,88 @@ struct Issuer {
             if (h > 0 && !wait.all(GDN_BAR(kv_full, at.stage), at.phase)) return false;
             tc::fence_after_sync();
             const uint32_t vd = tc::desc_lo(ring + at.stage * Sh::kStage, kPanel);
+            const uint32_t d = tmem + kTmemO + w * D + h * Sh::kCols, p = tmem + b * kKeys;
+            constexpr int kFirst = kWeightSteps - 3;
+            const bool last = h + 1 == Sh::kHalves;
             if (tc::elect_lane()) {
 #pragma unroll
-                for (int i = 0; i < kKeys / 16; ++i)
-                    tc::mma_f16_ta_lo(tmem + kTmemO + w * D + h * Sh::kCols, tmem + b * kKeys + i * 8, vd + i * (2048 >> 4),
-                                      kIdescO, !fresh || i > 0);
-                if (last_use) tc::mma_commit(GDN_BAR(kv_empty, at.stage));
-                if (h + 1 == Sh::kHalves) tc::mma_commit(GDN_BAR(o_done, w));
+                for (int i = 0; i < kFirst; ++i)
+                    tc::mma_f16_ta_lo(d, p + i * 8, vd + i * (2048 >> 4), kIdescO, !fresh || i > 0);
+            }
+            __syncwarp();
+            if (last) between();
+            if (tc::elect_lane()) {
+#pragma unroll
+                for (int i = kFirst; i < kWeightSteps; ++i) tc::mma_f16_ta_lo(d, p + i * 8, vd + i * (2048 >> 4), kIdescO, 1);
+                if (kFree) tc::mma_commit(GDN_BAR(kv_empty, at.stage));
+                if (last) tc::mma_commit(GDN_BAR(o_done, w));
             }
             __syncwarp();
             at.step(1);
+        }
+        return true;
+    }
+    // Looked at between other products: the next K, and the V of the unit left over (behind `skip` tiles of the ring).
+    __device__ __forceinline__ void look_k() { k_ready = seen(GDN_BAR(kv_full, next.stage), next.phase); }
+    __device__ __forceinline__ void look_v() {
+        if (any && take) v_ready = seen(GDN_BAR(kv_full, next.stage), next.phase);
+    }
+    // K of the next tile, which is then passed in the ring (and the V behind it, where that has been used).
+    __device__ __forceinline__ bool take_k(Place *k) {
+        if (!k_ready && !wait.all(GDN_BAR(kv_full, next.stage), next.phase)) return false;
+        k_ready = false;
+        *k = next;
+        next.step(Sh::kHalves);
+        if (early) next.step(Sh::kHalves);
+        early = false;
+        return true;
+    }
+    // The product held back, V from the ring where it is not at hand.
+    template <typename Between>
+    __device__ __forceinline__ bool use_left(Between between) {
+        if (take) {
+            v = next;
+            next.step(Sh::kHalves);
+        }
+        return weights<true>(v, between);
+    }
+    __device__ __forceinline__ void leave(uint32_t unit, bool starts, bool from_ring) {
+        any = true;
+        left = unit;
+        fresh = starts;
+        take = from_ring;
+        v_ready = !from_ring;
+    }
+    // An item of one row tile: unit g + t is key tile t.
+    __device__ __forceinline__ bool single(uint32_t g, int32_t tiles, uint32_t q, uint32_t q_bar) {
+        for (int32_t t = 0; t < tiles; ++t, ++g) {
+            const bool more = t + 1 < tiles;
+            Place k;
+            if (!take_k(&k) || !scores<true>(g, q, k, !more, q_bar, [&] { look_v(); })) return false;
+            if (any && !use_left([&] {
+                    if (more) look_k();
+                }))
+                return false;
+            leave(g, t < Sh::kStreams, true);
+        }
+        return true;
+    }
+    // An item of two row tiles: units g + 2t and g + 2t + 1 are key tile t.
+    __device__ __forceinline__ bool dual(uint32_t g, int32_t tiles, uint32_t q, uint32_t q_bar) {
+        for (int32_t t = 0; t < tiles; ++t, g += 2) {
+            const bool more = t + 1 < tiles;
+            Place k;
+            if (!take_k(&k) || !scores<false>(g, q, k, false, q_bar, [&] { look_v(); })) return false;
+            if (any && !use_left([] {})) return false;
+            leave(g, t == 0, true);
+            if (!scores<true>(g + 1, q + (Sh::kQTile >> 4), k, !more, q_bar, [&] { look_v(); })) return false;
+            v = next;
+            next.step(Sh::kHalves);
+            if (!weights<false>(v, [&] {
+                    if (more) look_k();
+                }))
+                return false;
+            leave(g + 1, t == 0, false);
         }
         return true;
     }
@@ -716,16 +827,17 @@ struct Issuer {
             const uint32_t s = n % kItems, slot = n_items & 1;
             // The product held back does not wait for what is late: the next item, its Q or its first K.  Its V lies
             // behind the place of that K.
-            if (any && !__all_sync(0xffffffffu, tc::mbar_test_wait(GDN_BAR(item_full, s), n / kItems & 1) &&
-                                                    tc::mbar_test_wait(GDN_BAR(q_full, slot), n_items >> 1 & 1) &&
-                                                    tc::mbar_test_wait(GDN_BAR(kv_full, next.stage), next.phase))) {
-                Place at = v;
-                early = take;
-                if (take) {
-                    at = next;
-                    at.step(Sh::kHalves);
+            if (any) {
+                k_ready = seen(GDN_BAR(kv_full, next.stage), next.phase);
+                if (!k_ready || !seen(GDN_BAR(item_full, s), n / kItems & 1) || !seen(GDN_BAR(q_full, slot), n_items >> 1 & 1)) {
+                    Place at = v;
+                    early = take;
+                    if (take) {
+                        at = next;
+                        at.step(Sh::kHalves);
+                    }
+                    if (!weights<true>(at, [] {})) break;
                 }
-                if (!weights(at)) break;
             }
             if (!wait.all(GDN_BAR(item_full, s), n / kItems & 1)) break;
             // (through a warp reduction: what the compiler knows to be uniform it keeps in uniform registers)
@@ -740,36 +852,9 @@ struct Issuer {
             const bool wide = Sh::kStreams == 2 ? two : !(few && tokens * L.group <= Sh::kSmallRows);
             if (!wait.all(GDN_BAR(q_full, slot), n_items >> 1 & 1)) break;
             const uint32_t q = tc::desc_lo(q_smem + (wide ? 0 : slot * Sh::kQSlot), 16);
-            const int32_t units = two ? 2 * tiles : tiles;
-            Place k = next;
-            int32_t u = 0;
-            for (; u < units; ++u, ++unit) {
-                const bool second = two && (u & 1);  // of a dual item's two units of a key tile
-                if (!second) {
-                    if (!wait.all(GDN_BAR(kv_full, next.stage), next.phase)) break;
-                    k = next;
-                }
-                if (!scores(unit, second ? q + (Sh::kQTile >> 4) : q, k, !two || second, u + 1 == units, GDN_BAR(q_empty, slot)))
-                    break;
-                if (!second) {
-                    next.step(Sh::kHalves);
-                    if (early) next.step(Sh::kHalves);
-                    early = false;
-                }
-                if (any) {
-                    if (take) {
-                        v = next;
-                        next.step(Sh::kHalves);
-                    }
-                    if (!weights(v)) break;
-                }
-                any = true;
-                left = unit;
-                fresh = u < Sh::kStreams;
-                take = !second;
-                last_use = !two || second;
-            }
-            if (u < units) break;
+            const uint32_t q_bar = GDN_BAR(q_empty, slot);
+            if (!(Sh::kStreams == 2 && two ? dual(unit, tiles, q, q_bar) : single(unit, tiles, q, q_bar))) break;
+            unit += two ? 2 * tiles : tiles;
             ++n_items;
         }
         if (tc::elect_lane()) tc::mma_commit(GDN_BAR(drain, 0));
@@ -1090,7 +1175,16 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attention_kernel(const 
         ctl->fail = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 3) tc::tmem_alloc(&ctl->tmem, kTmemCols);
+    if (warp == 3) {
+        if (lane == 0) {
+            tc::prefetch_tensor_map(&L.tm_k);
+            tc::prefetch_tensor_map(&L.tm_v);
+            tc::prefetch_tensor_map(&L.tm_q);
+            tc::prefetch_tensor_map(&L.tm_q_one);
+        }
+        __syncwarp();
+        tc::tmem_alloc(&ctl->tmem, kTmemCols);
+    }
     tc::fence_proxy_async_smem();
     tc::fence_before_sync();
     __syncthreads();
@@ -1134,53 +1228,112 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attention_kernel(const 
 // ---- joining the splits -----------------------------------------------------------------------
 
 constexpr int kJoinWarps = 4;
-constexpr int kJoinBlocksPerSm = 8;
+constexpr int kJoinBlocksPerSm = 16;
 
-// o = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s over a row's parts, in
-// their order; one warp per row, the rows dealt over a grid that fills the GPU
-// once.  Requests that were not split have no rows here.  Bound by the latency
-// of three dependent reads (rows, row, its partials) where there are few, by
-// L2 (the partials were just written) where there are many.
+// o = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s over a row's parts: a block
+// per row, warp k taking parts k, k + 4, ... in order, their four sums added in
+// order.  The rows are dealt over a grid that fills the GPU once; requests that
+// were not split have no rows here.  Bound by the latency of dependent reads
+// (the row, then all its partials at once) where there are few rows, by L2 or,
+// behind long contexts, by memory where there are many.
 template <int D, bool kHalf>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ AttentionLaunch L) {
-    const int lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(kJoinWarps * 32, kJoinBlocksPerSm / 2) join_kernel(const __grid_constant__ AttentionLaunch L) {
+    constexpr int kVec = D / 64;  // pairs of columns of a lane
+    constexpr int kBatch = 4;     // partials that a warp reads at once
+        constexpr int kMl = (kMaxSplits + 31) / 32;
+    __shared__ float2 sum[kJoinWarps - 1][D / 2];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t h_q = L.a.h_q;
     // Every thread waits for the attention kernel's end, also one with nothing to join: what follows this kernel in
     // the stream relies on both.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t rows = *L.ws.num_rows < L.ws.max_rows ? *L.ws.num_rows : L.ws.max_rows;
-    for (int64_t i = blockIdx.x * kJoinWarps + (threadIdx.x >> 5); i < rows; i += gridDim.x * kJoinWarps) {
-        const JoinRow row = L.ws.rows[i];
-        // (a call that timed out or was given overlapping token ranges leaves rows unwritten)
-        if (row.parts < 2 || row.parts > kMaxSplits + 1 || row.first < 0 ||
-            row.first + (row.parts - 1) * h_q >= L.ws.partials * h_q || row.out < 0 || row.out >= L.ws.max_rows)
-            continue;
+    // A block's rows, up to 32 at a time, one descriptor per lane: those that are in o already cost no round of their own.
+    const int64_t per = (rows + gridDim.x - 1) / gridDim.x, begin = blockIdx.x * per, end = begin + per < rows ? begin + per : rows;
+    for (int64_t i0 = begin; i0 < end; i0 += 32) {
+    JoinRow mine = {0, 0, 0};
+    if (i0 + lane < end) mine = L.ws.rows[i0 + lane];
+    // (a call that timed out or was given overlapping token ranges leaves rows unwritten)
+    uint32_t todo = __ballot_sync(0xffffffffu, mine.parts >= 2 && mine.parts <= kMaxSplits && mine.first >= 0 &&
+                                                   mine.first + (mine.parts - 1) * h_q < L.ws.partials * h_q &&
+                                                   mine.out >= 0 && mine.out < L.ws.max_rows);
+    for (; todo; todo &= todo - 1) {
+        const int src = __ffs(todo) - 1;
+        const JoinRow row = {__shfl_sync(0xffffffffu, mine.out, src), __shfl_sync(0xffffffffu, mine.parts, src),
+                             __shfl_sync(0xffffffffu, mine.first, src)};
+        float2 ml[kMl];
         float top = -INFINITY;
-        for (int32_t s = lane; s < row.parts; s += 32) top = fmaxf(top, L.ws.ml[row.first + s * h_q].x);
 #pragma unroll
-        for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        for (int k = 0; k < kMl; ++k) {
+            ml[k] = make_float2(-INFINITY, 0.f);
+            if (lane + 32 * k < row.parts) ml[k] = L.ws.ml[row.first + (lane + 32 * k) * h_q];
+            top = fmaxf(top, ml[k].x);
+        }
+        float2 acc[kVec];
+        float2 x[kBatch][kVec];
+        auto read = [&](int32_t s0) {
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j)
+                if (s0 + j * kJoinWarps < row.parts) {
+                    const float *o = L.ws.o + (row.first + (s0 + j * kJoinWarps) * h_q) * D + lane * 2;
+#pragma unroll
+                    for (int v = 0; v < kVec; ++v) x[j][v] = *reinterpret_cast<const float2 *>(o + v * 64);
+                }
+        };
+        read(warp);
+#pragma unroll
+        for (int v = 0; v < kVec; ++v) acc[v] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
         if (top == -INFINITY) top = 0.f;
-        constexpr int kVec = D / 64;  // pairs of columns of a lane
-        float acc[kVec][2] = {}, l = 0.f;
-#pragma unroll 8
-        for (int32_t s = 0; s < row.parts; ++s) {
-            const int64_t at = row.first + s * h_q;
-            const float2 ml = L.ws.ml[at];
-            const float w = ex2(ml.x - top);
-            l = fmaf(w, ml.y, l);
+        float l = 0.f;
 #pragma unroll
-            for (int v = 0; v < kVec; ++v) {
-                const float2 o = *reinterpret_cast<const float2 *>(L.ws.o + at * D + v * 64 + lane * 2);
-                acc[v][0] = fmaf(w, o.x, acc[v][0]);
-                acc[v][1] = fmaf(w, o.y, acc[v][1]);
+        for (int k = 0; k < kMl; ++k) {
+            ml[k].x = ex2(ml[k].x - top);  // the part's weight
+            l = fmaf(ml[k].x, ml[k].y, l);
+        }
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+        for (int32_t s0 = warp; s0 < row.parts; s0 += kBatch * kJoinWarps) {
+            if (s0 != warp) read(s0);
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const int32_t s = s0 + j * kJoinWarps;
+                float w = 0.f;
+#pragma unroll
+                for (int k = 0; k < kMl; ++k) {
+                    const float y = __shfl_sync(0xffffffffu, ml[k].x, s & 31);
+                    if (s >> 5 == k) w = y;
+                }
+                if (s < row.parts) {
+#pragma unroll
+                    for (int v = 0; v < kVec; ++v) {
+                        acc[v].x = fmaf(w, x[j][v].x, acc[v].x);
+                        acc[v].y = fmaf(w, x[j][v].y, acc[v].y);
+                    }
+                }
             }
         }
-        const bool none = l == 0.f;
-        const float f = none ? 0.f : 1.f / l;
-        uint16_t *out = L.a.o + static_cast<int64_t>(row.out) * D + lane * 2;
+        if (warp > 0)
 #pragma unroll
-        for (int v = 0; v < kVec; ++v)
-            *reinterpret_cast<uint32_t *>(out + v * 64) = none ? 0u : pack2<kHalf>(acc[v][0] * f, acc[v][1] * f);
+            for (int v = 0; v < kVec; ++v) sum[warp - 1][v * 32 + lane] = acc[v];
+        __syncthreads();
+        if (warp == 0) {
+            const bool none = l == 0.f;
+            const float f = none ? 0.f : 1.f / l;
+            uint16_t *out = L.a.o + static_cast<int64_t>(row.out) * D + lane * 2;
+#pragma unroll
+            for (int v = 0; v < kVec; ++v) {
+#pragma unroll
+                for (int k = 0; k < kJoinWarps - 1; ++k) {
+                    acc[v].x += sum[k][v * 32 + lane].x;
+                    acc[v].y += sum[k][v * 32 + lane].y;
+                }
+                *reinterpret_cast<uint32_t *>(out + v * 64) = none ? 0u : pack2<kHalf>(acc[v].x * f, acc[v].y * f);
+            }
+        }
+        __syncthreads();
+    }
     }
 }
 
@@ -1204,7 +1357,7 @@ cudaError_t launch_d(const AttentionLaunch &L, int64_t items, cudaStream_t strea
     attention_kernel<D, kHalf><<<blocks, Shape<D>::kThreads, Shape<D>::kSmem, stream>>>(L);
     e = cudaGetLastError();
     if (e != cudaSuccess || !L.ws.o) return e;
-    const int64_t joins = (L.a.num_tokens * L.a.h_q + kJoinWarps - 1) / kJoinWarps, most = int64_t{sms} * kJoinBlocksPerSm;
+    const int64_t joins = L.a.num_tokens * L.a.h_q, most = int64_t{sms} * kJoinBlocksPerSm;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(joins < most ? joins : most));
     cfg.blockDim = dim3(kJoinWarps * 32);

@@ -206,7 +206,7 @@ def test_another_stream_and_empty_calls(gdn):
 
 
 def test_long_contexts(gdn):
-    for h_q, h_kv, d, dtype in [(8, 1, 128, "fp16"), (4, 2, 256, "bf16"), (2, 2, 64, "bf16")]:
+    for h_q, h_kv, d, dtype in [(8, 1, 128, "fp16"), (4, 2, 256, "bf16"), (2, 2, 64, "bf16"), (80, 80, 64, "fp16")]:
         check(gdn, pu.make_case([(40000, 1), (70001, 2)], h_q, h_kv, d, dtype, page=16, seed=16))
 
 
