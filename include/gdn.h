@@ -474,10 +474,9 @@ gdn_status_t gdn_paged_kv_write(const gdn_paged_cache_t *cache, int64_t num_toke
  * gets zero outputs; one whose cu_seqlens run backwards or past num_tokens is
  * skipped.  A page id outside [0, num_pages) reads as zero keys
  * and values (GDN_DEV_BAD_SLOT).
- * Rows of the cache that no token of the request sees (the rest of its last
- * page, what the window has left behind) may hold anything, NaN included.
- * A NaN or infinity in a value that some token of the request sees reaches
- * that token's output and may reach those of the request's other new tokens.
+ * What a token does not see has no part in its output: rows of the cache past
+ * kv_len (the rest of the last page), behind the window, or of the request's
+ * later tokens may hold anything, NaN and infinities included.
  * A request's outputs depend on its own tokens, lengths and cache alone, bit
  * for bit: not on the batch, the pages it lies in, or the padding.
  */

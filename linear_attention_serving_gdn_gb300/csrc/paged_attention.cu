@@ -266,10 +266,11 @@ struct Control {
     uint64_t kv_full[Shape<D>::kStages], kv_empty[Shape<D>::kStages];
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2], p_full[2];
-    uint64_t o_done[2], o_free[2], ml_full[2];
+    uint64_t o_done[2], o_free[2], ml_full[2], scanned[2];
     uint64_t item_full[kItems], item_empty[kItems];
     uint64_t drain;
     Item items[kItems];
+    uint32_t dirty[2][2];  // per warpgroup: number of the last even or odd scan that found a NaN or infinity
     uint32_t tmem;
     int fail;
     // (m, l) of one warpgroup for the other; row r is only touched by the two threads of row r, in turn.
@@ -969,6 +970,96 @@ __device__ __forceinline__ void store32(void *p, const uint32_t *x) {
                  : "memory");
 }
 
+// Packed magnitudes: the larger of each half, NaN above all.
+template <bool kHalf>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    if (kHalf)
+        asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b & 0x7fff7fffu));
+    else
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b & 0x7fff7fffu));
+    return d;
+}
+template <bool kHalf>
+__device__ __forceinline__ uint32_t max_magnitude(uint32_t top, uint4 x) {
+    return max2<kHalf>(max2<kHalf>(max2<kHalf>(max2<kHalf>(top, x.x), x.y), x.z), x.w);
+}
+template <bool kHalf>
+__device__ __forceinline__ bool not_finite(uint32_t top) {
+    constexpr uint32_t kExp = kHalf ? 0x7c00u : 0x7f80u;
+    return (top & kExp) == kExp || (top >> 16 & kExp) == kExp;
+}
+
+template <bool kHalf>
+__device__ __forceinline__ float2 unpack2(uint32_t x) {
+    if (kHalf) return __half22float2(*reinterpret_cast<__half2 *>(&x));
+    return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+}
+
+// One row (token u of the item, query head) over the item's keys that it sees,
+// key after key by one warp: for items whose values hold a NaN or infinity
+// that not all of their tokens see.  part: the partial's row, or -1.
+template <int D, bool kHalf>
+__device__ __forceinline__ void exact_row(const AttentionLaunch &L, const Item &it, int32_t u, int64_t head, int64_t part,
+                                          int lane) {
+    const PagedAttentionArgs &a = L.a;
+    const gdn_paged_cache_t &c = a.cache;
+    constexpr int kPairs = D / 64;  // lane i: columns 2 i + 64 v
+    int32_t hi = it.pos + u + 1, lo = a.window > 0 && hi > a.window ? hi - a.window : 0;
+    if (hi > it.hi * kKeys) hi = it.hi * kKeys;
+    if (lo < it.lo * kKeys) lo = it.lo * kKeys;
+    const int64_t tok = static_cast<int64_t>(it.tok) + u;
+    float2 q[kPairs], o[kPairs];
+#pragma unroll
+    for (int v = 0; v < kPairs; ++v) {
+        q[v] = unpack2<kHalf>(*reinterpret_cast<const uint32_t *>(a.q + tok * a.q_token_stride + head * D + v * 64 + lane * 2));
+        o[v] = make_float2(0.f, 0.f);
+    }
+    float m = -INFINITY, l = 0.f;
+#pragma unroll 1
+    for (int32_t j = lo; j < hi; ++j) {
+        const int32_t idx = j / c.page_size, in = j - idx * c.page_size;
+        const int32_t page = a.block_table[it.req * a.table_stride + idx];
+        const bool good = page >= 0 && page < c.num_pages;  // a bad page reads as zeros (and has been reported)
+        const uint16_t *k = static_cast<const uint16_t *>(c.k) + page * c.k_page_stride + in * c.k_slot_stride +
+                            it.head * c.k_head_stride;
+        const uint16_t *val = static_cast<const uint16_t *>(c.v) + page * c.v_page_stride + in * c.v_slot_stride +
+                              it.head * c.v_head_stride;
+        float s = 0.f;
+        float2 x[kPairs];
+#pragma unroll
+        for (int v = 0; v < kPairs; ++v) {
+            const float2 y = unpack2<kHalf>(good ? *reinterpret_cast<const uint32_t *>(k + v * 64 + lane * 2) : 0u);
+            x[v] = unpack2<kHalf>(good ? *reinterpret_cast<const uint32_t *>(val + v * 64 + lane * 2) : 0u);
+            s = fmaf(q[v].y, y.y, fmaf(q[v].x, y.x, s));
+        }
+#pragma unroll
+        for (int i = 16; i > 0; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
+        s *= L.c;
+        const float top = fmaxf(m, s);
+        const float f = m == top ? 1.f : ex2(m - top), p = top == -INFINITY ? 0.f : ex2(s - top);
+        m = top;
+        l = fmaf(l, f, p);
+#pragma unroll
+        for (int v = 0; v < kPairs; ++v) {
+            o[v].x = fmaf(o[v].x, f, p * x[v].x);
+            o[v].y = fmaf(o[v].y, f, p * x[v].y);
+        }
+    }
+    if (part >= 0) {
+        if (lane == 0) L.ws.ml[part] = make_float2(m, l);
+#pragma unroll
+        for (int v = 0; v < kPairs; ++v) *reinterpret_cast<float2 *>(L.ws.o + part * D + v * 64 + lane * 2) = o[v];
+    } else {
+        const bool none = l == 0.f;
+        const float f = none ? 0.f : 1.f / l;
+#pragma unroll
+        for (int v = 0; v < kPairs; ++v)
+            *reinterpret_cast<uint32_t *>(a.o + (tok * a.h_q + head) * D + v * 64 + lane * 2) =
+                none ? 0u : pack2<kHalf>(o[v].x * f, o[v].y * f);
+    }
+}
+
 template <int D, bool kHalf>
 __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t *ring, uint32_t tmem, const Waiter &wait) {
     using Sh = Shape<D>;
@@ -983,7 +1074,7 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
     const float c = L.c;
     Ring pos;
     uint32_t unit0 = 0;              // first unit of the item
-    uint32_t ml_sent = 0, ml_got = 0;
+    uint32_t ml_got = 0, scans = 0;
     for (uint32_t n = 0;; ++n) {
         const uint32_t sl = n % kItems;
         if (!wait.all(ctl->item_full + sl, n / kItems & 1)) return;
@@ -1005,6 +1096,7 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
         visible_rows(it, a.window, &row_lo, &row_hi);
         const int32_t units = dual ? 2 * tiles : tiles;
         float m = -INFINITY, l = 0.f;
+        bool dirty = false;
         for (int32_t j = part; j < units; j += Sh::kStreams) {
             const uint32_t unit = unit0 + j, b = unit & 1;
             const int32_t t = dual ? j >> 1 : j;
@@ -1031,23 +1123,39 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
                 }
                 l += store_weights<kHalf>(t_s, x, c, m == -INFINITY ? 0.f : m * c);
             }
-            // Value rows that no token sees may hold anything (0 x NaN): zero them before the product.
-            if (k0 + kKeys > row_hi || k0 < row_lo) {
+            // A weight of zero does not keep a NaN or infinity out of the product.  Value rows that no token of the item
+            // sees are zeroed before it; where tokens see different keys of the tile, the rest is looked through, and an
+            // item that holds such a value is computed again, row by row (exact_rows).
+            const bool some = k0 + kKeys > row_hi || k0 < row_lo;
+            const bool differ = it.n > 1 && (k0 + kKeys > it.pos + 1 || (a.window > 0 && it.pos + it.n - k0 > a.window));
+            if (some || differ) {
                 const uint32_t at = pos.first + Sh::kHalves * pos.v_at(t, dual);
                 const bool dead = k0 + row >= row_hi || k0 + row < row_lo;
+                uint32_t top = 0;  // largest magnitudes of the row's even and odd columns
 #pragma unroll 1
                 for (uint32_t v = at; v < at + Sh::kHalves; ++v) {
                     // Two waits: a parity tells this fill from the one before only once that one has been consumed.
                     const uint32_t st = v % Sh::kStages, parity = v / Sh::kStages & 1;
                     if (!wait.all(ctl->kv_empty + st, parity ^ 1) || !wait.all(ctl->kv_full + st, parity)) return;
-                    if (dead) {
-#pragma unroll
-                        for (int p = 0; p < Sh::kPanels * 8; ++p)
-                            *reinterpret_cast<uint4 *>(ring + st * Sh::kStage + (p >> 3) * kPanel + row * 128 + (p & 7) * 16) =
-                                make_uint4(0, 0, 0, 0);
+                    uint4 *p = reinterpret_cast<uint4 *>(ring + st * Sh::kStage + row * 128);
+#pragma unroll 4
+                    for (int i = 0; i < Sh::kPanels * 8; ++i) {
+                        uint4 *x = p + (i >> 3) * (kPanel / 16) + ((i ^ row) & 7);  // (eight rows, eight banks)
+                        if (dead)
+                            *x = make_uint4(0, 0, 0, 0);
+                        else if (differ)
+                            top = max_magnitude<kHalf>(top, *x);
                     }
                 }
-                tc::fence_proxy_async_smem();
+                if (some) tc::fence_proxy_async_smem();
+                if (differ) {
+                    if (not_finite<kHalf>(top)) ctl->dirty[w][scans & 1] = scans + 1;
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(ctl->scanned + w);
+                    if (!wait.all(ctl->scanned + w, scans & 1)) return;
+                    dirty = dirty || ctl->dirty[w][scans & 1] == scans + 1;
+                    ++scans;
+                }
             }
             tc::fence_before_sync();
             __syncwarp();
@@ -1070,15 +1178,15 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
         float f0 = 1.f, f1 = 0.f;  // factors of this warpgroup's O and the other's
         bool writer = dual || part == 0;
         if (pair && part == 1) {
-            ctl->ml[Sh::kStreams == 2 ? row : 0] = make_float2(m, l);
+            ctl->ml[Sh::kStreams == 2 ? row : 0] = make_float2(dirty ? nanf("") : m, l);  // (m itself is never NaN)
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(ctl->ml_full + w);
-            ++ml_sent;
         } else if (pair) {
             if (!wait.all(ctl->ml_full + (w ^ 1), ml_got++ & 1)) return;
             tc::fence_after_sync();
             const float2 other = ctl->ml[Sh::kStreams == 2 ? row : 0];
+            dirty = __any_sync(0xffffffffu, dirty || isnan(other.x));
             const float top = fmaxf(m, other.x);
             if (top > -INFINITY) {
                 f0 = ex2((m - top) * c);
@@ -1100,13 +1208,19 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
                 const float inv = none ? 0.f : 1.f / l;
                 f0 *= inv;
                 f1 *= inv;
-            } else if (valid) {
+            } else if (valid && !dirty) {
                 L.ws.ml[prow] = make_float2(m * c, l);
             }
             uint16_t *out = a.o + ((static_cast<int64_t>(it.tok) + u) * a.h_q + head) * D;
             float *pout = L.ws.o + prow * D;
+            if (dirty) {
+                const int32_t count = rows - warp * 32 < 32 ? rows - warp * 32 : 32;
+                for (int r = 0; r < count; ++r)
+                    exact_row<D, kHalf>(L, it, __shfl_sync(0xffffffffu, u, r), __shfl_sync(0xffffffffu, head, r),
+                                        split ? __shfl_sync(0xffffffffu, prow, r) : -1, lane);
+            }
 #pragma unroll 1
-            for (int q = 0; q < D / 32; ++q) {
+            for (int q = 0; q < D / 32 && !dirty; ++q) {
                 uint32_t o[32];
                 tc::tmem_ld32(t_o + w * D + q * 32, o);
 #pragma unroll
@@ -1166,6 +1280,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attention_kernel(const 
             tc::mbar_init(ctl->o_done + i, 1);
             tc::mbar_init(ctl->o_free + i, 4);
             tc::mbar_init(ctl->ml_full + i, 4);
+            tc::mbar_init(ctl->scanned + i, 4);
+            ctl->dirty[i][0] = ctl->dirty[i][1] = 0;
         }
         for (int i = 0; i < kItems; ++i) {
             tc::mbar_init(ctl->item_full + i, 1);

@@ -93,7 +93,7 @@ def reference(c, window=0, scale=None):
             for h in range(h_q):
                 Q, Kh, Vh = q[t:t + m, h].double(), K[:, h * h_kv // h_q], V[:, h * h_kv // h_q]
                 s = torch.where(vis, Q @ Kh.T * scale, -torch.inf)
-                p = torch.nan_to_num(torch.softmax(s, -1), nan=0.0)
+                p = torch.where(vis.any(-1, keepdim=True), torch.softmax(s, -1), 0.0)  # no key: zeros
                 terms = torch.where(vis, Q.abs() @ Kh.abs().T * scale, 0.0).amax(-1, keepdim=True)
                 A = p @ Vh.abs()
                 o[t:t + m, h] = p @ Vh

@@ -81,6 +81,39 @@ def test_cache_rows_that_no_token_sees_may_hold_anything(gdn, d, junk):
     assert torch.isfinite(o).all()
 
 
+@pytest.mark.parametrize("h_q,h_kv,d,dtype", [(16, 2, 256, "bf16"), (8, 2, 128, "fp16"), (6, 2, 64, "bf16"), (3, 3, 64, "fp16"),
+                                              (2, 2, 256, "fp16")])
+@pytest.mark.parametrize("window", [0, 150])
+def test_what_a_token_does_not_see_has_no_part_in_it(gdn, h_q, h_kv, d, dtype, window):
+    """NaN and infinities in keys and values of the chunk's later tokens, and, with a window, of earlier ones."""
+    lens = [(300, 40), (1700, 9), (129, 129), (2600, 1), (700, 300)]
+    c = pu.make_case(lens, h_q, h_kv, d, dtype, page=16, seed=19)
+    bad = {0: [(280, "v", float("nan")), (299, "k", float("nan"))], 1: [(1697, "v", float("inf"))],
+           2: [(64, "v", float("-inf")), (128, "v", float("nan"))], 4: [(655, "v", float("nan")), (410, "v", float("inf"))]}
+    if window:
+        bad[0].append((115, "v", float("nan")))  # the first tokens' windows hold it, the last ones' do not
+    for r, where in bad.items():
+        for j, side, x in where:
+            page = c["table"][r, j // 16].long()
+            c[side][page, j % 16, :, 3] = x
+    o, st = pu.run_attention(gdn, c, window)
+    assert st == 0
+    t = 0
+    for r, (kv, m) in enumerate(lens):
+        for u in range(0, m, 1 if m < 50 else 7):
+            one = dict(c, q=c["q"][t + u:t + u + 1], table=c["table"][r:r + 1], lens=[(kv - m + u + 1, 1)])
+            ref, tol = pu.reference(one, window)
+            got = o[t + u].double()
+            finite = torch.isfinite(ref[0])
+            # a token that sees such a value shows it, the others come out as if it were not there
+            assert torch.equal(finite, torch.isfinite(got)), (r, u)
+            seen = [x for j, _, x in bad.get(r, []) if j <= kv - m + u and (not window or j > kv - m + u - window)]
+            assert bool(finite.all()) == (not seen)
+            if not seen:
+                pu.assert_close(got, ref[0], tol[0], f"request {r} token {u}")
+        t += m
+
+
 def test_pages_behind_the_window_are_not_looked_at(gdn):
     lens = [(1000, 1), (1000, 3)]
     c = pu.make_case(lens, 4, 2, 128, page=16, seed=7)
