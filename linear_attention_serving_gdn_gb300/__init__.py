@@ -531,10 +531,29 @@ def gdn_mixed_step_colaunch(num_decodes: int, q, k, v, g, beta, cu_seqlens_p, cu
 # ---------------------------------------------------------------------------
 
 _PAGED_DTYPES = {torch.bfloat16: GDN_BF16, torch.float16: GDN_FP16}
+_Tensor, _i32 = torch.Tensor, torch.int32
+
+
+# These calls' device work takes microseconds, so the checks of a good call are
+# one expression each and give the pointer at once; the slow way names what is
+# wrong.
+def _i32_vec(t, name):
+    if t.__class__ is _Tensor and t.dtype is _i32 and t.is_cuda and t.dim() == 1 and t.is_contiguous():
+        return t.data_ptr()
+    return _dev(t, name, _i32, 1).data_ptr()
+
+
+def _i32_word(t, name):
+    return None if t is None else _dev(t, name, _i32).data_ptr()
 
 
 def _strided(t, name, dtype, ndim):
-    """A CUDA tensor whose last dimension is contiguous; its other strides are free."""
+    """A CUDA tensor whose last dimension is contiguous; its other strides are
+    free.  Gives its strides."""
+    if t.__class__ is _Tensor and t.is_cuda and t.dtype is dtype and t.dim() == ndim:
+        st = t.stride()
+        if st[-1] == 1:
+            return st
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -545,25 +564,29 @@ def _strided(t, name, dtype, ndim):
         raise ValueError(f"{name} must have {ndim} dims, got {tuple(t.shape)}")
     if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    return t
+    return t.stride()
 
 
 def _paged_cache(k_cache, v_cache):
+    """The C description of a cache, and its shape."""
     dtype = getattr(k_cache, "dtype", None)
-    if dtype not in _PAGED_DTYPES:
+    code = _PAGED_DTYPES.get(dtype)
+    if code is None:
         raise TypeError(f"k_cache must be bfloat16 or float16, got {dtype}")
-    _strided(k_cache, "k_cache", dtype, 4), _strided(v_cache, "v_cache", dtype, 4)
-    if v_cache.shape != k_cache.shape:
+    ks, vs = _strided(k_cache, "k_cache", dtype, 4), _strided(v_cache, "v_cache", dtype, 4)
+    shape = k_cache.shape
+    if v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must have the same shape")
-    pages, page_size, h_kv, d = k_cache.shape
-    return PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), _PAGED_DTYPES[dtype], page_size, h_kv, d, pages,
-                      *k_cache.stride()[:3], *v_cache.stride()[:3])
+    pages, page_size, h_kv, d = shape
+    return PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), code, page_size, h_kv, d, pages,
+                      ks[0], ks[1], ks[2], vs[0], vs[1], vs[2]), shape
 
 
 def _block_table(t):
-    """The checked table and its row stride (one row's stride says nothing: its width stands for it)."""
-    t = _strided(t, "block_table", torch.int32, 2)
-    return t, t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    """Pointer, rows, width and row stride (one row's stride says nothing: its width stands for it)."""
+    st = _strided(t, "block_table", _i32, 2)
+    rows, width = t.shape
+    return t.data_ptr(), rows, width, st[0] if rows > 1 else width
 
 
 def gdn_paged_maps(context_lens, new_lens, block_table, page_size: int, num_pages: int, cu_seqlens, kv_lens,
@@ -573,43 +596,41 @@ def gdn_paged_maps(context_lens, new_lens, block_table, page_size: int, num_page
     ``block_table`` (in place), ``cu_seqlens``, ``kv_lens``, and the slot and
     position of every new token (see gdn.h).  ``free_head_out`` defaults to
     ``free_head``, which then advances in place."""
-    lib = load_library()
-    i32 = torch.int32
-    context_lens, new_lens = _dev(context_lens, "context_lens", i32, 1), _dev(new_lens, "new_lens", i32, 1)
-    block_table, table_stride = _block_table(block_table)
-    cu_seqlens, kv_lens = _dev(cu_seqlens, "cu_seqlens", i32, 1), _dev(kv_lens, "kv_lens", i32, 1)
-    slot_map, positions = _dev(slot_map, "slot_map", i32, 1), _dev(positions, "positions", i32, 1)
-    free_pages = _dev(free_pages, "free_pages", i32, 1, optional=True)
-    free_head = _dev(free_head, "free_head", i32, optional=free_pages is None)
-    free_head_out = free_head if free_head_out is None else _dev(free_head_out, "free_head_out", i32)
-    dev_status = _dev(dev_status, "dev_status", i32, optional=True)
-    n = context_lens.shape[0]
-    if not (new_lens.shape[0] == n and block_table.shape[0] == n and cu_seqlens.shape[0] == n + 1
-            and kv_lens.shape[0] == n and positions.shape == slot_map.shape):
+    lib = _lib or load_library()
+    ctx, new = _i32_vec(context_lens, "context_lens"), _i32_vec(new_lens, "new_lens")
+    table, rows, width, table_stride = _block_table(block_table)
+    cu, kv = _i32_vec(cu_seqlens, "cu_seqlens"), _i32_vec(kv_lens, "kv_lens")
+    slots, pos = _i32_vec(slot_map, "slot_map"), _i32_vec(positions, "positions")
+    n, capacity = context_lens.numel(), slot_map.numel()
+    if not (new_lens.numel() == n and rows == n and cu_seqlens.numel() == n + 1 and kv_lens.numel() == n
+            and positions.numel() == capacity):
         raise ValueError("inconsistent paged-maps shapes")
-    # an empty list serves no page, unlike no list at all: any non-null pointer stands for it
-    pages = None if free_pages is None else (free_pages.data_ptr() or cu_seqlens.data_ptr())
-    _check(lib.gdn_paged_maps(n, int(page_size), int(num_pages), _ptr(context_lens), _ptr(new_lens),
-                              _ptr(block_table), block_table.shape[1], table_stride,
-                              pages, 0 if free_pages is None else free_pages.shape[0], _ptr(free_head),
-                              _ptr(free_head_out), _ptr(cu_seqlens), _ptr(kv_lens), slot_map.shape[0],
-                              _ptr(slot_map), _ptr(positions), _ptr(dev_status), _stream(stream)),
-           "gdn_paged_maps")
+    pages = head = head_out = None
+    num_free = 0
+    if free_pages is not None:
+        num_free = free_pages.numel()
+        # an empty list serves no page, unlike no list at all: any non-null pointer stands for it
+        pages = _i32_vec(free_pages, "free_pages") or cu
+        head = _dev(free_head, "free_head", _i32).data_ptr()
+        head_out = head if free_head_out is None else _dev(free_head_out, "free_head_out", _i32).data_ptr()
+    _check(lib.gdn_paged_maps(n, page_size, num_pages, ctx, new, table, width, table_stride, pages, num_free, head,
+                              head_out, cu, kv, capacity, slots, pos, _i32_word(dev_status, "dev_status"),
+                              _stream(stream)), "gdn_paged_maps")
 
 
 def gdn_paged_kv_write(k, v, k_cache, v_cache, slot_map, dev_status=None, stream=None) -> None:
     """Rows of ``k`` and ``v`` ([T][h_kv][d]) into the caches' slots
     ``slot_map`` (see gdn.h).  The caches are viewed as
     [pages][page_size][h_kv][d]; any strides with a contiguous last dimension."""
-    lib = load_library()
-    cache = _paged_cache(k_cache, v_cache)
-    k, v = _strided(k, "k", k_cache.dtype, 3), _strided(v, "v", k_cache.dtype, 3)
-    slot_map = _dev(slot_map, "slot_map", torch.int32, 1)
-    dev_status = _dev(dev_status, "dev_status", torch.int32, optional=True)
-    if not (k.shape == v.shape and k.shape[1:] == k_cache.shape[2:] and slot_map.shape[0] == k.shape[0]):
+    lib = _lib or load_library()
+    cache, shape = _paged_cache(k_cache, v_cache)
+    ks, vs = _strided(k, "k", k_cache.dtype, 3), _strided(v, "v", k_cache.dtype, 3)
+    slots = _i32_vec(slot_map, "slot_map")
+    T, h_kv, d = rows = k.shape
+    if not (rows == v.shape and h_kv == shape[2] and d == shape[3] and slot_map.numel() == T):
         raise ValueError("inconsistent K/V write shapes")
-    _check(lib.gdn_paged_kv_write(ctypes.byref(cache), k.shape[0], _ptr(k), k.stride(0), k.stride(1), _ptr(v),
-                                  v.stride(0), v.stride(1), _ptr(slot_map), _ptr(dev_status), _stream(stream)),
+    _check(lib.gdn_paged_kv_write(ctypes.byref(cache), T, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
+                                  slots, _i32_word(dev_status, "dev_status"), _stream(stream)),
            "gdn_paged_kv_write")
 
 
@@ -630,27 +651,25 @@ def gdn_paged_attention(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, o
     dense; ``scale`` defaults to d ** -0.5; ``max_kv_len`` bounds ``kv_lens``
     (0: what the block table can hold); ``workspace`` is a uint8 tensor of
     ``gdn_paged_attention_workspace_bytes`` for that bound."""
-    lib = load_library()
-    i32 = torch.int32
-    cache = _paged_cache(k_cache, v_cache)
-    q = _strided(q, "q", k_cache.dtype, 3)
+    lib = _lib or load_library()
+    cache, shape = _paged_cache(k_cache, v_cache)
+    qs = _strided(q, "q", k_cache.dtype, 3)
     o = _dev(o, "o", k_cache.dtype, 3)
-    block_table, table_stride = _block_table(block_table)
-    cu_seqlens, kv_lens = _dev(cu_seqlens, "cu_seqlens", i32, 1), _dev(kv_lens, "kv_lens", i32, 1)
-    workspace = _dev(workspace, "workspace", torch.uint8, optional=True)
-    dev_status = _dev(dev_status, "dev_status", i32, optional=True)
+    table, rows, width, table_stride = _block_table(block_table)
+    cu, kv = _i32_vec(cu_seqlens, "cu_seqlens"), _i32_vec(kv_lens, "kv_lens")
     T, h_q, d = q.shape
-    n = kv_lens.shape[0]
-    if not (o.shape == q.shape and d == cache.d and cu_seqlens.shape[0] == n + 1 and block_table.shape[0] == n):
+    n = kv_lens.numel()
+    if not (o.shape == q.shape and d == shape[3] and cu_seqlens.numel() == n + 1 and rows == n):
         raise ValueError("inconsistent paged-attention shapes")
-    if q.stride(1) != d and h_q > 1:
+    if qs[1] != d and h_q > 1:
         raise ValueError("q's heads must be adjacent")
-    _check(lib.gdn_paged_attention(ctypes.byref(cache), n, T, h_q, d ** -0.5 if scale is None else scale,
-                                   int(window), int(max_kv_len), _ptr(q), q.stride(0), _ptr(block_table),
-                                   block_table.shape[1], table_stride,
-                                   _ptr(cu_seqlens), _ptr(kv_lens), _ptr(o), _ptr(workspace),
-                                   0 if workspace is None else workspace.numel(), _ptr(dev_status),
-                                   _stream(stream)),
+    ws = ws_bytes = 0
+    if workspace is not None:
+        workspace = _dev(workspace, "workspace", torch.uint8)
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel()
+    _check(lib.gdn_paged_attention(ctypes.byref(cache), n, T, h_q, d ** -0.5 if scale is None else scale, window,
+                                   max_kv_len, q.data_ptr(), qs[0], table, width, table_stride, cu, kv, o.data_ptr(),
+                                   ws, ws_bytes, _i32_word(dev_status, "dev_status"), _stream(stream)),
            "gdn_paged_attention")
 
 

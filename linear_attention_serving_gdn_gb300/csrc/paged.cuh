@@ -19,6 +19,7 @@ struct PagedMapsArgs {
     int32_t *cu_seqlens, *kv_lens;
     int64_t token_capacity;
     int32_t *slot_map, *positions;
+    bool aligned;  // slot_map and positions start at 16-byte boundaries
     int32_t *dev_status;
 };
 

@@ -9,6 +9,7 @@ namespace {
 
 constexpr int64_t kMaxStride = int64_t{1} << 39;  // elements: a tensor map's strides are under 2^40 bytes
 constexpr int64_t kMaxKeys = int64_t{1} << 30;    // keys of a request: key indices stay inside int32
+constexpr int32_t kMaxHeads = 65536;              // K/V heads: pieces of a token stay inside int32
 constexpr int32_t kMaxGroup = 128;  // query heads per K/V head: one token's heads fit a 128-row tile
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -27,7 +28,7 @@ gdn_status_t cache_ok(const gdn_paged_cache_t *in, gdn_paged_cache_t *c) {
     if (c->h_kv <= 0 || c->d <= 0 || c->page_size <= 0 || c->num_pages <= 0) return GDN_ERR_INVALID_ARG;
     if (c->dtype != GDN_BF16 && c->dtype != GDN_FP16) return GDN_ERR_UNSUPPORTED;
     if (c->d != 64 && c->d != 128 && c->d != 256) return GDN_ERR_UNSUPPORTED;
-    if (c->page_size % 16 != 0) return GDN_ERR_UNSUPPORTED;
+    if (c->page_size % 16 != 0 || c->h_kv > kMaxHeads) return GDN_ERR_UNSUPPORTED;
     if (c->num_pages > INT_MAX / c->page_size) return GDN_ERR_UNSUPPORTED;
     if (!c->k || !c->v) return GDN_ERR_INVALID_ARG;
     if (!aligned16(c->k) || !aligned16(c->v)) return GDN_ERR_INVALID_ARG;

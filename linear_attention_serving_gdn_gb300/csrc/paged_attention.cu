@@ -315,11 +315,15 @@ constexpr long long kDrainCycles = 2000000000LL;
 // block reports it at its end).
 struct Waiter {
     volatile int *fail;
+    // (try_wait suspends the thread for some microseconds by itself: a shorter limit asks without that)
+    static __device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity) {
+        return kWaitCycles < 10000 ? tc::mbar_test_wait(bar, parity) : tc::mbar_try_wait(bar, parity);
+    }
     // bar: shared-memory address
     __device__ __forceinline__ bool at(uint32_t bar, uint32_t parity) const {
-        if (tc::mbar_try_wait(bar, parity)) return true;
+        if (poll(bar, parity)) return true;
         const long long start = clock64();
-        while (!tc::mbar_try_wait(bar, parity)) {
+        while (!poll(bar, parity)) {
             if (*fail) return false;
             if (clock64() - start > kWaitCycles) {
                 *fail = 1;
