@@ -244,7 +244,7 @@ struct Item {
 template <int D>
 struct Shape {
     static constexpr int kStreams = streams_of(D);
-    static constexpr int kThreads = 128 + 128 * kStreams;
+    static constexpr int kThreads = 384;
     static constexpr int kCols = D < 128 ? D : 128;  // columns of a stage
     static constexpr int kHalves = D / kCols;        // stages of a K or V tile
     static constexpr int kPanels = kCols / 64;
@@ -266,7 +266,7 @@ struct Control {
     uint64_t kv_full[Shape<D>::kStages], kv_empty[Shape<D>::kStages];
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2], p_full[2];
-    uint64_t o_done[2], o_free[2], ml_full[2], scanned[2];
+    uint64_t o_done[2], o_free[2], ml_full[2], ml_empty, item_done, scanned[2];
     uint64_t item_full[kItems], item_empty[kItems];
     uint64_t drain;
     Item items[kItems];
@@ -274,7 +274,7 @@ struct Control {
     uint32_t tmem;
     int fail;
     // (m, l) of one warpgroup for the other; row r is only touched by the two threads of row r, in turn.
-    float2 ml[Shape<D>::kStreams == 2 ? kRows : 1];
+    float2 ml[kRows];
 };
 
 // Units.  The work of an item is a sequence of units, each one S = Q K^T and
@@ -679,9 +679,9 @@ struct Issuer {
     Place next;     // of the next first use
     uint32_t used;  // per O: parity of the items that used it
     // The unit whose product with P is still to be issued: its number, whether it starts O, whether its V is the next
-    // in the ring (else it is at `v`, loaded).
+    // in the ring (else it is at `v`, loaded), whether it is its item's last.
     uint32_t left;
-    bool any, fresh, take;
+    bool any, fresh, take, final;
     Place v;
     bool early;    // the V behind the next K has been used already
     bool k_ready;  // the next K has been seen to be there
@@ -755,6 +755,7 @@ struct Issuer {
                 for (int i = kFirst; i < kWeightSteps; ++i) tc::mma_f16_ta_lo(d, p + i * 8, vd + i * (2048 >> 4), kIdescO, 1);
                 if (kFree) tc::mma_commit(GDN_BAR(kv_empty, at.stage));
                 if (last) tc::mma_commit(GDN_BAR(o_done, w));
+                if (Sh::kStreams == 1 && last && final) tc::mma_commit(GDN_BAR(item_done, 0));
             }
             __syncwarp();
             at.step(1);
@@ -785,8 +786,9 @@ struct Issuer {
         }
         return weights<true>(v, between);
     }
-    __device__ __forceinline__ void leave(uint32_t unit, bool starts, bool from_ring) {
+    __device__ __forceinline__ void leave(uint32_t unit, bool starts, bool from_ring, bool ends) {
         any = true;
+        final = ends;
         left = unit;
         fresh = starts;
         take = from_ring;
@@ -802,7 +804,7 @@ struct Issuer {
                     if (more) look_k();
                 }))
                 return false;
-            leave(g, t < Sh::kStreams, true);
+            leave(g, t < Sh::kStreams, true, !more);
         }
         return true;
     }
@@ -813,7 +815,7 @@ struct Issuer {
             Place k;
             if (!take_k(&k) || !scores<false>(g, q, k, false, q_bar, [&] { look_v(); })) return false;
             if (any && !use_left([] {})) return false;
-            leave(g, t == 0, true);
+            leave(g, t == 0, true, false);
             if (!scores<true>(g + 1, q + (Sh::kQTile >> 4), k, !more, q_bar, [&] { look_v(); })) return false;
             v = next;
             next.step(Sh::kHalves);
@@ -821,7 +823,7 @@ struct Issuer {
                     if (more) look_k();
                 }))
                 return false;
-            leave(g + 1, t == 0, false);
+            leave(g + 1, t == 0, false, !more);
         }
         return true;
     }
@@ -1064,12 +1066,24 @@ __device__ __forceinline__ void exact_row(const AttentionLaunch &L, const Item &
     }
 }
 
+// f(byte offset) for each 16-byte piece of rows [r0, r1) of a V stage, dealt over the warpgroup's threads.
+template <int D, typename F>
+__device__ __forceinline__ void value_rows(int32_t r0, int32_t r1, int32_t thread, F f) {
+    constexpr int kPieces = Shape<D>::kPanels * 8;
+    if (r0 < 0) r0 = 0;
+    if (r1 > kKeys) r1 = kKeys;
+#pragma unroll 1
+    for (int32_t i = r0 * kPieces + thread; i < r1 * kPieces; i += 128)
+        f((i % kPieces / 8) * kPanel + i / kPieces * 128 + i % 8 * 16);
+}
+
 template <int D, bool kHalf>
 __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t *ring, uint32_t tmem, const Waiter &wait) {
     using Sh = Shape<D>;
     const PagedAttentionArgs &a = L.a;
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
-    const uint32_t w = Sh::kStreams == 2 ? (threadIdx.x >> 7) - 1 : 0;  // warpgroup = buffer = O, with two streams
+    const uint32_t group = (threadIdx.x >> 7) - 1;
+    const uint32_t w = Sh::kStreams == 2 ? group : 0;  // warpgroup = buffer = O, with two streams
     const int row = warp * 32 + lane;
     const int32_t u_tile = row / L.group, g = row - u_tile * L.group;
     const int32_t tile_tokens = kRows / L.group;
@@ -1078,7 +1092,7 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
     const float c = L.c;
     Ring pos;
     uint32_t unit0 = 0;              // first unit of the item
-    uint32_t ml_got = 0, scans = 0;
+    uint32_t n_items = 0, ml_got = 0, scans = 0;
     for (uint32_t n = 0;; ++n) {
         const uint32_t sl = n % kItems;
         if (!wait.all(ctl->item_full + sl, n / kItems & 1)) return;
@@ -1101,7 +1115,8 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
         const int32_t units = dual ? 2 * tiles : tiles;
         float m = -INFINITY, l = 0.f;
         bool dirty = false;
-        for (int32_t j = part; j < units; j += Sh::kStreams) {
+        // (with one stream the second warpgroup writes an item's O while the first one is on with the next)
+        for (int32_t j = part; j < units && (Sh::kStreams == 2 || group == 0); j += Sh::kStreams) {
             const uint32_t unit = unit0 + j, b = unit & 1;
             const int32_t t = dual ? j >> 1 : j;
             const int32_t k0 = (it.lo + t) * kKeys;
@@ -1134,21 +1149,23 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
             const bool differ = it.n > 1 && (k0 + kKeys > it.pos + 1 || (a.window > 0 && it.pos + it.n - k0 > a.window));
             if (some || differ) {
                 const uint32_t at = pos.first + Sh::kHalves * pos.v_at(t, dual);
-                const bool dead = k0 + row >= row_hi || k0 + row < row_lo;
-                uint32_t top = 0;  // largest magnitudes of the row's even and odd columns
+                uint32_t top = 0;  // largest magnitudes seen
 #pragma unroll 1
                 for (uint32_t v = at; v < at + Sh::kHalves; ++v) {
                     // Two waits: a parity tells this fill from the one before only once that one has been consumed.
                     const uint32_t st = v % Sh::kStages, parity = v / Sh::kStages & 1;
                     if (!wait.all(ctl->kv_empty + st, parity ^ 1) || !wait.all(ctl->kv_full + st, parity)) return;
-                    uint4 *p = reinterpret_cast<uint4 *>(ring + st * Sh::kStage + row * 128);
-#pragma unroll 4
-                    for (int i = 0; i < Sh::kPanels * 8; ++i) {
-                        uint4 *x = p + (i >> 3) * (kPanel / 16) + ((i ^ row) & 7);  // (eight rows, eight banks)
-                        if (dead)
-                            *x = make_uint4(0, 0, 0, 0);
-                        else if (differ)
-                            top = max_magnitude<kHalf>(top, *x);
+                    uint8_t *tile = ring + st * Sh::kStage;
+                    if (some) {
+                        value_rows<D>(row_hi - k0, kKeys, row, [&](uint32_t x) { *reinterpret_cast<uint4 *>(tile + x) = make_uint4(0, 0, 0, 0); });
+                        value_rows<D>(0, row_lo - k0, row, [&](uint32_t x) { *reinterpret_cast<uint4 *>(tile + x) = make_uint4(0, 0, 0, 0); });
+                    }
+                    if (differ) {  // past the first token, and behind the last one's window
+                        const int32_t past = a.window > 0 ? it.pos + it.n - a.window - k0 : 0;
+                        value_rows<D>(it.pos + 1 - k0, row_hi - k0, row,
+                                      [&](uint32_t x) { top = max_magnitude<kHalf>(top, *reinterpret_cast<uint4 *>(tile + x)); });
+                        value_rows<D>(row_lo - k0, past, row,
+                                      [&](uint32_t x) { top = max_magnitude<kHalf>(top, *reinterpret_cast<uint4 *>(tile + x)); });
                     }
                 }
                 if (some) tc::fence_proxy_async_smem();
@@ -1167,29 +1184,37 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
         }
         // O to memory: the result, or this split's part of it.
         const bool pair = Sh::kStreams == 2 && !dual && tiles > 1;  // two warpgroups hold one row tile's parts
-        if (dual || part < tiles) {
-            if (Sh::kStreams == 2) {
-                const uint32_t last = unit0 + units - 1 - ((units - 1 - part) & 1);
-                if (!wait.all(ctl->o_done + w, last >> 1 & 1)) return;
-            } else {
-                // The last two products in turn: S of the last unit only told that the third-last is done, and a
-                // parity tells two phases apart.
-                if (tiles > 1 && !wait.all(ctl->o_done, (unit0 + units) & 1)) return;
-                if (!wait.all(ctl->o_done, (unit0 + units - 1) & 1)) return;
-            }
+        if (Sh::kStreams == 1 && group == 0) {
+            if (!wait.all(&ctl->ml_empty, (n_items & 1) ^ 1)) return;
+            ctl->ml[row] = make_float2(dirty ? nanf("") : m, l);  // (m itself is never NaN)
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(ctl->ml_full);
+        } else if (Sh::kStreams == 1) {
+            if (!wait.all(ctl->ml_full, n_items & 1)) return;
+            m = ctl->ml[row].x;
+            l = ctl->ml[row].y;
+            dirty = __any_sync(0xffffffffu, isnan(m));
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&ctl->ml_empty);
+            if (!wait.all(&ctl->item_done, n_items & 1)) return;
+            tc::fence_after_sync();
+        } else if (dual || part < tiles) {
+            const uint32_t last = unit0 + units - 1 - ((units - 1 - part) & 1);
+            if (!wait.all(ctl->o_done + w, last >> 1 & 1)) return;
             tc::fence_after_sync();
         }
+        ++n_items;
         float f0 = 1.f, f1 = 0.f;  // factors of this warpgroup's O and the other's
-        bool writer = dual || part == 0;
+        const bool writer = Sh::kStreams == 2 ? dual || part == 0 : group == 1;
         if (pair && part == 1) {
-            ctl->ml[Sh::kStreams == 2 ? row : 0] = make_float2(dirty ? nanf("") : m, l);  // (m itself is never NaN)
+            ctl->ml[row] = make_float2(dirty ? nanf("") : m, l);
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(ctl->ml_full + w);
         } else if (pair) {
             if (!wait.all(ctl->ml_full + (w ^ 1), ml_got++ & 1)) return;
             tc::fence_after_sync();
-            const float2 other = ctl->ml[Sh::kStreams == 2 ? row : 0];
+            const float2 other = ctl->ml[row];
             dirty = __any_sync(0xffffffffu, dirty || isnan(other.x));
             const float top = fmaxf(m, other.x);
             if (top > -INFINITY) {
@@ -1289,8 +1314,10 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attention_kernel(const 
         }
         for (int i = 0; i < kItems; ++i) {
             tc::mbar_init(ctl->item_full + i, 1);
-            tc::mbar_init(ctl->item_empty + i, 3 + 4 * Sh::kStreams);  // two load warps, MMA, softmax warps
+            tc::mbar_init(ctl->item_empty + i, 3 + 8);  // two load warps, MMA, softmax warps
         }
+        tc::mbar_init(&ctl->ml_empty, 4);
+        tc::mbar_init(&ctl->item_done, 1);
         tc::mbar_init(&ctl->drain, 1);
         ctl->fail = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -1313,7 +1340,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attention_kernel(const 
     const Waiter wait = {&ctl->fail};
     // 384 threads are launched with 168 registers each: 128 x 72 + 256 x 216 is the same sum.
     if (warp < 4) {
-        if (Sh::kStreams == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == 0) {
             load_tiles<D, true>(L, ctl, tc::smem_u32(base), tc::smem_u32(ring), wait);
         } else if (warp == 1) {
@@ -1331,7 +1358,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attention_kernel(const 
             load_tiles<D, false>(L, ctl, tc::smem_u32(base), tc::smem_u32(ring), wait);
         }
     } else {
-        if (Sh::kStreams == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         softmax_rows<D, kHalf>(L, ctl, ring, tmem, wait);
     }
     __syncwarp();
