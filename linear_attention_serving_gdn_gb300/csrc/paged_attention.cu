@@ -46,7 +46,7 @@
 #include <stddef.h>
 
 #ifndef GDN_WAIT_CYCLES
-#define GDN_WAIT_CYCLES 2000000000LL
+#define GDN_WAIT_CYCLES 2000000000LL  // about a second; under 2^32
 #endif
 
 namespace gdn {
@@ -91,6 +91,7 @@ constexpr int kMaxSplitTiles = 16;  // of few rows, while kMaxSplits allow: long
 // kernel as the others do, so their number grows with the root of the keys.
 __host__ __device__ __forceinline__ int32_t least_split_tiles(int32_t tiles, int32_t rows) {
     int32_t n = rows / 8 > kMinSplitTiles ? rows / 8 : kMinSplitTiles;
+#pragma unroll 1
     while (n * n * 2 < tiles) ++n;
     return n;
 }
@@ -307,39 +308,36 @@ struct Ring {
     }
 };
 
-constexpr long long kWaitCycles = GDN_WAIT_CYCLES;
+constexpr uint32_t kWaitCycles = GDN_WAIT_CYCLES;
 constexpr long long kDrainCycles = 2000000000LL;
 
-// Bounded wait for the phase of `bar` with the given parity; gives up as soon
-// as any thread has flagged a failure, and flags one when it runs out (the
-// block reports it at its end).
+// Bounded wait of a whole warp for the phase of `bar` with the given parity:
+// true for all lanes or for none.  Gives up as soon as any thread has flagged a
+// failure, and flags one when it runs out (the block reports it at its end).
 struct Waiter {
     volatile int *fail;
     // (try_wait suspends the thread for some microseconds by itself: a shorter limit asks without that)
     static __device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity) {
-        return kWaitCycles < 10000 ? tc::mbar_test_wait(bar, parity) : tc::mbar_try_wait(bar, parity);
+        return __all_sync(0xffffffffu,
+                          kWaitCycles < 10000 ? tc::mbar_test_wait(bar, parity) : tc::mbar_try_wait(bar, parity));
     }
-    // bar: shared-memory address
-    __device__ __forceinline__ bool at(uint32_t bar, uint32_t parity) const {
+    __device__ __forceinline__ bool all(uint32_t bar, uint32_t parity) const {  // bar: shared-memory address
         if (poll(bar, parity)) return true;
-        const long long start = clock64();
-        while (!poll(bar, parity)) {
-            if (*fail) return false;
-            if (clock64() - start > kWaitCycles) {
+        const uint32_t start = static_cast<uint32_t>(clock());
+#pragma unroll 1
+        do {
+            if (__any_sync(0xffffffffu, *fail || static_cast<uint32_t>(clock()) - start > kWaitCycles)) {
                 *fail = 1;
                 return false;
             }
-        }
+        } while (!poll(bar, parity));
         return true;
-    }
-    // For a whole warp: true for all lanes or for none.
-    __device__ __forceinline__ bool all(uint32_t bar, uint32_t parity) const {
-        return __all_sync(0xffffffffu, at(bar, parity));
     }
     __device__ __forceinline__ bool all(uint64_t *bar, uint32_t parity) const { return all(tc::smem_u32(bar), parity); }
 };
 __device__ __forceinline__ void drain_bar(uint64_t *bar, uint32_t parity) {
     const long long start = clock64();
+#pragma unroll 1
     while (!tc::mbar_try_wait(bar, parity))
         if (clock64() - start > kDrainCycles) return;
 }
@@ -382,6 +380,7 @@ template <int D>
 __device__ __forceinline__ void zero_rows(const AttentionLaunch &L, const Item &it, int lane) {
     const PagedAttentionArgs &a = L.a;
     const int32_t pieces = L.group * (D / 8);
+#pragma unroll 1
     for (int32_t i = lane; i < it.n * pieces; i += 32) {
         const int32_t u = i / pieces, k = i - u * pieces;
         uint16_t *out = a.o + ((static_cast<int64_t>(it.tok) + u) * a.h_q + it.head * L.group) * D;
@@ -408,6 +407,7 @@ __device__ void schedule(const AttentionLaunch &L, Control<D> *ctl, const Waiter
             ++begun;
         };
         if (n >= kItems && begun == n - kItems) pass();
+#pragma unroll 1
         while (ahead > kAheadTiles) {
             if (!wait.all(ctl->item_empty + begun % kItems, begun / kItems & 1)) return false;
             pass();
@@ -434,13 +434,14 @@ __device__ void schedule(const AttentionLaunch &L, Control<D> *ctl, const Waiter
     if (!advance()) return;
     int64_t items0 = 0, partials0 = 0, rows0 = 0;
     // From the last request to the first: long prompts stand behind the decode rows and should start first.
+#pragma unroll 1
     for (int64_t base = 0; base < a.num_reqs; base += 32) {
         const int64_t r = a.num_reqs - 1 - base - lane;
         const Request q = load_request(a, r, blockIdx.x == 0);
         const Plan p = plan_request(q.kv, q.m, L.group, D, a.cache.h_kv, a.window);
         const int64_t split_rows = p.splits > 1 ? static_cast<int64_t>(q.m) * a.h_q : 0;
         int64_t items = p.items, partials = p.partials, rows = split_rows;
-#pragma unroll
+#pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t x = __shfl_up_sync(0xffffffffu, items, o), y = __shfl_up_sync(0xffffffffu, partials, o);
             const int64_t z = __shfl_up_sync(0xffffffffu, rows, o);
@@ -452,6 +453,7 @@ __device__ void schedule(const AttentionLaunch &L, Control<D> *ctl, const Waiter
         }
         if (blockIdx.x == 0 && L.ws.o && r == 0) *L.ws.num_rows = rows0 + rows;
         const int64_t group_items = __shfl_sync(0xffffffffu, items, 31);
+#pragma unroll 1
         while (next < items0 + group_items) {
             const int src = __ffs(__ballot_sync(0xffffffffu, items0 + items > next)) - 1;
             // Items of a request: the last row item first (it sees the most keys), all its splits and heads.
@@ -556,15 +558,17 @@ struct Boxes {
 
 // Warp 0 loads Q and the K tiles, warp 3 the V tiles: issuing one box takes a
 // warp some tens of cycles, which pages of 16 rows (16 boxes per 32 KB) would
-// make the bound of a single load warp.
-template <int D, bool kIsK>
-__device__ void load_tiles(const AttentionLaunch &L, Control<D> *ctl, uint32_t q_smem, uint32_t ring, const Waiter &wait) {
+// make the bound of a single load warp.  (One body for both: the block's code
+// is large enough for instruction fetch to matter.)
+template <int D>
+__device__ void load_tiles(const AttentionLaunch &L, Control<D> *ctl, uint32_t q_smem, uint32_t ring, const Waiter &wait,
+                           bool is_k) {
     using Sh = Shape<D>;
     const PagedAttentionArgs &a = L.a;
     const int lane = threadIdx.x & 31;
     const int boxes = kKeys / L.box_rows;
     Boxes where = {a, L.box_rows, lane % boxes, 0, 0, 0, nullptr};
-    const CUtensorMap *map = kIsK ? &L.tm_k : &L.tm_v;
+    const CUtensorMap *map = is_k ? &L.tm_k : &L.tm_v;
     Ring pos;
     uint32_t n_items = 0;
     bool ok = true, wide_before = false;
@@ -582,7 +586,7 @@ __device__ void load_tiles(const AttentionLaunch &L, Control<D> *ctl, uint32_t q
         int32_t id = where.fetch(it.lo);
         const int32_t tile_tokens = kRows / L.group;
         const bool dual = Sh::kStreams == 2 && it.n > tile_tokens;
-        if (kIsK) {
+        if (is_k) {
             // Few tokens: a box per token and panel, one per lane, instead of the full tile's.
             constexpr int kQPanels = D / 64;
             const bool few = it.n < tile_tokens && it.n * kQPanels <= 32;
@@ -609,11 +613,12 @@ __device__ void load_tiles(const AttentionLaunch &L, Control<D> *ctl, uint32_t q
             }
         }
         ++n_items;
+#pragma unroll 1
         for (int32_t t = 0; ok && t < tiles; ++t) {
             int32_t page, row;
             where.place(it.lo + t, id, &page, &row);
             id = where.fetch(it.lo + t + 1);
-            const uint32_t at = pos.first + Sh::kHalves * (kIsK ? pos.k_at(t, dual) : pos.v_at(t, dual));
+            const uint32_t at = pos.first + Sh::kHalves * (is_k ? pos.k_at(t, dual) : pos.v_at(t, dual));
 #pragma unroll 1
             for (int h = 0; h < Sh::kHalves; ++h) {
                 const uint32_t st = (at + h) % Sh::kStages;
@@ -637,7 +642,7 @@ __device__ void load_tiles(const AttentionLaunch &L, Control<D> *ctl, uint32_t q
     // After a failure: copies in flight land before the block may leave (else every copy has been consumed).
     if (!ok) {
         if (lane < Sh::kStages && filled >= 0) drain_bar(ctl->kv_full + lane, filled);
-        if (kIsK && lane < 2 && n_items > static_cast<uint32_t>(lane)) {
+        if (is_k && lane < 2 && n_items > static_cast<uint32_t>(lane)) {
             const uint32_t i = n_items - 1 - lane;
             drain_bar(ctl->q_full + (i & 1), i >> 1 & 1);
         }
@@ -796,6 +801,7 @@ struct Issuer {
     }
     // An item of one row tile: unit g + t is key tile t.
     __device__ __forceinline__ bool single(uint32_t g, int32_t tiles, uint32_t q, uint32_t q_bar) {
+#pragma unroll 1
         for (int32_t t = 0; t < tiles; ++t, ++g) {
             const bool more = t + 1 < tiles;
             Place k;
@@ -810,6 +816,7 @@ struct Issuer {
     }
     // An item of two row tiles: units g + 2t and g + 2t + 1 are key tile t.
     __device__ __forceinline__ bool dual(uint32_t g, int32_t tiles, uint32_t q, uint32_t q_bar) {
+#pragma unroll 1
         for (int32_t t = 0; t < tiles; ++t, g += 2) {
             const bool more = t + 1 < tiles;
             Place k;
@@ -1244,6 +1251,7 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
             float *pout = L.ws.o + prow * D;
             if (dirty) {
                 const int32_t count = rows - warp * 32 < 32 ? rows - warp * 32 : 32;
+#pragma unroll 1
                 for (int r = 0; r < count; ++r)
                     exact_row<D, kHalf>(L, it, __shfl_sync(0xffffffffu, u, r), __shfl_sync(0xffffffffu, head, r),
                                         split ? __shfl_sync(0xffffffffu, prow, r) : -1, lane);
@@ -1341,21 +1349,20 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attention_kernel(const 
     // 384 threads are launched with 168 registers each: 128 x 72 + 256 x 216 is the same sum.
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        if (warp == 0) {
-            load_tiles<D, true>(L, ctl, tc::smem_u32(base), tc::smem_u32(ring), wait);
+        if (warp == 0 || warp == 3) {
+            load_tiles<D>(L, ctl, tc::smem_u32(base), tc::smem_u32(ring), wait, warp == 0);
         } else if (warp == 1) {
             Issuer<D, kHalf> issuer = {wait, tc::smem_u32(ctl), tc::smem_u32(ring), __reduce_max_sync(0xffffffffu, tmem)};
             issuer.run(ctl, L, tc::smem_u32(base));
-        } else if (warp == 2) {
+        } else {
             schedule<D>(L, ctl, wait);
             // Tokens of no request: zeros.
             const PagedAttentionArgs &a = L.a;
             const int32_t end = a.num_reqs > 0 ? a.cu_seqlens[a.num_reqs] : 0;
             const int64_t chunk = static_cast<int64_t>(a.h_q) * D / 8;
+#pragma unroll 1
             for (int64_t i = (end > 0 ? end : 0) * chunk + blockIdx.x * 32 + lane; i < a.num_tokens * chunk; i += gridDim.x * 32)
                 reinterpret_cast<uint4 *>(a.o)[i] = make_uint4(0, 0, 0, 0);
-        } else {
-            load_tiles<D, false>(L, ctl, tc::smem_u32(base), tc::smem_u32(ring), wait);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
