@@ -1382,19 +1382,50 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attention_kernel(const 
 // ---- joining the splits -----------------------------------------------------------------------
 
 constexpr int kJoinWarps = 4;
-constexpr int kJoinBlocksPerSm = 16;
+constexpr int kJoinBlocksPerSm = 8;
 
-// o = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s over a row's parts: a block
-// per row, warp k taking parts k, k + 4, ... in order, their four sums added in
-// order.  The rows are dealt over a grid that fills the GPU once; requests that
-// were not split have no rows here.  Bound by the latency of dependent reads
-// (the row, then all its partials at once) where there are few rows, by L2 or,
-// behind long contexts, by memory where there are many.
+// Adds parts s0 + j * step (j < 4) of a row to sums[j * kMore]; a part's weight is in ml[s / 32].x of lane s % 32, lane i
+// holds columns 2 i + 64 v.
+template <int D, int kWords, int kMore>
+__device__ __forceinline__ void add_parts(const float *o, int64_t stride, int32_t s0, int32_t step, int32_t parts,
+                                          const float2 (&ml)[kWords], float2 (&sums)[3 * kMore + 1][D / 64], int lane) {
+    constexpr int kVec = D / 64;
+    float2 x[4][kVec];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (s0 + j * step < parts)
+#pragma unroll
+            for (int v = 0; v < kVec; ++v)
+                x[j][v] = *reinterpret_cast<const float2 *>(o + (s0 + j * step) * stride + v * 64 + lane * 2);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int32_t s = s0 + j * step;
+        float w = 0.f;
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) {
+            const float y = __shfl_sync(0xffffffffu, ml[k].x, s & 31);
+            if (s >> 5 == k) w = y;
+        }
+        if (s < parts)
+#pragma unroll
+            for (int v = 0; v < kVec; ++v) {
+                sums[j * kMore][v].x = fmaf(w, x[j][v].x, sums[j * kMore][v].x);
+                sums[j * kMore][v].y = fmaf(w, x[j][v].y, sums[j * kMore][v].y);
+            }
+    }
+}
+
+// o = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s over a row's parts.  Four
+// sums, of parts k, k + 4, ..., are added up in order: where rows are few, by
+// the four warps of a block, one block a row; else by one warp, four rows a
+// block - in the same order, so a row's bits do not depend on how many there
+// are.  Requests that were not split have no rows here.  Bound by the latency
+// of dependent reads (the row, then its partials) where there are few rows, by
+// L2 or, behind long contexts, by memory where there are many.
 template <int D, bool kHalf>
-__global__ void __launch_bounds__(kJoinWarps * 32, kJoinBlocksPerSm / 2) join_kernel(const __grid_constant__ AttentionLaunch L) {
-    constexpr int kVec = D / 64;  // pairs of columns of a lane
-    constexpr int kBatch = 4;     // partials that a warp reads at once
-        constexpr int kMl = (kMaxSplits + 31) / 32;
+__global__ void __launch_bounds__(kJoinWarps * 32, 5) join_kernel(const __grid_constant__ AttentionLaunch L) {
+    constexpr int kVec = D / 64;
+    constexpr int kWords = (kMaxSplits + 31) / 32;
     __shared__ float2 sum[kJoinWarps - 1][D / 2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t h_q = L.a.h_q;
@@ -1402,92 +1433,85 @@ __global__ void __launch_bounds__(kJoinWarps * 32, kJoinBlocksPerSm / 2) join_ke
     // the stream relies on both.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t rows = *L.ws.num_rows < L.ws.max_rows ? *L.ws.num_rows : L.ws.max_rows;
-    // A block's rows, up to 32 at a time, one descriptor per lane: those that are in o already cost no round of their own.
-    const int64_t per = (rows + gridDim.x - 1) / gridDim.x, begin = blockIdx.x * per, end = begin + per < rows ? begin + per : rows;
+    const bool alone = rows <= gridDim.x;  // a block a row
+    // The rows of a block or warp, up to 32 at a time, one descriptor per lane: those that are in o already cost no
+    // round of their own.
+    const int64_t teams = alone ? gridDim.x : gridDim.x * kJoinWarps, team = alone ? blockIdx.x : blockIdx.x * kJoinWarps + warp;
+    const int64_t per = (rows + teams - 1) / teams, begin = team * per, end = begin + per < rows ? begin + per : rows;
     for (int64_t i0 = begin; i0 < end; i0 += 32) {
-    JoinRow mine = {0, 0, 0};
-    if (i0 + lane < end) mine = L.ws.rows[i0 + lane];
-    // (a call that timed out or was given overlapping token ranges leaves rows unwritten)
-    uint32_t todo = __ballot_sync(0xffffffffu, mine.parts >= 2 && mine.parts <= kMaxSplits && mine.first >= 0 &&
-                                                   mine.first + (mine.parts - 1) * h_q < L.ws.partials * h_q &&
-                                                   mine.out >= 0 && mine.out < L.ws.max_rows);
-    for (; todo; todo &= todo - 1) {
-        const int src = __ffs(todo) - 1;
-        const JoinRow row = {__shfl_sync(0xffffffffu, mine.out, src), __shfl_sync(0xffffffffu, mine.parts, src),
-                             __shfl_sync(0xffffffffu, mine.first, src)};
-        float2 ml[kMl];
-        float top = -INFINITY;
+        JoinRow mine = {0, 0, 0};
+        if (i0 + lane < end) mine = L.ws.rows[i0 + lane];
+        // (a call that timed out or was given overlapping token ranges leaves rows unwritten)
+        uint32_t todo = __ballot_sync(0xffffffffu, mine.parts >= 2 && mine.parts <= kMaxSplits && mine.first >= 0 &&
+                                                       mine.first + (mine.parts - 1) * h_q < L.ws.partials * h_q &&
+                                                       mine.out >= 0 && mine.out < L.ws.max_rows);
+        for (; todo; todo &= todo - 1) {
+            const int src = __ffs(todo) - 1;
+            const int32_t row_out = __shfl_sync(0xffffffffu, mine.out, src), parts = __shfl_sync(0xffffffffu, mine.parts, src);
+            const int64_t first = __shfl_sync(0xffffffffu, mine.first, src);
+            float2 ml[kWords];
+            float top = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < kMl; ++k) {
-            ml[k] = make_float2(-INFINITY, 0.f);
-            if (lane + 32 * k < row.parts) ml[k] = L.ws.ml[row.first + (lane + 32 * k) * h_q];
-            top = fmaxf(top, ml[k].x);
-        }
-        float2 acc[kVec];
-        float2 x[kBatch][kVec];
-        auto read = [&](int32_t s0) {
+            for (int k = 0; k < kWords; ++k) {
+                ml[k] = make_float2(-INFINITY, 0.f);
+                if (lane + 32 * k < parts) ml[k] = L.ws.ml[first + (lane + 32 * k) * h_q];
+                top = fmaxf(top, ml[k].x);
+            }
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j)
-                if (s0 + j * kJoinWarps < row.parts) {
-                    const float *o = L.ws.o + (row.first + (s0 + j * kJoinWarps) * h_q) * D + lane * 2;
+            for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+            if (top == -INFINITY) top = 0.f;
+            float l = 0.f;
 #pragma unroll
-                    for (int v = 0; v < kVec; ++v) x[j][v] = *reinterpret_cast<const float2 *>(o + v * 64);
+            for (int k = 0; k < kWords; ++k) {
+                ml[k].x = ex2(ml[k].x - top);  // the part's weight
+                l = fmaf(ml[k].x, ml[k].y, l);
+            }
+#pragma unroll
+            for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
+            const float *o = L.ws.o + first * D;
+            float2 acc[kVec];
+            if (alone) {
+                float2 mine4[1][kVec] = {};
+#pragma unroll 1
+                for (int32_t s = warp; s < parts; s += 4 * kJoinWarps)
+                    add_parts<D, kWords, 0>(o, h_q * D, s, kJoinWarps, parts, ml, mine4, lane);
+                if (warp > 0)
+#pragma unroll
+                    for (int v = 0; v < kVec; ++v) sum[warp - 1][v * 32 + lane] = mine4[0][v];
+                __syncthreads();
+#pragma unroll
+                for (int v = 0; v < kVec; ++v) {
+                    acc[v] = mine4[0][v];
+#pragma unroll
+                    for (int k = 0; k < kJoinWarps - 1; ++k) {
+                        acc[v].x += sum[k][v * 32 + lane].x;
+                        acc[v].y += sum[k][v * 32 + lane].y;
+                    }
                 }
-        };
-        read(warp);
+                __syncthreads();
+            } else {
+                float2 four[4][kVec] = {};
+#pragma unroll 1
+                for (int32_t s = 0; s < parts; s += 4) add_parts<D, kWords, 1>(o, h_q * D, s, 1, parts, ml, four, lane);
 #pragma unroll
-        for (int v = 0; v < kVec; ++v) acc[v] = make_float2(0.f, 0.f);
+                for (int v = 0; v < kVec; ++v) {
+                    acc[v] = four[0][v];
 #pragma unroll
-        for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-        if (top == -INFINITY) top = 0.f;
-        float l = 0.f;
-#pragma unroll
-        for (int k = 0; k < kMl; ++k) {
-            ml[k].x = ex2(ml[k].x - top);  // the part's weight
-            l = fmaf(ml[k].x, ml[k].y, l);
-        }
-#pragma unroll
-        for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
-        for (int32_t s0 = warp; s0 < row.parts; s0 += kBatch * kJoinWarps) {
-            if (s0 != warp) read(s0);
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-                const int32_t s = s0 + j * kJoinWarps;
-                float w = 0.f;
-#pragma unroll
-                for (int k = 0; k < kMl; ++k) {
-                    const float y = __shfl_sync(0xffffffffu, ml[k].x, s & 31);
-                    if (s >> 5 == k) w = y;
-                }
-                if (s < row.parts) {
-#pragma unroll
-                    for (int v = 0; v < kVec; ++v) {
-                        acc[v].x = fmaf(w, x[j][v].x, acc[v].x);
-                        acc[v].y = fmaf(w, x[j][v].y, acc[v].y);
+                    for (int k = 1; k < 4; ++k) {
+                        acc[v].x += four[k][v].x;
+                        acc[v].y += four[k][v].y;
                     }
                 }
             }
-        }
-        if (warp > 0)
+            if (!alone || warp == 0) {
+                const bool none = l == 0.f;
+                const float f = none ? 0.f : 1.f / l;
+                uint16_t *out = L.a.o + static_cast<int64_t>(row_out) * D + lane * 2;
 #pragma unroll
-            for (int v = 0; v < kVec; ++v) sum[warp - 1][v * 32 + lane] = acc[v];
-        __syncthreads();
-        if (warp == 0) {
-            const bool none = l == 0.f;
-            const float f = none ? 0.f : 1.f / l;
-            uint16_t *out = L.a.o + static_cast<int64_t>(row.out) * D + lane * 2;
-#pragma unroll
-            for (int v = 0; v < kVec; ++v) {
-#pragma unroll
-                for (int k = 0; k < kJoinWarps - 1; ++k) {
-                    acc[v].x += sum[k][v * 32 + lane].x;
-                    acc[v].y += sum[k][v * 32 + lane].y;
-                }
-                *reinterpret_cast<uint32_t *>(out + v * 64) = none ? 0u : pack2<kHalf>(acc[v].x * f, acc[v].y * f);
+                for (int v = 0; v < kVec; ++v)
+                    *reinterpret_cast<uint32_t *>(out + v * 64) = none ? 0u : pack2<kHalf>(acc[v].x * f, acc[v].y * f);
             }
         }
-        __syncthreads();
-    }
     }
 }
 
