@@ -469,7 +469,8 @@ gdn_status_t gdn_paged_kv_write(const gdn_paged_cache_t *cache, int64_t num_toke
  *                sizes the workspace.
  *   scale        finite, >= 0.
  *   workspace    gdn_paged_attention_workspace_bytes() bytes for the same
- *                sizes, 256-byte aligned; needs no initial value.
+ *                sizes, 256-byte aligned; needs no initial value, and is not
+ *                shared by calls that may run at the same time.
  * GDN_DEV_BAD_LENGTH: a request whose kv_len is negative or over max_kv_len
  * gets zero outputs; one whose cu_seqlens run backwards or past num_tokens is
  * skipped.  A page id outside [0, num_pages) reads as zero keys

@@ -13,6 +13,11 @@ Layouts (all row-major, device memory):
   g, beta     [T][h_v]       float32   (alpha = exp(g))
   state       [num_slots][h_v][d_v][d_k] float32   (S^T per slot and head)
   chunk_states [n_emit][h_v][d_v][d_k] float32
+
+Full-attention layers beside these (bfloat16 or float16, d = 64, 128 or 256):
+  q, o        [T][h_q][d];  k, v [T][h_kv][d]
+  k_cache, v_cache [pages][page_size][h_kv][d], any strides with d contiguous
+  block_table [requests][width] int32 page ids
 """
 from __future__ import annotations
 

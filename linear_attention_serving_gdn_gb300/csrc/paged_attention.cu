@@ -16,21 +16,25 @@
 // whose partial (O, m, l) a second kernel joins in split order.  The cut
 // depends on the request's lengths alone (plan_request), never on the batch,
 // so a request's bits do not change with what else is in the step.  A
-// persistent grid (one block per SM) takes the items round robin; lengths are
-// read on the device, so a captured call replays for others.
+// persistent grid (one block per SM) takes the items from a counter, the
+// requests from the last to the first and each one's longest row items first;
+// lengths are read on the device, so a captured call replays for others.
 //
-// One block, eight warps:
-//   load   TMA boxes of K and V (one per page piece) into a ring of stages
-//          128 keys x up to 128 columns, running ahead over item borders
-//   mma    S = Q K^T (two TMEM buffers, so that the next tile's scores are
-//          computed while this one's weights are), O += P V with P from TMEM
-//   sched  walks the requests, cutting them into items
-//   spare  TMEM allocation, zeros for padding tokens
-//   4 softmax warps, one row per thread: S from TMEM, masks, maximum, exp2,
-//          P back to TMEM over S; at the end O from TMEM to memory
+// One block, twelve warps:
+//   load (2)   TMA boxes of K and V (one per page piece) into a ring of stages
+//              128 keys x up to 128 columns, running ahead over item borders
+//   mma        S = Q K^T into one of two TMEM buffers, O += P V with P from
+//              TMEM; the scores of one unit are computed while the weights of
+//              the one before are (struct Ring)
+//   sched      walks the requests, cutting them into items
+//   softmax (2 x 4)  one row per thread: S from TMEM, masks, maximum, exp2, P
+//              back to TMEM over S; at the end O from TMEM to memory.  With
+//              d <= 128 each warpgroup has its own O; with d = 256 there is
+//              one, and the second warpgroup writes it while the first is on
+//              with the next item.
 //
-// The running maximum only moves when it grows by more than 2^8: weights are
-// then at most 2^8, exact in the sums, and O is rarely touched.  The rule is
+// The running maximum only moves when a score passes it by more than 8 (in
+// powers of two): weights are then at most 2^8, and O is rarely touched.  The rule is
 // per row, so a row's bits do not depend on its neighbours.
 //
 // Every wait is bounded: one that runs out sets GDN_DEV_TIMEOUT and a flag
@@ -120,13 +124,15 @@ __device__ __forceinline__ void key_tiles(int32_t kv, int32_t m, int32_t u, int3
     if (*lo > *hi) *lo = *hi;
 }
 
+// Splits that let a request of few rows fill half of kSplitUnits.
+int32_t few_splits_of(int32_t h_kv) { return h_kv < kSplitUnits / 2 ? kSplitUnits / 2 / h_kv : 1; }
+
 // How a request of m new tokens and kv keys is cut; depends on nothing else of the batch.
-__device__ __forceinline__ Plan plan_request(int32_t kv, int32_t m, int32_t group, int32_t d, int32_t h_kv,
-                                             int32_t window) {
+__device__ __forceinline__ Plan plan_request(int32_t kv, int32_t m, int32_t group, int32_t tile_tokens, int32_t few_splits,
+                                             int32_t d, int32_t h_kv, int32_t window) {
     Plan p;
-    const int32_t streams = streams_of(d);
-    p.item_tokens = kRows / group * streams;
-    p.row_items = ceil_div(m, p.item_tokens);
+    p.item_tokens = tile_tokens * streams_of(d);
+    p.row_items = m <= p.item_tokens ? (m > 0 ? 1 : 0) : ceil_div(m, p.item_tokens);  // (divisions are most of the time here)
     int32_t lo, hi;
     key_tiles(kv, m, 0, m, window, &lo, &hi);
     p.first_tile = lo;
@@ -135,9 +141,8 @@ __device__ __forceinline__ Plan plan_request(int32_t kv, int32_t m, int32_t grou
     const int64_t units = static_cast<int64_t>(p.row_items) * h_kv;
     const int32_t rows = (m < p.item_tokens ? m : p.item_tokens) * group;
     const bool few = rows < kRows / 2;
-    const int32_t fill = few ? kSplitUnits / 2 : kSplitUnits;
-    if (m > 0 && (few || units * 2 <= fill)) {
-        int32_t want = units < fill ? fill / static_cast<int32_t>(units) : 1;
+    if (m > 0 && (few || units * 2 <= kSplitUnits)) {
+        int32_t want = few ? few_splits : kSplitUnits / static_cast<int32_t>(units);
         if (want > kMaxSplits) want = kMaxSplits;
         const int32_t even = ceil_div(hi - lo, want), least = least_split_tiles(hi - lo, rows);
         p.split_tiles = even > least ? even : least;
@@ -226,7 +231,7 @@ struct AttentionLaunch {
     CUtensorMap tm_k, tm_v;  // [page][head][row][d]: boxes of box_rows x 64
     PagedAttentionArgs a;
     Workspace ws;
-    int32_t group, box_rows;
+    int32_t group, tile_tokens, few_splits, box_rows;
     float c;  // scale * log2(e)
 };
 
@@ -391,7 +396,7 @@ __device__ __forceinline__ void zero_rows(const AttentionLaunch &L, const Item &
 }
 
 template <int D>
-__device__ void schedule(const AttentionLaunch &L, Control<D> *ctl, const Waiter &wait) {
+__device__ void schedule(const AttentionLaunch &L, Control<D> *ctl, const Waiter &wait, const Request &first_read) {
     const PagedAttentionArgs &a = L.a;
     const int lane = threadIdx.x & 31;
     uint32_t n = 0;
@@ -437,8 +442,8 @@ __device__ void schedule(const AttentionLaunch &L, Control<D> *ctl, const Waiter
 #pragma unroll 1
     for (int64_t base = 0; base < a.num_reqs; base += 32) {
         const int64_t r = a.num_reqs - 1 - base - lane;
-        const Request q = load_request(a, r, blockIdx.x == 0);
-        const Plan p = plan_request(q.kv, q.m, L.group, D, a.cache.h_kv, a.window);
+        const Request q = base == 0 ? first_read : load_request(a, r, blockIdx.x == 0);
+        const Plan p = plan_request(q.kv, q.m, L.group, L.tile_tokens, L.few_splits, D, a.cache.h_kv, a.window);
         const int64_t split_rows = p.splits > 1 ? static_cast<int64_t>(q.m) * a.h_q : 0;
         int64_t items = p.items, partials = p.partials, rows = split_rows;
 #pragma unroll 1
@@ -467,22 +472,25 @@ __device__ void schedule(const AttentionLaunch &L, Control<D> *ctl, const Waiter
             const int32_t first = __shfl_sync(0xffffffffu, q.first, src);
             const int64_t pbase = partials0 + __shfl_sync(0xffffffffu, partials - p.partials, src);
             const uint32_t heads = static_cast<uint32_t>(a.cache.h_kv), per_piece = heads * static_cast<uint32_t>(splits);
-            const uint32_t nth = local / per_piece, rest = local - nth * per_piece;
+            const uint32_t nth = row_items == 1 ? 0 : local / per_piece, rest = local - nth * per_piece;
             const int32_t piece = row_items - 1 - static_cast<int32_t>(nth);
-            const int32_t split = static_cast<int32_t>(rest / heads);
+            const int32_t split = static_cast<int32_t>(splits == 1 ? 0 : rest / heads);
             const int64_t rbase = rows0 + __shfl_sync(0xffffffffu, rows - split_rows, src);
             Item it;
             it.stop = 0;
             it.req = static_cast<int32_t>(a.num_reqs - 1 - base) - src;
-            it.head = static_cast<int32_t>(rest % heads);
+            it.head = static_cast<int32_t>(rest - static_cast<uint32_t>(split) * heads);
             const int32_t u = piece * p.item_tokens;
             it.n = m - u < p.item_tokens ? m - u : p.item_tokens;
             it.tok = first + u;
             it.pos = kv - m + u;
             int32_t lo, hi;
             key_tiles(kv, m, u, it.n, a.window, &lo, &hi);
-            const int32_t split_lo = (lo - first_tile) / split_tiles;
-            const int32_t split_hi = hi > lo ? (hi - 1 - first_tile) / split_tiles : split_lo;
+            int32_t split_lo = 0, split_hi = splits - 1;
+            if (row_items > 1) {
+                split_lo = splits == 1 ? 0 : (lo - first_tile) / split_tiles;
+                split_hi = splits == 1 || hi == lo ? split_lo : (hi - 1 - first_tile) / split_tiles;
+            }
             const int64_t s_lo = first_tile + static_cast<int64_t>(split) * split_tiles, s_hi = s_lo + split_tiles;
             it.lo = s_lo > lo ? static_cast<int32_t>(s_lo) : lo;
             it.hi = s_hi < hi ? static_cast<int32_t>(s_hi) : hi;
@@ -584,7 +592,7 @@ __device__ void load_tiles(const AttentionLaunch &L, Control<D> *ctl, uint32_t q
         const int32_t tiles = it.hi - it.lo;
         where.start(it);
         int32_t id = where.fetch(it.lo);
-        const int32_t tile_tokens = kRows / L.group;
+        const int32_t tile_tokens = L.tile_tokens;
         const bool dual = Sh::kStreams == 2 && it.n > tile_tokens;
         if (is_k) {
             // Few tokens: a box per token and panel, one per lane, instead of the full tile's.
@@ -835,7 +843,7 @@ struct Issuer {
         return true;
     }
     __device__ __forceinline__ void run(Control<D> *ctl, const AttentionLaunch &L, uint32_t q_smem) {
-        const int32_t tile_tokens = kRows / L.group;
+        const int32_t tile_tokens = L.tile_tokens;
         uint32_t unit = 0, n_items = 0;
         for (uint32_t n = 0;; ++n) {
             const uint32_t s = n % kItems, slot = n_items & 1;
@@ -1093,7 +1101,7 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
     const uint32_t w = Sh::kStreams == 2 ? group : 0;  // warpgroup = buffer = O, with two streams
     const int row = warp * 32 + lane;
     const int32_t u_tile = row / L.group, g = row - u_tile * L.group;
-    const int32_t tile_tokens = kRows / L.group;
+    const int32_t tile_tokens = L.tile_tokens;
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;  // this warp's TMEM lanes
     const uint32_t t_o = tmem + kTmemO + lanes;
     const float c = L.c;
@@ -1330,6 +1338,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attention_kernel(const 
         ctl->fail = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    Request first_read = {0, 0, 0};  // the scheduler's first lengths, on their way while the block sets up
+    if (warp == 2) first_read = load_request(L.a, static_cast<int64_t>(L.a.num_reqs) - 1 - lane, blockIdx.x == 0);
     if (warp == 3) {
         if (lane == 0) {
             tc::prefetch_tensor_map(&L.tm_k);
@@ -1355,7 +1365,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attention_kernel(const 
             Issuer<D, kHalf> issuer = {wait, tc::smem_u32(ctl), tc::smem_u32(ring), __reduce_max_sync(0xffffffffu, tmem)};
             issuer.run(ctl, L, tc::smem_u32(base));
         } else {
-            schedule<D>(L, ctl, wait);
+            schedule<D>(L, ctl, wait, first_read);
             // Tokens of no request: zeros.
             const PagedAttentionArgs &a = L.a;
             const int32_t end = a.num_reqs > 0 ? a.cu_seqlens[a.num_reqs] : 0;
@@ -1561,6 +1571,8 @@ cudaError_t launch_paged_attention(const PagedAttentionArgs &a, cudaStream_t str
     AttentionLaunch L = {};
     L.a = a;
     L.group = a.h_q / c.h_kv;
+    L.tile_tokens = kRows / L.group;
+    L.few_splits = few_splits_of(c.h_kv);
     L.box_rows = kKeys;
     while (c.page_size % L.box_rows != 0) L.box_rows /= 2;
     // A scale of zero weighs all keys alike; the least one keeps masked scores at minus infinity (0 x inf is NaN).
@@ -1569,7 +1581,7 @@ cudaError_t launch_paged_attention(const PagedAttentionArgs &a, cudaStream_t str
     const cuuint64_t d = static_cast<cuuint64_t>(c.d);
     const cuuint64_t q_dims[3] = {d, static_cast<cuuint64_t>(a.h_q), static_cast<cuuint64_t>(a.num_tokens)};
     const cuuint64_t q_strides[2] = {d * 2, static_cast<cuuint64_t>(a.q_token_stride) * 2};
-    const cuuint32_t tile_tokens = static_cast<cuuint32_t>(kRows / L.group);
+    const cuuint32_t tile_tokens = static_cast<cuuint32_t>(L.tile_tokens);
     const cuuint32_t q_box[3] = {64, static_cast<uint32_t>(L.group), tile_tokens}, q_one[3] = {64, q_box[1], 1};
     const cuuint64_t dims[4] = {d, static_cast<cuuint64_t>(c.page_size), static_cast<cuuint64_t>(c.h_kv),
                               static_cast<cuuint64_t>(c.num_pages)};
