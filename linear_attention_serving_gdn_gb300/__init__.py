@@ -23,6 +23,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -126,10 +127,11 @@ def _configure(lib: ctypes.CDLL) -> ctypes.CDLL:
     lib.gdn_paged_maps.argtypes = [_I32, _I32, _I64, _P, _P, _P, _I32, _I64, _P, _I32, _P, _P, _P, _P, _I64,
                                    _P, _P, _P, _P]
     lib.gdn_paged_kv_write.restype = ctypes.c_int
-    lib.gdn_paged_kv_write.argtypes = [ctypes.POINTER(PagedCache), _I64, _P, _I64, _I64, _P, _I64, _I64,
+    lib.gdn_paged_kv_write.argtypes = [_P, _I64,  # the cache: a PagedCache by reference, or its bytes
+                                       _P, _I64, _I64, _P, _I64, _I64,
                                        _P, _P, _P]
     lib.gdn_paged_attention.restype = ctypes.c_int
-    lib.gdn_paged_attention.argtypes = [ctypes.POINTER(PagedCache), _I32, _I64, _I32, _F32, _I32, _I64,
+    lib.gdn_paged_attention.argtypes = [_P, _I32, _I64, _I32, _F32, _I32, _I64,
                                         _P, _I64, _P, _I32, _I64, _P, _P, _P, _P, _SZ, _P, _P]
     lib.gdn_paged_attention_workspace_bytes.restype = _SZ
     lib.gdn_paged_attention_workspace_bytes.argtypes = [_I32, _I32, _I32, _I32, _I64, _I64]
@@ -182,13 +184,14 @@ def _ptr(t):
 # The current stream's handle without building a Stream object (a third of
 # a small call's Python time); the public route where torch lacks it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _stream(stream):
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(_current_device())
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -537,6 +540,7 @@ def gdn_mixed_step_colaunch(num_decodes: int, q, k, v, g, beta, cu_seqlens_p, cu
 
 _PAGED_DTYPES = {torch.bfloat16: GDN_BF16, torch.float16: GDN_FP16}
 _Tensor, _i32 = torch.Tensor, torch.int32
+_pack_cache = struct.Struct("=QQiiii7q").pack  # the bytes of a PagedCache, in a third of its constructor's time
 
 
 # These calls' device work takes microseconds, so the checks of a good call are
@@ -573,7 +577,7 @@ def _strided(t, name, dtype, ndim):
 
 
 def _paged_cache(k_cache, v_cache):
-    """The C description of a cache, and its shape."""
+    """The C description of a cache (its bytes), and its shape."""
     dtype = getattr(k_cache, "dtype", None)
     code = _PAGED_DTYPES.get(dtype)
     if code is None:
@@ -583,8 +587,8 @@ def _paged_cache(k_cache, v_cache):
     if v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must have the same shape")
     pages, page_size, h_kv, d = shape
-    return PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), code, page_size, h_kv, d, pages,
-                      ks[0], ks[1], ks[2], vs[0], vs[1], vs[2]), shape
+    return _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), code, page_size, h_kv, d, pages,
+                       ks[0], ks[1], ks[2], vs[0], vs[1], vs[2]), shape
 
 
 def _block_table(t):
@@ -634,7 +638,7 @@ def gdn_paged_kv_write(k, v, k_cache, v_cache, slot_map, dev_status=None, stream
     T, h_kv, d = rows = k.shape
     if not (rows == v.shape and h_kv == shape[2] and d == shape[3] and slot_map.numel() == T):
         raise ValueError("inconsistent K/V write shapes")
-    _check(lib.gdn_paged_kv_write(ctypes.byref(cache), T, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
+    _check(lib.gdn_paged_kv_write(cache, T, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
                                   slots, _i32_word(dev_status, "dev_status"), _stream(stream)),
            "gdn_paged_kv_write")
 
@@ -672,7 +676,7 @@ def gdn_paged_attention(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, o
     if workspace is not None:
         workspace = _dev(workspace, "workspace", torch.uint8)
         ws, ws_bytes = workspace.data_ptr(), workspace.numel()
-    _check(lib.gdn_paged_attention(ctypes.byref(cache), n, T, h_q, d ** -0.5 if scale is None else scale, window,
+    _check(lib.gdn_paged_attention(cache, n, T, h_q, d ** -0.5 if scale is None else scale, window,
                                    max_kv_len, q.data_ptr(), qs[0], table, width, table_stride, cu, kv, o.data_ptr(),
                                    ws, ws_bytes, _i32_word(dev_status, "dev_status"), _stream(stream)),
            "gdn_paged_attention")

@@ -1589,11 +1589,14 @@ cudaError_t launch_paged_attention(const PagedAttentionArgs &a, cudaStream_t str
     const cuuint64_t k_strides[3] = {bytes(c.k_slot_stride), bytes(c.k_head_stride), bytes(c.k_page_stride)};
     const cuuint64_t v_strides[3] = {bytes(c.v_slot_stride), bytes(c.v_head_stride), bytes(c.v_page_stride)};
     const cuuint32_t box[4] = {64, static_cast<uint32_t>(L.box_rows), 1, 1};
-    if (!encode_tiles(&L.tm_q, a.q, c.dtype, 3, q_dims, q_strides, q_box) ||
-        !encode_tiles(&L.tm_q_one, a.q, c.dtype, 3, q_dims, q_strides, q_one) ||
+    // (with so few tokens no item takes the full tile's box)
+    const bool no_full = a.num_tokens < L.tile_tokens && a.num_tokens * (c.d / 64) <= 32;
+    if (!encode_tiles(&L.tm_q_one, a.q, c.dtype, 3, q_dims, q_strides, q_one) ||
+        (!no_full && !encode_tiles(&L.tm_q, a.q, c.dtype, 3, q_dims, q_strides, q_box)) ||
         !encode_tiles(&L.tm_k, c.k, c.dtype, 4, dims, k_strides, box) ||
         !encode_tiles(&L.tm_v, c.v, c.dtype, 4, dims, v_strides, box))
         return cudaErrorNotSupported;
+    if (no_full) L.tm_q = L.tm_q_one;
     const int64_t items = items_bound(L.group, streams_of(c.d), c.h_kv, a.num_reqs, a.num_tokens, L.ws.partials > 0);
     const bool half = c.dtype == GDN_FP16;
     switch (c.d) {

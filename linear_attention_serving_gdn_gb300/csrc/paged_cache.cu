@@ -252,6 +252,10 @@ cudaError_t launch_paged_maps(const PagedMapsArgs &a, cudaStream_t stream) {
         while (threads > 32 && a.num_reqs <= threads / 2 && a.token_capacity <= 2 * threads) threads /= 2;
     PagedMapsArgs k = a;
     k.aligned = ((reinterpret_cast<uintptr_t>(a.slot_map) | reinterpret_cast<uintptr_t>(a.positions)) & 15u) == 0;
+    if (blocks == 1) {  // no cluster, whose launch costs more
+        maps_kernel<<<1, threads, 0, stream>>>(k);
+        return cudaGetLastError();
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(blocks);
     cfg.blockDim = dim3(threads);
