@@ -115,6 +115,15 @@ struct Plan {
 
 __host__ __device__ __forceinline__ int32_t ceil_div(int32_t a, int32_t b) { return (a + b - 1) / b; }
 
+// ceil(a / b) for 0 <= a < 2^23, b > 0: a reciprocal and a correction, half the time of an integer division.
+__device__ __forceinline__ int32_t ceil_quotient(int32_t a, int32_t b) {
+    int32_t q = __float2int_rz(__fdividef(static_cast<float>(a), static_cast<float>(b)));  // off by one at most
+    if (q * b < a) ++q;
+    if (q * b < a) ++q;
+    if ((q - 1) * b >= a) --q;
+    return q;
+}
+
 // Key tiles [lo, hi) that tokens [u, u + n) of a request see together.
 __device__ __forceinline__ void key_tiles(int32_t kv, int32_t m, int32_t u, int32_t n, int32_t window, int32_t *lo,
                                           int32_t *hi) {
@@ -144,13 +153,13 @@ __device__ __forceinline__ Plan plan_request(int32_t kv, int32_t m, int32_t grou
     if (m > 0 && (few || units * 2 <= kSplitUnits)) {
         int32_t want = few ? few_splits : kSplitUnits / static_cast<int32_t>(units);
         if (want > kMaxSplits) want = kMaxSplits;
-        const int32_t even = ceil_div(hi - lo, want), least = least_split_tiles(hi - lo, rows);
+        const int32_t even = ceil_quotient(hi - lo, want), least = least_split_tiles(hi - lo, rows);
         p.split_tiles = even > least ? even : least;
         if (few) {
             const int32_t most = ceil_div(hi - lo, kMaxSplits) > kMaxSplitTiles ? ceil_div(hi - lo, kMaxSplits) : kMaxSplitTiles;
             if (p.split_tiles > most) p.split_tiles = most;
         }
-        p.splits = hi > lo ? ceil_div(hi - lo, p.split_tiles) : 1;
+        p.splits = hi > lo ? ceil_quotient(hi - lo, p.split_tiles) : 1;
     }
     p.items = units * p.splits;
     p.partials = p.splits > 1 ? static_cast<int64_t>(m) * p.splits : 0;
@@ -446,6 +455,22 @@ __device__ void schedule(const AttentionLaunch &L, Control<D> *ctl, const Waiter
         const Plan p = plan_request(q.kv, q.m, L.group, L.tile_tokens, L.few_splits, D, a.cache.h_kv, a.window);
         const int64_t split_rows = p.splits > 1 ? static_cast<int64_t>(q.m) * a.h_q : 0;
         int64_t items = p.items, partials = p.partials, rows = split_rows;
+        if (__all_sync(0xffffffffu, (items | partials | rows) < (1 << 26))) {  // their sums fit 32 bits
+            int32_t i32 = static_cast<int32_t>(items), p32 = static_cast<int32_t>(partials), r32 = static_cast<int32_t>(rows);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int32_t x = __shfl_up_sync(0xffffffffu, i32, o), y = __shfl_up_sync(0xffffffffu, p32, o);
+                const int32_t z = __shfl_up_sync(0xffffffffu, r32, o);
+                if (lane >= o) {
+                    i32 += x;
+                    p32 += y;
+                    r32 += z;
+                }
+            }
+            items = i32;
+            partials = p32;
+            rows = r32;
+        } else
 #pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t x = __shfl_up_sync(0xffffffffu, items, o), y = __shfl_up_sync(0xffffffffu, partials, o);
@@ -1264,26 +1289,38 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
                     exact_row<D, kHalf>(L, it, __shfl_sync(0xffffffffu, u, r), __shfl_sync(0xffffffffu, head, r),
                                         split ? __shfl_sync(0xffffffffu, prow, r) : -1, lane);
             }
+            if (__any_sync(0xffffffffu, none)) {  // a row that saw no key
+#pragma unroll 1
+                for (int j = 0; valid && none && j < D; j += 8) {
+                    if (split) {
+                        *reinterpret_cast<uint4 *>(pout + j) = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4 *>(pout + j + 4) = make_uint4(0, 0, 0, 0);
+                    } else {
+                        *reinterpret_cast<uint4 *>(out + j) = make_uint4(0, 0, 0, 0);
+                    }
+                }
+            }
+            const bool writes = valid && !none;
 #pragma unroll 1
             for (int q = 0; q < D / 32 && !dirty; ++q) {
                 uint32_t o[32];
                 tc::tmem_ld32(t_o + w * D + q * 32, o);
-#pragma unroll
-                for (int j = 0; j < 32; ++j) o[j] = none ? 0u : __float_as_uint(__uint_as_float(o[j]) * f0);
                 if (pair) {
                     uint32_t o1[32];
                     tc::tmem_ld32(t_o + (w ^ 1) * D + q * 32, o1);
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        o[j] = none ? 0u : __float_as_uint(fmaf(__uint_as_float(o1[j]), f1, __uint_as_float(o[j])));
+                        o[j] = __float_as_uint(fmaf(__uint_as_float(o1[j]), f1, __uint_as_float(o[j]) * f0));
                 }
-                if (valid && split) {
+                if (split) {  // (f0 is 1 without a pair)
+                    if (writes)
 #pragma unroll
-                    for (int j = 0; j < 32; j += 8) store32(pout + q * 32 + j, o + j);
-                } else if (valid) {
+                        for (int j = 0; j < 32; j += 8) store32(pout + q * 32 + j, o + j);
+                } else if (writes) {
+                    const float f = pair ? 1.f : f0;
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
-                        o[j] = pack2<kHalf>(__uint_as_float(o[2 * j]), __uint_as_float(o[2 * j + 1]));
+                        o[j] = pack2<kHalf>(__uint_as_float(o[2 * j]) * f, __uint_as_float(o[2 * j + 1]) * f);
 #pragma unroll
                     for (int j = 0; j < 16; j += 8) store32(out + q * 32 + j * 2, o + j);
                 }
