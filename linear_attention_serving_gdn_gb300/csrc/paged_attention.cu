@@ -166,15 +166,22 @@ __device__ __forceinline__ Plan plan_request(int32_t kv, int32_t m, int32_t grou
     return p;
 }
 
-// Bound of `partials` over the requests of a call: no more splits than
-// kMaxSplits or than the longest context's.
-int64_t partials_bound(int32_t group, int32_t d, int32_t h_kv, int32_t num_reqs, int64_t num_tokens, int64_t max_kv_len) {
+// Bound of a request's splits: no more than kMaxSplits or than the longest
+// context's.  least_split_tiles(s) >= sqrt(s / 2), so s tiles make at most
+// sqrt(2 s) splits, or as many as the cap makes of them.
+int64_t splits_bound(int64_t max_kv_len) {
     const int64_t tiles = (max_kv_len + kKeys - 1) / kKeys;
-    if (tiles <= kMinSplitTiles || num_tokens == 0 || num_reqs == 0) return 0;
-    // least_split_tiles(s) >= sqrt(s / 2), so s tiles make at most sqrt(2 s) splits, or as many as the cap makes of them.
+    if (tiles <= kMinSplitTiles) return 1;
     int64_t splits = (tiles + kMaxSplitTiles - 1) / kMaxSplitTiles;
-    while (splits * splits < 2 * tiles) ++splits;
-    if (splits > kMaxSplits) splits = kMaxSplits;
+    if (splits > kMaxSplits) return kMaxSplits;
+    while (splits * splits < 2 * tiles && splits < kMaxSplits) ++splits;
+    return splits;
+}
+
+// Bound of `partials` over the requests of a call.
+int64_t partials_bound(int32_t group, int32_t d, int32_t h_kv, int32_t num_reqs, int64_t num_tokens, int64_t max_kv_len) {
+    const int64_t splits = splits_bound(max_kv_len);
+    if (splits == 1 || num_tokens == 0 || num_reqs == 0) return 0;
     // With full tiles m tokens make at least m / item_tokens row items and at most kSplitUnits / (h_kv * row items)
     // splits; fewer tokens than half a tile's make at most kMaxSplits.
     const int64_t full = static_cast<int64_t>(kRows / group * streams_of(d)) * ceil_div(kSplitUnits, h_kv);
@@ -184,9 +191,9 @@ int64_t partials_bound(int32_t group, int32_t d, int32_t h_kv, int32_t num_reqs,
 }
 
 // Bound of the items of a call.
-int64_t items_bound(int32_t group, int32_t streams, int32_t h_kv, int32_t num_reqs, int64_t num_tokens, bool split) {
-    const int64_t rows = num_tokens / (kRows / group * streams) + num_reqs;
-    return (rows < num_tokens ? rows : num_tokens) * h_kv * (split ? kMaxSplits : 1);
+int64_t items_bound(int32_t group, int32_t d, int32_t h_kv, int32_t num_reqs, int64_t num_tokens, int64_t max_kv_len) {
+    const int64_t rows = num_tokens / (kRows / group * streams_of(d)) + num_reqs;
+    return (rows < num_tokens ? rows : num_tokens) * h_kv * splits_bound(max_kv_len);
 }
 
 // What the joining kernel needs of a row (token and query head) of a request
@@ -211,12 +218,12 @@ struct Workspace {
 Workspace workspace_at(void *ws, int32_t h_q, int32_t h_kv, int32_t d, int32_t num_reqs, int64_t num_tokens,
                        int64_t max_kv_len) {
     auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
-    const int32_t group = h_q / h_kv, streams = streams_of(d);
+    const int32_t group = h_q / h_kv;
     Workspace w = {};
     char *p = static_cast<char *>(ws);
     w.partials = partials_bound(group, d, h_kv, num_reqs, num_tokens, max_kv_len);
-    // One item per block at most: nothing to balance.
-    if (items_bound(group, streams, h_kv, num_reqs, num_tokens, w.partials > 0) > kSplitUnits) {
+    // With few items per block there is little to balance, less than the counter's reset costs.
+    if (items_bound(group, d, h_kv, num_reqs, num_tokens, max_kv_len) > 3 * kSplitUnits) {
         w.counter = reinterpret_cast<unsigned long long *>(p);
         w.bytes = 256;
     }
@@ -413,6 +420,7 @@ __device__ void schedule(const AttentionLaunch &L, Control<D> *ctl, const Waiter
     uint32_t begun = 0;  // items known to have begun
     int32_t ahead = 0;   // key tiles of those that are not
     int64_t next = -1;
+    bool counted = false;
     // The next item's number, taken when there is room for the item.
     auto advance = [&]() {
         if (!wait.all(ctl->item_empty + n % kItems, (n / kItems & 1) ^ 1)) return false;
@@ -426,12 +434,16 @@ __device__ void schedule(const AttentionLaunch &L, Control<D> *ctl, const Waiter
             if (!wait.all(ctl->item_empty + begun % kItems, begun / kItems & 1)) return false;
             pass();
         }
-        if (!L.ws.counter) {
-            next = next < 0 ? blockIdx.x : next + gridDim.x;
+        if (next < 0) {
+            next = blockIdx.x;
+        } else if (!L.ws.counter) {
+            next += gridDim.x;
         } else {
+            if (!counted) asm volatile("griddepcontrol.wait;" ::: "memory");  // the counter's reset
+            counted = true;
             unsigned long long x = 0;
             if (lane == 0) x = atomicAdd(L.ws.counter, 1ull);
-            next = static_cast<int64_t>(__shfl_sync(0xffffffffu, x, 0));
+            next = gridDim.x + static_cast<int64_t>(__shfl_sync(0xffffffffu, x, 0));
         }
         return true;
     };
@@ -1562,6 +1574,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 5) join_kernel(const __grid_c
     }
 }
 
+// Zeroes the item counter.  The attention kernel starts beside it and waits for
+// it before its blocks take a second item; a memory-set node in its place costs
+// 4 us more.
+__global__ void reset_kernel(unsigned long long *counter) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    *counter = 0;
+}
+
 template <int D, bool kHalf>
 cudaError_t launch_d(const AttentionLaunch &L, int64_t items, cudaStream_t stream) {
     static int set[kMaxDevices] = {};
@@ -1574,24 +1594,28 @@ cudaError_t launch_d(const AttentionLaunch &L, int64_t items, cudaStream_t strea
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < kMaxDevices) __atomic_store_n(&set[dev], 1, __ATOMIC_RELEASE);
     }
+    // A kernel whose launch may overlap the end of the one before; each waits for that where it has to.
+    cudaLaunchAttribute overlap[1];
+    overlap[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    overlap[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = stream;
+    cfg.attrs = overlap;
+    cfg.gridDim = dim3(static_cast<unsigned>(items < sms ? (items > 0 ? items : 1) : sms));
+    cfg.blockDim = dim3(Shape<D>::kThreads);
+    cfg.dynamicSmemBytes = Shape<D>::kSmem;
     if (L.ws.counter) {
-        e = cudaMemsetAsync(L.ws.counter, 0, sizeof(*L.ws.counter), stream);
+        reset_kernel<<<1, 1, 0, stream>>>(L.ws.counter);
+        e = cudaGetLastError();
         if (e != cudaSuccess) return e;
+        cfg.numAttrs = 1;
     }
-    const unsigned blocks = static_cast<unsigned>(items < sms ? (items > 0 ? items : 1) : sms);
-    attention_kernel<D, kHalf><<<blocks, Shape<D>::kThreads, Shape<D>::kSmem, stream>>>(L);
-    e = cudaGetLastError();
+    e = cudaLaunchKernelEx(&cfg, attention_kernel<D, kHalf>, L);
     if (e != cudaSuccess || !L.ws.o) return e;
     const int64_t joins = L.a.num_tokens * L.a.h_q, most = int64_t{sms} * kJoinBlocksPerSm;
-    cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(joins < most ? joins : most));
     cfg.blockDim = dim3(kJoinWarps * 32);
-    cfg.stream = stream;
-    // Its launch overlaps the attention kernel's end; it waits for that before it reads.
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
+    cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, join_kernel<D, kHalf>, L);
 }
@@ -1634,7 +1658,7 @@ cudaError_t launch_paged_attention(const PagedAttentionArgs &a, cudaStream_t str
         !encode_tiles(&L.tm_v, c.v, c.dtype, 4, dims, v_strides, box))
         return cudaErrorNotSupported;
     if (no_full) L.tm_q = L.tm_q_one;
-    const int64_t items = items_bound(L.group, streams_of(c.d), c.h_kv, a.num_reqs, a.num_tokens, L.ws.partials > 0);
+    const int64_t items = items_bound(L.group, c.d, c.h_kv, a.num_reqs, a.num_tokens, a.max_kv_len);
     const bool half = c.dtype == GDN_FP16;
     switch (c.d) {
         case 64: return half ? launch_d<64, true>(L, items, stream) : launch_d<64, false>(L, items, stream);
