@@ -8,15 +8,19 @@
 // of up to 8 blocks runs it in one launch.  Every block scans all requests
 // (1024 at a time, one per thread, sums carried in 64 bits), so no block
 // waits for another's sums; the tokens and the new table entries of those
-// 1024 requests are then dealt out over the cluster's threads, each finding
-// its request by bisection in shared memory, so one long prompt among
-// thousands of decode rows is still spread over all threads.  The cluster
-// barrier orders every block's read of free_head before its update, which
-// makes updating it in place sound.
+// 1024 requests are then dealt out over the cluster's threads, four tokens a
+// thread and round, each finding its request by bisection in shared memory, so
+// one long prompt among thousands of decode rows is still spread over all
+// threads.  The cluster barrier orders every block's read of free_head before
+// its update, which makes updating it in place sound.  Measured: 8 rows 4.9
+// us, 1000 rows and 24 chunks (61 thousand tokens) 9.7 us (12.9 us with one
+// token a thread), both in a replayed graph.
 //
-// write_kernel.  A copy: 16-byte pieces, K and V in one launch, several
-// pieces' loads in flight per thread; bound by HBM for long chunks and by the
-// launch for decode steps.
+// write_kernel.  A copy: 16-byte pieces, K and V in one launch, four pieces'
+// loads in flight per thread; bound by HBM for long chunks and by the launch
+// for decode steps.  Measured: 32768 tokens of 8 x 128 43.1 us (6.2 TB/s, 0.92
+// of the copy peak; 50.7 us with 64-bit index arithmetic per piece), 256
+// tokens of 2 x 256 2.7 us.
 #include "paged.cuh"
 
 #include <limits.h>
