@@ -27,6 +27,7 @@
 //              TMEM; the scores of one unit are computed while the weights of
 //              the one before are (struct Ring)
 //   sched      walks the requests, cutting them into items
+//              (d = 64: one load warp, and one MMA warp for each of the products)
 //   softmax (2 x 4)  one row per thread: S from TMEM, masks, maximum, exp2, P
 //              back to TMEM over S; at the end O from TMEM to memory.  With
 //              d <= 128 each warpgroup has its own O; with d = 256 there is
@@ -275,6 +276,7 @@ struct Item {
 template <int D>
 struct Shape {
     static constexpr int kStreams = streams_of(D);
+    static constexpr bool kEarly = D == 64;  // scores run ahead of the weights (struct Ring)
     static constexpr int kThreads = 384;
     static constexpr int kCols = D < 128 ? D : 128;  // columns of a stage
     static constexpr int kHalves = D / kCols;        // stages of a K or V tile
@@ -289,6 +291,11 @@ struct Shape {
     // As many stages as 227 KB hold beside Q and the control block.
     static constexpr int kControl = 2048;
     static constexpr int kStages = (227 * 1024 - 1024 - kControl - static_cast<int>(kQ)) / static_cast<int>(kStage);
+    static constexpr uint32_t kSide = kStages / 2;  // of K, and of V, where they have a ring each
+    // P of unit g in TMEM: over its S, or behind O.
+    static __device__ __forceinline__ uint32_t p_at(uint32_t g) {
+        return kEarly ? kTmemO + kStreams * D + (g & 1) * (kKeys / 2) : (g & 1) * kKeys;
+    }
     static constexpr uint32_t kSmem = 1024 + kQ + kStages * kStage + kControl;
 };
 
@@ -296,10 +303,10 @@ template <int D>
 struct Control {
     uint64_t kv_full[Shape<D>::kStages], kv_empty[Shape<D>::kStages];
     uint64_t q_full[2], q_empty[2];
-    uint64_t s_full[2], p_full[2];
+    uint64_t s_full[2], s_free[2], p_full[2];
     uint64_t o_done[2], o_free[2], ml_full[2], ml_empty, item_done, scanned[2];
     uint64_t item_full[kItems], item_empty[kItems];
-    uint64_t drain;
+    uint64_t drain[2];
     Item items[kItems];
     uint32_t dirty[2][2];  // per warpgroup: number of the last even or odd scan that found a NaN or infinity
     uint32_t tmem;
@@ -323,17 +330,37 @@ struct Control {
 // tile of an item of one row tile is used after the next item's first K and
 // lies behind it.  `first` is the item's first stage, `late` whether such a V
 // of the item before lies behind its first K.
+//
+// With d = 64 (kEarly) TMEM has room for P beside S, and scores run ahead of
+// the weights: S of unit g + 2 is written as soon as that of g is in registers,
+// so a warpgroup that is done with a unit finds the next one's scores there
+// instead of waiting for two products in turn.  K and V then have their own
+// rings, and `first` counts tiles.  (Five chunks of 700 tokens on 16 thousand
+// keys, 16/4 of 64: 382 -> 331 us; 8192 tokens, 16/16: 216 -> 190.)
+template <int D>
 struct Ring {
+    using Sh = Shape<D>;
+    struct Place {
+        uint32_t stage, parity;
+    };
     uint32_t first = 0, late = 0;
-    // in tiles from `first`:
-    __device__ __forceinline__ uint32_t k_at(uint32_t t, bool dual) const {
-        return t == 0 ? 0 : dual ? late + 2 * t : late + 2 * t - 1;
+    // Half h of the K or V of the item's key tile t.
+    __device__ __forceinline__ Place at(bool is_k, uint32_t t, bool dual, uint32_t h) const {
+        if (Sh::kEarly) {
+            const uint32_t n = first + t;
+            return {n % Sh::kSide + (is_k ? 0 : Sh::kSide), n / Sh::kSide & 1};
+        }
+        const uint32_t tile = dual ? late + 2 * t + (is_k && t == 0 ? 0 - late : is_k ? 0 : 1)
+                                   : late + 2 * t + (is_k && t == 0 ? 0 - late : is_k ? 0u - 1 : 2);
+        const uint32_t n = first + Sh::kHalves * tile + h;
+        return {n % Sh::kStages, n / Sh::kStages & 1};
     }
-    __device__ __forceinline__ uint32_t v_at(uint32_t t, bool dual) const {
-        return dual ? 1 + late + 2 * t : 2 + late + 2 * t;
-    }
-    __device__ __forceinline__ void next(uint32_t tiles, bool dual, uint32_t halves) {
-        first += halves * (late + 2 * tiles - (dual ? 0 : 1));
+    __device__ __forceinline__ void next(uint32_t tiles, bool dual) {
+        if (Sh::kEarly) {
+            first += tiles;
+            return;
+        }
+        first += Sh::kHalves * (late + 2 * tiles - (dual ? 0 : 1));
         late = dual ? 0 : 1;
     }
 };
@@ -576,44 +603,62 @@ __device__ __forceinline__ void visible_rows(const Item &it, int32_t window, int
 
 // ---- the load warps -----------------------------------------------------------------
 
-// Page and row of this lane's box of a key tile.  A box that no token sees, or
-// whose page id is bad, is loaded from past the last page: TMA fills zeros.
+// Page and row of this lane's box of a key tile, tile after tile (a step
+// without divisions).  A box that no token sees, or whose page id is bad, is
+// loaded from past the last page: TMA fills zeros.
 struct Boxes {
     const PagedAttentionArgs &a;
-    int32_t box_rows, box;  // this lane's box of a tile
-    int32_t row_lo, row_hi, hi;
+    int32_t box_rows, box;        // this lane's box of a tile
+    int32_t step_idx, step_row;   // of kKeys keys: whole pages, rows beyond
+    int32_t key, idx, row;        // of the box whose id is fetched next: first key, place in the table, row in the page
+    int32_t row_lo, row_hi, end;  // keys that some token sees, end of the item's
     const int32_t *table;
+    int32_t next_id, next_row;
+    bool next_seen;
     __device__ __forceinline__ void start(const Item &it) {
         visible_rows(it, a.window, &row_lo, &row_hi);
-        hi = it.hi;
+        end = it.hi * kKeys;
+        if (row_hi < end) end = row_hi;
         table = a.block_table + it.req * a.table_stride;
-    }
-    __device__ __forceinline__ bool seen(int32_t tile) const {
-        const int32_t key = tile * kKeys + box * box_rows;
-        return tile < hi && key < row_hi && key + box_rows > row_lo;
+        key = it.lo * kKeys + box * box_rows;
+        idx = key / a.cache.page_size;
+        row = key - idx * a.cache.page_size;
+        fetch();
     }
     // The table's entry, asked for one tile ahead of its use.
-    __device__ __forceinline__ int32_t fetch(int32_t tile) const {
-        return seen(tile) ? table[(tile * kKeys + box * box_rows) / a.cache.page_size] : 0;
+    __device__ __forceinline__ void fetch() {
+        next_seen = key < end && key + box_rows > row_lo;
+        next_id = next_seen ? table[idx] : 0;
+        next_row = row;
+        key += kKeys;
+        idx += step_idx;
+        row += step_row;
+        if (row >= a.cache.page_size) {
+            row -= a.cache.page_size;
+            ++idx;
+        }
     }
-    __device__ __forceinline__ void place(int32_t tile, int32_t id, int32_t *page, int32_t *row) const {
+    __device__ __forceinline__ void place(int32_t *page, int32_t *at) {
         *page = static_cast<int32_t>(a.cache.num_pages);
-        *row = 0;
-        if (seen(tile)) {
-            if (id >= 0 && id < *page) {
-                *page = id;
-                *row = (tile * kKeys + box * box_rows) % a.cache.page_size;
+        *at = 0;
+        if (next_seen) {
+            if (next_id >= 0 && next_id < *page) {
+                *page = next_id;
+                *at = next_row;
             } else {
                 report(a.dev_status, GDN_DEV_BAD_SLOT);
             }
         }
+        fetch();
     }
 };
 
-// Warp 0 loads Q and the K tiles, warp 3 the V tiles: issuing one box takes a
-// warp some tens of cycles, which pages of 16 rows (16 boxes per 32 KB) would
-// make the bound of a single load warp.  (One body for both: the block's code
-// is large enough for instruction fetch to matter.)
+// Warp 0 loads Q and the K tiles, warp 3 the V tiles: a box takes a warp 65 to
+// 100 cycles to issue, one lane's after another's, which pages of 16 rows (16
+// boxes per 32 KB) would make the bound of a single load warp.  (One body for
+// both: the block's code is large enough for instruction fetch to matter.)
+// With d = 64 there are only 16 KB a tile, and warp 0 loads K and V, a box of
+// each from the same coordinates; warp 3 issues products.
 template <int D>
 __device__ void load_tiles(const AttentionLaunch &L, Control<D> *ctl, uint32_t q_smem, uint32_t ring, const Waiter &wait,
                            bool is_k) {
@@ -621,9 +666,9 @@ __device__ void load_tiles(const AttentionLaunch &L, Control<D> *ctl, uint32_t q
     const PagedAttentionArgs &a = L.a;
     const int lane = threadIdx.x & 31;
     const int boxes = kKeys / L.box_rows;
-    Boxes where = {a, L.box_rows, lane % boxes, 0, 0, 0, nullptr};
     const CUtensorMap *map = is_k ? &L.tm_k : &L.tm_v;
-    Ring pos;
+    Boxes where = {a, L.box_rows, lane % boxes, kKeys / a.cache.page_size, kKeys % a.cache.page_size};
+    Ring<D> pos;
     uint32_t n_items = 0;
     bool ok = true, wide_before = false;
     int32_t filled = -1;  // of stage `lane`: this warp's last fill
@@ -637,7 +682,6 @@ __device__ void load_tiles(const AttentionLaunch &L, Control<D> *ctl, uint32_t q
         if (it.stop) break;
         const int32_t tiles = it.hi - it.lo;
         where.start(it);
-        int32_t id = where.fetch(it.lo);
         const int32_t tile_tokens = L.tile_tokens;
         const bool dual = Sh::kStreams == 2 && it.n > tile_tokens;
         if (is_k) {
@@ -670,28 +714,40 @@ __device__ void load_tiles(const AttentionLaunch &L, Control<D> *ctl, uint32_t q
 #pragma unroll 1
         for (int32_t t = 0; ok && t < tiles; ++t) {
             int32_t page, row;
-            where.place(it.lo + t, id, &page, &row);
-            id = where.fetch(it.lo + t + 1);
-            const uint32_t at = pos.first + Sh::kHalves * (is_k ? pos.k_at(t, dual) : pos.v_at(t, dual));
+            where.place(&page, &row);
+            if constexpr (Sh::kEarly) {
+                const auto [sk, parity] = pos.at(true, t, dual, 0);
+                const uint32_t sv = sk + Sh::kSide;
+                ok = wait.all(ctl->kv_empty + sk, parity ^ 1) && wait.all(ctl->kv_empty + sv, parity ^ 1);
+                if (!ok) break;
+                if (lane == 0) {
+                    tc::mbar_expect_tx(ctl->kv_full + sk, Sh::kStage);
+                    tc::mbar_expect_tx(ctl->kv_full + sv, Sh::kStage);
+                }
+                __syncwarp();
+                if (lane < boxes) {
+                    const uint32_t to = ring + sk * Sh::kStage + lane * L.box_rows * 128;
+                    tc::tma_load_4d(to, &L.tm_k, 0, row, it.head, page, ctl->kv_full + sk);
+                    tc::tma_load_4d(to + Sh::kSide * Sh::kStage, &L.tm_v, 0, row, it.head, page, ctl->kv_full + sv);
+                }
+                if (lane == static_cast<int>(sk) || lane == static_cast<int>(sv)) filled = static_cast<int32_t>(parity);
+            } else
 #pragma unroll 1
             for (int h = 0; h < Sh::kHalves; ++h) {
-                const uint32_t st = (at + h) % Sh::kStages;
-                ok = wait.all(ctl->kv_empty + st, ((at + h) / Sh::kStages & 1) ^ 1);
+                const auto [st, parity] = pos.at(is_k, t, dual, h);
+                ok = wait.all(ctl->kv_empty + st, parity ^ 1);
                 if (!ok) break;
                 if (lane == 0) tc::mbar_expect_tx(ctl->kv_full + st, Sh::kStage);
-#pragma unroll 1
-                for (int b = 0; b < boxes; ++b) {
-                    const int32_t bp = __shfl_sync(0xffffffffu, page, b), br = __shfl_sync(0xffffffffu, row, b);
-                    if (lane == 0)
+                __syncwarp();
+                if (lane < boxes)
 #pragma unroll
-                        for (int p = 0; p < Sh::kPanels; ++p)
-                            tc::tma_load_4d(ring + st * Sh::kStage + p * kPanel + b * L.box_rows * 128, map,
-                                            h * Sh::kCols + p * 64, br, it.head, bp, ctl->kv_full + st);
-                }
-                if (lane == static_cast<int>(st)) filled = static_cast<int32_t>((at + h) / Sh::kStages & 1);
+                    for (int p = 0; p < Sh::kPanels; ++p)
+                        tc::tma_load_4d(ring + st * Sh::kStage + p * kPanel + lane * L.box_rows * 128, map,
+                                        h * Sh::kCols + p * 64, row, it.head, page, ctl->kv_full + st);
+                if (lane == static_cast<int>(st)) filled = static_cast<int32_t>(parity);
             }
         }
-        pos.next(tiles, dual, Sh::kHalves);
+        pos.next(tiles, dual);
     }
     // After a failure: copies in flight land before the block may leave (else every copy has been consumed).
     if (!ok) {
@@ -714,12 +770,18 @@ __device__ void load_tiles(const AttentionLaunch &L, Control<D> *ctl, uint32_t q
 // product only its commits and the wait for the weights stand before the next
 // one.  Stages are used in ring order: the place only steps.
 
+// Instruction descriptors of the two products.
+template <int D, bool kHalf>
+struct Products {
+    static constexpr uint32_t kType = kHalf ? 0u : tc::kIdescBf16;
+    static constexpr uint32_t kIdescS = tc::idesc_f16_f32acc(kRows, kKeys) | kType;
+    static constexpr uint32_t kIdescO = tc::idesc_f16_f32acc(kRows, Shape<D>::kCols) | kType | tc::kIdescBmn;
+};
+
 template <int D, bool kHalf>
 struct Issuer {
     using Sh = Shape<D>;
-    static constexpr uint32_t kType = kHalf ? 0u : tc::kIdescBf16;
-    static constexpr uint32_t kIdescS = tc::idesc_f16_f32acc(kRows, kKeys) | kType;
-    static constexpr uint32_t kIdescO = tc::idesc_f16_f32acc(kRows, Sh::kCols) | kType | tc::kIdescBmn;
+    static constexpr uint32_t kIdescS = Products<D, kHalf>::kIdescS, kIdescO = Products<D, kHalf>::kIdescO;
     static constexpr int kScoreSteps = Sh::kCols / 16, kWeightSteps = kKeys / 16;  // products of a stage
     // A place in the ring: stage and the parity of its filling.
     struct Place {
@@ -927,7 +989,122 @@ struct Issuer {
         }
         if (tc::elect_lane()) tc::mma_commit(GDN_BAR(drain, 0));
         __syncwarp();
-        drain_bar(&ctl->drain, 0);
+        drain_bar(ctl->drain, 0);
+    }
+};
+
+// With scores ahead of the weights (d = 64) nothing orders the two but the
+// barriers, and a warp for each issues them: one for both takes 1500 cycles a
+// unit with everything there, of which the products are 640.
+template <int D, bool kHalf>
+struct EarlyIssuer {
+    using Sh = Shape<D>;
+    static constexpr uint32_t kIdescS = Products<D, kHalf>::kIdescS, kIdescO = Products<D, kHalf>::kIdescO;
+    // A place in the ring of K or of V.
+    struct Place {
+        uint32_t stage, phase;
+        __device__ __forceinline__ void step() {
+            if (++stage == Sh::kSide) {
+                stage = 0;
+                phase ^= 1;
+            }
+        }
+    };
+    const Waiter &wait;
+    uint32_t bars;  // address of the control block
+    uint32_t ring, tmem;
+    Place at;       // of the next K or V
+    uint32_t unit;
+
+    // Tokens and key tiles of the n-th item; false at the end.
+    __device__ __forceinline__ bool take(Control<D> *ctl, uint32_t n, int32_t *tokens, int32_t *tiles) const {
+        const uint32_t s = n % kItems;
+        if (!wait.all(GDN_BAR(item_full, s), n / kItems & 1)) return false;
+        // (through a warp reduction: what the compiler knows to be uniform it keeps in uniform registers)
+        const int32_t stop = __reduce_max_sync(0xffffffffu, ctl->items[s].stop);
+        *tokens = __reduce_max_sync(0xffffffffu, ctl->items[s].n);
+        *tiles = __reduce_max_sync(0xffffffffu, ctl->items[s].hi - ctl->items[s].lo);
+        if (tc::elect_lane()) tc::mbar_arrive(ctl->item_empty + s);
+        __syncwarp();
+        return !stop;
+    }
+    // S of the next unit from Q at q and the next K (`passes`: its last use).
+    __device__ __forceinline__ bool scores(uint32_t q, bool passes, bool q_free, uint32_t q_bar) {
+        const uint32_t b = unit & 1;
+        if (!wait.all(GDN_BAR(kv_full, at.stage), at.phase)) return false;
+        if (!wait.all(GDN_BAR(s_free, b), (unit >> 1 & 1) ^ 1)) return false;
+        tc::fence_after_sync();
+        const uint32_t kd = tc::desc_lo(ring + at.stage * Sh::kStage, 16), d = tmem + b * kKeys;
+        if (tc::elect_lane()) {
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) tc::mma_f16_lo(d, q + i * 2, kd + i * 2, kIdescS, i > 0);
+            tc::mma_commit(GDN_BAR(s_full, b));
+            if (passes) tc::mma_commit(GDN_BAR(kv_empty, at.stage));
+            if (q_free) tc::mma_commit(q_bar);
+        }
+        __syncwarp();
+        if (passes) at.step();
+        ++unit;
+        return true;
+    }
+    // O (+)= P V of the next unit.
+    __device__ __forceinline__ bool weights(bool passes, bool starts, uint32_t &used) {
+        const uint32_t b = unit & 1, stage = Sh::kSide + at.stage;
+        if (starts) {
+            if (!wait.all(GDN_BAR(o_free, b), (used >> b & 1) ^ 1)) return false;
+            used ^= 1u << b;
+        }
+        if (!wait.all(GDN_BAR(kv_full, stage), at.phase)) return false;
+        if (!wait.all(GDN_BAR(p_full, b), unit >> 1 & 1)) return false;
+        tc::fence_after_sync();
+        const uint32_t vd = tc::desc_lo(ring + stage * Sh::kStage, kPanel);
+        const uint32_t d = tmem + kTmemO + b * D, p = tmem + Sh::p_at(unit);
+        if (tc::elect_lane()) {
+#pragma unroll
+            for (int i = 0; i < kKeys / 16; ++i) tc::mma_f16_ta_lo(d, p + i * 8, vd + i * (2048 >> 4), kIdescO, !starts || i > 0);
+            tc::mma_commit(GDN_BAR(o_done, b));
+            if (passes) tc::mma_commit(GDN_BAR(kv_empty, stage));
+        }
+        __syncwarp();
+        if (passes) at.step();
+        ++unit;
+        return true;
+    }
+    __device__ __forceinline__ void run_scores(Control<D> *ctl, const AttentionLaunch &L, uint32_t q_smem) {
+        int32_t tokens, tiles;
+        bool ok = true;
+#pragma unroll 1
+        for (uint32_t n = 0; ok && take(ctl, n, &tokens, &tiles); ++n) {
+            const uint32_t slot = n & 1;
+            const bool two = tokens > L.tile_tokens;
+            if (!wait.all(GDN_BAR(q_full, slot), n >> 1 & 1)) break;
+            const uint32_t q = tc::desc_lo(q_smem + (two ? 0 : slot * Sh::kQSlot), 16), q_bar = GDN_BAR(q_empty, slot);
+            const int32_t units = two ? 2 * tiles : tiles;
+#pragma unroll 1
+            for (int32_t j = 0; ok && j < units; ++j) {
+                const bool second = two && (j & 1);
+                ok = scores(second ? q + (Sh::kQTile >> 4) : q, second || !two, j + 1 == units, q_bar);
+            }
+        }
+        drain(ctl, 0);
+    }
+    __device__ __forceinline__ void run_weights(Control<D> *ctl, const AttentionLaunch &L) {
+        int32_t tokens, tiles;
+        uint32_t used = 0;  // per O: parity of the items that used it
+        bool ok = true;
+#pragma unroll 1
+        for (uint32_t n = 0; ok && take(ctl, n, &tokens, &tiles); ++n) {
+            const bool two = tokens > L.tile_tokens;
+            const int32_t units = two ? 2 * tiles : tiles;
+#pragma unroll 1
+            for (int32_t j = 0; ok && j < units; ++j) ok = weights(!two || (j & 1), j < Sh::kStreams, used);
+        }
+        drain(ctl, 1);
+    }
+    __device__ __forceinline__ void drain(Control<D> *ctl, int i) const {
+        if (tc::elect_lane()) tc::mma_commit(GDN_BAR(drain, i));
+        __syncwarp();
+        drain_bar(ctl->drain + i, 0);
     }
 #undef GDN_BAR
 };
@@ -1151,7 +1328,7 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;  // this warp's TMEM lanes
     const uint32_t t_o = tmem + kTmemO + lanes;
     const float c = L.c;
-    Ring pos;
+    Ring<D> pos;
     uint32_t unit0 = 0;              // first unit of the item
     uint32_t n_items = 0, ml_got = 0, scans = 0;
     for (uint32_t n = 0;; ++n) {
@@ -1183,17 +1360,36 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
             const int32_t k0 = (it.lo + t) * kKeys;
             if (!wait.all(ctl->s_full + b, unit >> 1 & 1)) return;
             tc::fence_after_sync();
+            // With scores ahead of the weights S may be written again once it is in registers.
+            auto taken = [&] {
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(ctl->s_free + b);
+            };
+            // And the weights before these have to be used (the last of the item before were waited for with its O).
+            auto used = [&] {
+                if (j >= Sh::kStreams && !wait.all(ctl->o_done + w, (unit - 2) >> 1 & 1)) return false;
+                tc::fence_after_sync();
+                return true;
+            };
+            if (Sh::kEarly && !any_row) {
+                taken();
+                if (!used()) return;
+            }
             if (any_row) {
                 const uint32_t t_s = tmem + b * kKeys + lanes;
                 if (__any_sync(0xffffffffu, valid && (k0 + kKeys > key_hi || k0 < key_lo)))
                     mask_scores(t_s, key_lo - k0, key_hi - k0);
                 uint32_t x[kKeys];
                 tc::tmem_ld128(t_s, x);
+                if (Sh::kEarly) taken();
                 float f;
-                if (move_max(x, valid, c, m, &f)) {
+                const bool moved = move_max(x, valid, c, m, &f);
+                if (Sh::kEarly && !used()) return;
+                if (moved) {
                     l *= f;
                     if (j >= Sh::kStreams) {
-                        // With two streams S of this unit told that O is done: both are this warpgroup's buffers.
+                        // With two streams O is done: S of this unit came after it, or see above.
                         if (Sh::kStreams == 1) {
                             if (!wait.all(ctl->o_done, (unit - 1) & 1)) return;
                             tc::fence_after_sync();
@@ -1201,7 +1397,7 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
                         scale_o<D>(t_o + w * D, f);
                     }
                 }
-                l += store_weights<kHalf>(t_s, x, c, m == -INFINITY ? 0.f : m * c);
+                l += store_weights<kHalf>(tmem + Sh::p_at(unit) + lanes, x, c, m == -INFINITY ? 0.f : m * c);
             }
             // A weight of zero does not keep a NaN or infinity out of the product.  Value rows that no token of the item
             // sees are zeroed before it; where tokens see different keys of the tile, the rest is looked through, and an
@@ -1209,12 +1405,11 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
             const bool some = k0 + kKeys > row_hi || k0 < row_lo;
             const bool differ = it.n > 1 && (k0 + kKeys > it.pos + 1 || (a.window > 0 && it.pos + it.n - k0 > a.window));
             if (some || differ) {
-                const uint32_t at = pos.first + Sh::kHalves * pos.v_at(t, dual);
                 uint32_t top = 0;  // largest magnitudes seen
 #pragma unroll 1
-                for (uint32_t v = at; v < at + Sh::kHalves; ++v) {
+                for (uint32_t h = 0; h < Sh::kHalves; ++h) {
                     // Two waits: a parity tells this fill from the one before only once that one has been consumed.
-                    const uint32_t st = v % Sh::kStages, parity = v / Sh::kStages & 1;
+                    const auto [st, parity] = pos.at(false, t, dual, h);
                     if (!wait.all(ctl->kv_empty + st, parity ^ 1) || !wait.all(ctl->kv_full + st, parity)) return;
                     uint8_t *tile = ring + st * Sh::kStage;
                     if (some) {
@@ -1355,7 +1550,7 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
                 if (pair) tc::mbar_arrive(ctl->o_free + (w ^ 1));
             }
         }
-        pos.next(tiles, dual, Sh::kHalves);
+        pos.next(tiles, dual);
         unit0 += units;
     }
 }
@@ -1378,7 +1573,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attention_kernel(const 
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(ctl->q_full + i, 1);
             tc::mbar_init(ctl->q_empty + i, 1);
+            tc::mbar_init(ctl->drain + i, 1);
             tc::mbar_init(ctl->s_full + i, 1);
+            tc::mbar_init(ctl->s_free + i, 4);
             tc::mbar_init(ctl->p_full + i, 4);
             tc::mbar_init(ctl->o_done + i, 1);
             tc::mbar_init(ctl->o_free + i, 4);
@@ -1388,11 +1585,10 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attention_kernel(const 
         }
         for (int i = 0; i < kItems; ++i) {
             tc::mbar_init(ctl->item_full + i, 1);
-            tc::mbar_init(ctl->item_empty + i, 3 + 8);  // two load warps, MMA, softmax warps
+            tc::mbar_init(ctl->item_empty + i, 3 + 8);  // load and MMA warps, softmax warps
         }
         tc::mbar_init(&ctl->ml_empty, 4);
         tc::mbar_init(&ctl->item_done, 1);
-        tc::mbar_init(&ctl->drain, 1);
         ctl->fail = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -1417,11 +1613,20 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attention_kernel(const 
     // 384 threads are launched with 168 registers each: 128 x 72 + 256 x 216 is the same sum.
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        if (warp == 0 || warp == 3) {
+        if (warp == 0 || (warp == 3 && !Sh::kEarly)) {
             load_tiles<D>(L, ctl, tc::smem_u32(base), tc::smem_u32(ring), wait, warp == 0);
-        } else if (warp == 1) {
-            Issuer<D, kHalf> issuer = {wait, tc::smem_u32(ctl), tc::smem_u32(ring), __reduce_max_sync(0xffffffffu, tmem)};
-            issuer.run(ctl, L, tc::smem_u32(base));
+        } else if (warp != 2) {
+            const uint32_t t = __reduce_max_sync(0xffffffffu, tmem);
+            if constexpr (Sh::kEarly) {
+                EarlyIssuer<D, kHalf> issuer = {wait, tc::smem_u32(ctl), tc::smem_u32(ring), t};
+                if (warp == 1)
+                    issuer.run_scores(ctl, L, tc::smem_u32(base));
+                else
+                    issuer.run_weights(ctl, L);
+            } else {
+                Issuer<D, kHalf> issuer = {wait, tc::smem_u32(ctl), tc::smem_u32(ring), t};
+                issuer.run(ctl, L, tc::smem_u32(base));
+            }
         } else {
             schedule<D>(L, ctl, wait, first_read);
             // Tokens of no request: zeros.
