@@ -39,12 +39,12 @@
 // per row, so a row's bits do not depend on its neighbours.
 //
 // What bounds it: HBM for single tokens over long contexts (8 rows of 100 to
-// 131 thousand keys, 32/8 heads of 128: 3.68 GB in 555 us, 0.97 of the copy
+// 131 thousand keys, 32/8 heads of 128: 3.68 GB in 545 us, 0.99 of the copy
 // peak; 256 rows of up to 4095 keys, 16/2 of 256: 6.3 TB/s); the tensor pipe
 // for long chunks (2048 tokens twice at 32 thousand keys, 16/2 of 256: 1450 to
-// 1560 us, 1.44 to 1.55 PF/s; a prompt of 8192 tokens, 32/8 of 128: 403 us,
-// 1.36 PF/s); the fill and drain of the pipe per item for short prompts (8 of
-// 116 to 2000 tokens: 101 us); a chain of ~10 us (lengths, page ids, first tile,
+// 1560 us, 1.44 to 1.55 PF/s; a prompt of 8192 tokens, 32/8 of 128: 400 us,
+// 1.37 PF/s); the softmax warps with d = 64; the fill and drain of the pipe per
+// item for short prompts (8 of 116 to 2000 tokens: 96 us); a chain of ~10 us (lengths, page ids, first tile,
 // softmax, result, most of it instruction fetch) for a few short rows.
 //
 // Every wait is bounded: one that runs out sets GDN_DEV_TIMEOUT and a flag
@@ -86,8 +86,10 @@ constexpr int kRows = 128;     // query rows of a tile (TMEM lanes)
 constexpr int kKeys = 128;     // keys of a tile
 constexpr int kPanel = 16384;  // 128 rows of 64 16-bit elements
 constexpr int kItems = 4;      // items between the scheduler and the other warps
-// Items are taken ahead of their turn while those that have not begun hold no more keys and values than this.
-constexpr int kAheadBytes = 512 * 1024;
+// Items are taken ahead of their turn while those that have not begun hold no more keys and values than this: what a
+// block holds no other can take at the end.  (512 KB: mixed step with a window 60 -> 64 us, eight prompts 96 -> 101;
+// 64 KB: 58 and 97.)
+constexpr int kAheadBytes = 256 * 1024;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 256;  // O after the two S buffers
 
@@ -1144,7 +1146,8 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 // Scores outside columns [lo, hi) of this thread's row become minus infinity.
 __device__ __forceinline__ void mask_scores(uint32_t t_s, int32_t lo, int32_t hi) {
 #pragma unroll 1
-    for (int q = 0; q < kKeys; q += 32) {
+    for (int q = 0; q < kKeys; q += 32) {  // (columns that all the warp's rows see stay)
+        if (!__any_sync(0xffffffffu, lo > q || hi < q + 32)) continue;
         uint32_t x[32];
         tc::tmem_ld32(t_s + q, x);
 #pragma unroll
@@ -1379,7 +1382,7 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
             if (any_row) {
                 const uint32_t t_s = tmem + b * kKeys + lanes;
                 if (__any_sync(0xffffffffu, valid && (k0 + kKeys > key_hi || k0 < key_lo)))
-                    mask_scores(t_s, key_lo - k0, key_hi - k0);
+                    mask_scores(t_s, valid ? key_lo - k0 : 0, valid ? key_hi - k0 : kKeys);
                 uint32_t x[kKeys];
                 tc::tmem_ld128(t_s, x);
                 if (Sh::kEarly) taken();
@@ -1657,19 +1660,21 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attention_kernel(const 
 constexpr int kJoinWarps = 4;
 constexpr int kJoinBlocksPerSm = 8;
 
-// Adds parts s0 + j * step (j < 4) of a row to sums[j * kMore]; a part's weight is in ml[s / 32].x of lane s % 32, lane i
-// holds columns 2 i + 64 v.
-template <int D, int kWords, int kMore>
-__device__ __forceinline__ void add_parts(const float *o, int64_t stride, int32_t s0, int32_t step, int32_t parts,
-                                          const float2 (&ml)[kWords], float2 (&sums)[3 * kMore + 1][D / 64], int lane) {
-    constexpr int kVec = D / 64;
-    float2 x[4][kVec];
+// Parts s0 + j * step (j < 4) of a row; lane i holds columns 2 i + 64 v.
+template <int D>
+__device__ __forceinline__ void read_parts(const float *o, int64_t stride, int32_t s0, int32_t step, int32_t parts,
+                                           float2 (&x)[4][D / 64], int lane) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
         if (s0 + j * step < parts)
 #pragma unroll
-            for (int v = 0; v < kVec; ++v)
+            for (int v = 0; v < D / 64; ++v)
                 x[j][v] = *reinterpret_cast<const float2 *>(o + (s0 + j * step) * stride + v * 64 + lane * 2);
+}
+// Adds them to sums[j * kMore]; a part's weight is in ml[s / 32].x of lane s % 32.
+template <int D, int kWords, int kMore>
+__device__ __forceinline__ void add_parts(const float2 (&x)[4][D / 64], int32_t s0, int32_t step, int32_t parts,
+                                          const float2 (&ml)[kWords], float2 (&sums)[3 * kMore + 1][D / 64]) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int32_t s = s0 + j * step;
@@ -1681,7 +1686,7 @@ __device__ __forceinline__ void add_parts(const float *o, int64_t stride, int32_
         }
         if (s < parts)
 #pragma unroll
-            for (int v = 0; v < kVec; ++v) {
+            for (int v = 0; v < D / 64; ++v) {
                 sums[j * kMore][v].x = fmaf(w, x[j][v].x, sums[j * kMore][v].x);
                 sums[j * kMore][v].y = fmaf(w, x[j][v].y, sums[j * kMore][v].y);
             }
@@ -1705,15 +1710,24 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 5) join_kernel(const __grid_c
     // Every thread waits for the attention kernel's end, also one with nothing to join: what follows this kernel in
     // the stream relies on both.
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // A descriptor is asked for with the number of rows: of the row that is this team's where there are as many teams.
+    const int64_t nth = blockIdx.x * static_cast<int64_t>(kJoinWarps) + warp;
+    JoinRow of_block = {0, 0, 0}, of_warp = {0, 0, 0};
+    if (lane == 0 && blockIdx.x < L.ws.max_rows) of_block = L.ws.rows[blockIdx.x];
+    if (lane == 0 && nth < L.ws.max_rows) of_warp = L.ws.rows[nth];
     const int64_t rows = *L.ws.num_rows < L.ws.max_rows ? *L.ws.num_rows : L.ws.max_rows;
     const bool alone = rows <= gridDim.x;  // a block a row
     // The rows of a block or warp, up to 32 at a time, one descriptor per lane: those that are in o already cost no
     // round of their own.
-    const int64_t teams = alone ? gridDim.x : gridDim.x * kJoinWarps, team = alone ? blockIdx.x : blockIdx.x * kJoinWarps + warp;
+    const int64_t teams = alone ? gridDim.x : gridDim.x * kJoinWarps, team = alone ? blockIdx.x : nth;
     const int64_t per = (rows + teams - 1) / teams, begin = team * per, end = begin + per < rows ? begin + per : rows;
     for (int64_t i0 = begin; i0 < end; i0 += 32) {
         JoinRow mine = {0, 0, 0};
-        if (i0 + lane < end) mine = L.ws.rows[i0 + lane];
+        if (per == 1) {
+            if (lane == 0) mine = alone ? of_block : of_warp;
+        } else if (i0 + lane < end) {
+            mine = L.ws.rows[i0 + lane];
+        }
         // (a call that timed out or was given overlapping token ranges leaves rows unwritten)
         uint32_t todo = __ballot_sync(0xffffffffu, mine.parts >= 2 && mine.parts <= kMaxSplits && mine.first >= 0 &&
                                                        mine.first + (mine.parts - 1) * h_q < L.ws.partials * h_q &&
@@ -1722,6 +1736,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 5) join_kernel(const __grid_c
             const int src = __ffs(todo) - 1;
             const int32_t row_out = __shfl_sync(0xffffffffu, mine.out, src), parts = __shfl_sync(0xffffffffu, mine.parts, src);
             const int64_t first = __shfl_sync(0xffffffffu, mine.first, src);
+            const float *o = L.ws.o + first * D;
+            const int32_t s0 = alone ? warp : 0, step = alone ? kJoinWarps : 1;
+            float2 x[4][kVec];
+            read_parts<D>(o, h_q * D, s0, step, parts, x, lane);
             float2 ml[kWords];
             float top = -INFINITY;
 #pragma unroll
@@ -1741,13 +1759,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 5) join_kernel(const __grid_c
             }
 #pragma unroll
             for (int k = 16; k > 0; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
-            const float *o = L.ws.o + first * D;
             float2 acc[kVec];
             if (alone) {
                 float2 mine4[1][kVec] = {};
 #pragma unroll 1
-                for (int32_t s = warp; s < parts; s += 4 * kJoinWarps)
-                    add_parts<D, kWords, 0>(o, h_q * D, s, kJoinWarps, parts, ml, mine4, lane);
+                for (int32_t s = warp; s < parts; s += 4 * kJoinWarps) {
+                    if (s > warp) read_parts<D>(o, h_q * D, s, step, parts, x, lane);
+                    add_parts<D, kWords, 0>(x, s, kJoinWarps, parts, ml, mine4);
+                }
                 if (warp > 0)
 #pragma unroll
                     for (int v = 0; v < kVec; ++v) sum[warp - 1][v * 32 + lane] = mine4[0][v];
@@ -1765,7 +1784,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 5) join_kernel(const __grid_c
             } else {
                 float2 four[4][kVec] = {};
 #pragma unroll 1
-                for (int32_t s = 0; s < parts; s += 4) add_parts<D, kWords, 1>(o, h_q * D, s, 1, parts, ml, four, lane);
+                for (int32_t s = 0; s < parts; s += 4) {
+                    if (s > 0) read_parts<D>(o, h_q * D, s, step, parts, x, lane);
+                    add_parts<D, kWords, 1>(x, s, 1, parts, ml, four);
+                }
 #pragma unroll
                 for (int v = 0; v < kVec; ++v) {
                     acc[v] = four[0][v];
