@@ -246,3 +246,19 @@ def test_long_contexts(gdn):
 def test_many_requests(gdn):
     lens = [(1 + 37 * i % 700, 1) for i in range(700)] + [(400, 133), (90, 90)]
     check(gdn, pu.make_case(lens, 4, 1, 64, page=16, seed=17))
+
+
+@pytest.mark.parametrize("page", [16, 32, 48, 80, 128, 256, 1088])
+def test_pages_of_short_heads(gdn, page):
+    # heads of 64: one warp loads K and V, stepping through pages that a tile's end cuts
+    lens = [(page + 1, 1), (2 * page, 5), (page - 1, page - 1), (3 * page + 7, 130), (5 * page + 300, 2)]
+    check(gdn, pu.make_case(lens, 4, 2, 64, "bf16", page=page, layout="joint", seed=18), window=page + 100)
+
+
+@pytest.mark.parametrize("window", [0, 300])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_items_of_all_kinds_after_one_another(gdn, d, window):
+    # several items per block: one, two and many key tiles, one and two row tiles, split and whole, in mixed order
+    new = [1, 130, 5, 1, 64, 33, 1, 300, 65, 2]
+    lens = [(37 * i % 900 + new[i % 10], new[i % 10]) for i in range(60)]
+    check(gdn, pu.make_case(lens, 16, 8, d, "fp16", page=32, seed=19), window=window)
