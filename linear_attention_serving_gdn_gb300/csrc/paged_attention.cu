@@ -352,8 +352,8 @@ struct Ring {
             const uint32_t n = first + t;
             return {n % Sh::kSide + (is_k ? 0 : Sh::kSide), n / Sh::kSide & 1};
         }
-        const uint32_t tile = dual ? late + 2 * t + (is_k && t == 0 ? 0 - late : is_k ? 0 : 1)
-                                   : late + 2 * t + (is_k && t == 0 ? 0 - late : is_k ? 0u - 1 : 2);
+        const uint32_t past = late + 2 * t;
+        const uint32_t tile = !is_k ? past + (dual ? 1 : 2) : t == 0 ? 0 : past - (dual ? 0 : 1);
         const uint32_t n = first + Sh::kHalves * tile + h;
         return {n % Sh::kStages, n / Sh::kStages & 1};
     }
