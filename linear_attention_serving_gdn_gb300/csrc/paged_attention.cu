@@ -260,7 +260,8 @@ struct AttentionLaunch {
     PagedAttentionArgs a;
     Workspace ws;
     int32_t group, tile_tokens, few_splits, box_rows;
-    float c;  // scale * log2(e)
+    bool o_32;  // o starts at a 32-byte boundary, and so do its rows
+    float c;    // scale * log2(e)
 };
 
 struct Item {
@@ -1217,7 +1218,7 @@ __device__ __forceinline__ void scale_o(uint32_t t_o, float f) {
     }
 }
 
-// 32 bytes at once: whole sectors from threads that each write their own row.
+// 32 bytes at once, at a multiple of 32: whole sectors from threads that each write their own row.
 __device__ __forceinline__ void store32(void *p, const uint32_t *x) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]),
                  "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
@@ -1560,7 +1561,14 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
                     for (int j = 0; j < 16; ++j)
                         o[j] = pack2<kHalf>(__uint_as_float(o[2 * j]) * f, __uint_as_float(o[2 * j + 1]) * f);
 #pragma unroll
-                    for (int j = 0; j < 16; j += 8) store32(out + q * 32 + j * 2, o + j);
+                    for (int j = 0; j < 16; j += 8) {
+                        if (L.o_32) {
+                            store32(out + q * 32 + j * 2, o + j);
+                        } else {  // the caller's o lies at a multiple of 16
+                            *reinterpret_cast<uint4 *>(out + q * 32 + j * 2) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                            *reinterpret_cast<uint4 *>(out + q * 32 + j * 2 + 8) = make_uint4(o[j + 4], o[j + 5], o[j + 6], o[j + 7]);
+                        }
+                    }
                 }
             }
         }
@@ -1891,6 +1899,7 @@ cudaError_t launch_paged_attention(const PagedAttentionArgs &a, cudaStream_t str
     L.few_splits = few_splits_of(c.h_kv);
     L.box_rows = kKeys;
     while (c.page_size % L.box_rows != 0) L.box_rows /= 2;
+    L.o_32 = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
     // A scale of zero weighs all keys alike; the least one keeps masked scores at minus infinity (0 x inf is NaN).
     L.c = fmaxf(a.scale * 1.4426950408889634f, 1e-30f);
     L.ws = workspace_at(a.workspace, a.h_q, c.h_kv, c.d, a.num_reqs, a.num_tokens, a.max_kv_len);
