@@ -1291,8 +1291,9 @@ __device__ __forceinline__ void exact_row(const AttentionLaunch &L, const Item &
 #pragma unroll
         for (int i = 16; i > 0; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
         s *= L.c;
+        // (fmaxf passes over a NaN score, whose weight has to be NaN: only a score of minus infinity has none)
         const float top = fmaxf(m, s);
-        const float f = m == top ? 1.f : ex2(m - top), p = top == -INFINITY ? 0.f : ex2(s - top);
+        const float f = m == top ? 1.f : ex2(m - top), p = s == -INFINITY ? 0.f : ex2(s - (top == -INFINITY ? 0.f : top));
         m = top;
         l = fmaf(l, f, p);
 #pragma unroll

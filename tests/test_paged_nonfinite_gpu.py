@@ -1,0 +1,74 @@
+"""NaN and infinities in what a token sees show in its output as the definition has them; in what it does not see they
+have no part in it."""
+import pytest
+import torch
+
+from tests import paged_util as pu
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def gdn():
+    import linear_attention_serving_gdn_gb300 as g
+    g.load_library()
+    return g
+
+
+HEADS = [(16, 2, 256, "bf16"), (2, 2, 256, "fp16"), (8, 2, 128, "fp16"), (5, 1, 128, "bf16"), (6, 2, 64, "bf16"), (3, 3, 64, "fp16")]
+NAN, INF = float("nan"), float("inf")
+
+
+def put(c, side, r, j, x, column=slice(None)):
+    """x into key or value j of request r, in one column of all heads or in all of them."""
+    c[side][c["table"][r, j // c["page"]].long(), j % c["page"], :, column] = x
+
+
+def check_tokens(gdn, c, window=0, step=1):
+    """Every step-th token against a request of that token alone, by the definition: NaN where that is NaN, infinite
+    where that is, and inside the tolerance elsewhere."""
+    o, st = pu.run_attention(gdn, c, window)
+    assert st == 0
+    t = 0
+    for r, (kv, m) in enumerate(c["lens"]):
+        for u in range(0, m, step):
+            one = dict(c, q=c["q"][t + u:t + u + 1], table=c["table"][r:r + 1], lens=[(kv - m + u + 1, 1)])
+            ref, tol = (x[0] for x in pu.reference(one, window))
+            got, what = o[t + u].double(), f"request {r} token {u}"
+            assert torch.equal(torch.isnan(got), torch.isnan(ref)), what
+            inf = torch.isinf(ref)
+            assert torch.equal(got[inf], ref[inf]), what
+            ok = torch.isfinite(ref)
+            pu.assert_close(got[ok], ref[ok], tol[ok], what)
+        t += m
+    return o
+
+
+@pytest.mark.parametrize("window", [0, 30])
+@pytest.mark.parametrize("h_q,h_kv,d,dtype", HEADS)
+def test_a_token_of_nan(gdn, h_q, h_kv, d, dtype, window):
+    # q, k and v of one token, not the first of its row tile: the ones before it are whole, it and those that see it NaN
+    lens = [(200, 40), (129, 129), (1500, 12), (700, 1)]
+    c = pu.make_case(lens, h_q, h_kv, d, dtype, page=16, seed=51)
+    q = c["q"].clone()
+    t = 0
+    for r, (kv, m) in enumerate(lens):
+        if m > 1:
+            u = m // 2 + 1
+            q[t + u] = NAN
+            put(c, "k", r, kv - m + u, NAN)
+            put(c, "v", r, kv - m + u, NAN)
+        t += m
+    o = check_tokens(gdn, dict(c, q=q), window, step=1 if window else 3)
+    assert torch.isnan(o[21]).all() and torch.isfinite(o[20]).all()
+
+
+@pytest.mark.parametrize("h_q,h_kv,d,dtype", HEADS)
+def test_a_score_of_nan_at_a_windows_first_key(gdn, h_q, h_kv, d, dtype):
+    # request 0: the first keys that some tokens see; request 1: at a tile's first and last key
+    c = pu.make_case([(300, 100), (400, 250)], h_q, h_kv, d, dtype, page=48, seed=52)
+    for r, j in ((0, 230), (0, 255), (1, 128), (1, 255)):
+        put(c, "k", r, j, NAN, 5)
+    put(c, "v", 0, 280, NAN, 3)
+    put(c, "v", 1, 390, INF, 4)
+    check_tokens(gdn, c, window=60, step=2)
