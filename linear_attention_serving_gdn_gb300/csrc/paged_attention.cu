@@ -1496,13 +1496,16 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
             tc::fence_after_sync();
             const float2 other = ctl->ml[row];
             dirty = __any_sync(0xffffffffu, dirty || isnan(other.x));
+            // (Both empty: factors of one.  Either half's sum may still be NaN, from scores that are, or stand for weights
+            // of a half to be computed again.)
             const float top = fmaxf(m, other.x);
+            f1 = 1.f;
             if (top > -INFINITY) {
                 f0 = ex2((m - top) * c);
                 f1 = ex2((other.x - top) * c);
                 m = top;
-                l = l * f0 + other.y * f1;
             }
+            l = l * f0 + other.y * f1;
         }
         if (writer && any_row) {
             const int64_t head = static_cast<int64_t>(it.head) * L.group + g;

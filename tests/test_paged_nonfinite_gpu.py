@@ -72,3 +72,31 @@ def test_a_score_of_nan_at_a_windows_first_key(gdn, h_q, h_kv, d, dtype):
     put(c, "v", 0, 280, NAN, 3)
     put(c, "v", 1, 390, INF, 4)
     check_tokens(gdn, c, window=60, step=2)
+
+
+@pytest.mark.parametrize("window", [1, 2])
+@pytest.mark.parametrize("h_q,h_kv,d,dtype", HEADS)
+def test_scores_of_nan_in_one_of_two_tiles(gdn, h_q, h_kv, d, dtype, window):
+    # a row tile whose tokens see one key tile or the other, and all that some of them see is NaN
+    lens = [(130, 4), (258, 5), (385, 3)]
+    c = pu.make_case(lens, h_q, h_kv, d, dtype, page=16, seed=53)
+    for r, j in ((0, 128), (1, 255), (1, 256), (2, 383), (2, 384)):
+        put(c, "k", r, j, NAN, 7)
+    check_tokens(gdn, c, window)
+
+
+@pytest.mark.parametrize("window", [0, 90])
+@pytest.mark.parametrize("h_q,h_kv,d,dtype", HEADS)
+def test_infinite_values(gdn, h_q, h_kv, d, dtype, window):
+    lens = [(500, 60), (256, 256), (900, 7)]
+    c = pu.make_case(lens, h_q, h_kv, d, dtype, page=32, seed=54, q_gain=0.5)
+    for r, (kv, m) in enumerate(lens):
+        put(c, "v", r, kv - m + 1, INF, 0)
+        put(c, "v", r, kv - m + 3, INF, d - 1)
+        put(c, "v", r, kv - m + 4, -INF, d - 1)   # both signs: NaN from here on
+        put(c, "v", r, kv - 2, -INF, 33)
+    for r, j in ((0, 380), (1, 100)):             # in earlier tokens: all see it, or with a window the first ones do
+        put(c, "v", r, j, -INF, 1)
+    put(c, "k", 1, 200, -INF, 2)                  # scores of either infinity beside an infinite value
+    put(c, "v", 1, 200, INF, 2)
+    check_tokens(gdn, c, window, step=3)
