@@ -311,11 +311,11 @@ struct Control {
     uint64_t kv_full[Shape<D>::kStages], kv_empty[Shape<D>::kStages];
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2], s_free[2], p_full[2];
-    uint64_t o_done[2], o_free[2], ml_full[2], ml_empty, item_done, scanned[2];
+    uint64_t o_done[2], o_free[2], ml_full[2], ml_empty, item_done;
     uint64_t item_full[kItems], item_empty[kItems];
     uint64_t drain[2];
     Item items[kItems];
-    uint32_t dirty[2][2];  // per warpgroup: number of the last even or odd scan that found a NaN or infinity
+    uint32_t bad[kItems];  // per item slot: number of the last item (from 1) with values left out of its products
     uint32_t tmem;
     int fail;
     // (m, l) of one warpgroup for the other; row r is only touched by the two threads of row r, in turn.
@@ -1251,68 +1251,94 @@ __device__ __forceinline__ float2 unpack2(uint32_t x) {
     return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
 }
 
-// One row (token u of the item, query head) over the item's keys that it sees,
-// key after key by one warp: for items whose values hold a NaN or infinity
-// that not all of their tokens see.  part: the partial's row, or -1.
+// Packed pairs with zeros for NaN and infinities.
+template <bool kHalf>
+__device__ __forceinline__ uint32_t finite_part(uint32_t x) {
+    constexpr uint32_t kExp = kHalf ? 0x7c00u : 0x7f80u;
+    if ((x & kExp) == kExp) x &= 0xffff0000u;
+    if ((x >> 16 & kExp) == kExp) x &= 0x0000ffffu;
+    return x;
+}
+
+// Adds to this thread's row of O, in TMEM, what the products left out: p V of the values that are NaN or infinite, over the
+// keys that the row sees of [past.x, past.y) and [next.x, next.y), which not all of the item's tokens see.  p is made anew
+// from the row's maximum.  At most the item's tokens and a window's edge of keys are looked at, whatever the context.  Out of
+// line, as leave_out is: in line they cost a prompt of 8192 tokens, which calls neither, 2 % (instruction fetch).
+struct LeftOut {
+    int2 past, next;
+    int32_t key_lo, key_hi;  // what the row sees
+    int64_t req, head;       // request, K/V head
+    const uint16_t *q;       // of the row
+    float mc;                // its maximum times c
+    uint32_t t_o, t_other;   // its accumulators: the sum of both with these factors is left in the first
+    bool two;
+    float f0, f1;
+};
 template <int D, bool kHalf>
-__device__ __forceinline__ void exact_row(const AttentionLaunch &L, const Item &it, int32_t u, int64_t head, int64_t part,
-                                          int lane) {
-    const PagedAttentionArgs &a = L.a;
-    const gdn_paged_cache_t &c = a.cache;
-    constexpr int kPairs = D / 64;  // lane i: columns 2 i + 64 v
-    int32_t hi = it.pos + u + 1, lo = a.window > 0 && hi > a.window ? hi - a.window : 0;
-    if (hi > it.hi * kKeys) hi = it.hi * kKeys;
-    if (lo < it.lo * kKeys) lo = it.lo * kKeys;
-    const int64_t tok = static_cast<int64_t>(it.tok) + u;
-    float2 q[kPairs], o[kPairs];
-#pragma unroll
-    for (int v = 0; v < kPairs; ++v) {
-        q[v] = unpack2<kHalf>(*reinterpret_cast<const uint32_t *>(a.q + tok * a.q_token_stride + head * D + v * 64 + lane * 2));
-        o[v] = make_float2(0.f, 0.f);
-    }
-    float m = -INFINITY, l = 0.f;
+__device__ __noinline__ void add_left_out(const AttentionLaunch &L, const LeftOut r) {
+    const gdn_paged_cache_t &c = L.a.cache;
+    const int lane = threadIdx.x & 31;
+    // Element 0 of key j's K or V; null: a bad page, whose keys are zeros.
+    auto key = [&](int32_t j, const void *base, int64_t page_stride, int64_t slot_stride, int64_t head_stride) {
+        const int32_t idx = j / c.page_size, page = L.a.block_table[r.req * L.a.table_stride + idx];
+        const bool good = page >= 0 && page < c.num_pages;
+        return good ? static_cast<const uint16_t *>(base) + page * page_stride + (j - idx * c.page_size) * slot_stride +
+                          r.head * head_stride
+                    : nullptr;
+    };
+    const int32_t n_past = max(r.past.y - r.past.x, 0), n = n_past + max(r.next.y - r.next.x, 0);
 #pragma unroll 1
-    for (int32_t j = lo; j < hi; ++j) {
-        const int32_t idx = j / c.page_size, in = j - idx * c.page_size;
-        const int32_t page = a.block_table[it.req * a.table_stride + idx];
-        const bool good = page >= 0 && page < c.num_pages;  // a bad page reads as zeros (and has been reported)
-        const uint16_t *k = static_cast<const uint16_t *>(c.k) + page * c.k_page_stride + in * c.k_slot_stride +
-                            it.head * c.k_head_stride;
-        const uint16_t *val = static_cast<const uint16_t *>(c.v) + page * c.v_page_stride + in * c.v_slot_stride +
-                              it.head * c.v_head_stride;
-        float s = 0.f;
-        float2 x[kPairs];
+    for (int col = 0; col < D; col += 16) {
+        uint32_t o[16];
+        tc::tmem_ld16(r.t_o + col, o);
+        if (r.two) {
+            uint32_t o1[16];
+            tc::tmem_ld16(r.t_other + col, o1);
 #pragma unroll
-        for (int v = 0; v < kPairs; ++v) {
-            const float2 y = unpack2<kHalf>(good ? *reinterpret_cast<const uint32_t *>(k + v * 64 + lane * 2) : 0u);
-            x[v] = unpack2<kHalf>(good ? *reinterpret_cast<const uint32_t *>(val + v * 64 + lane * 2) : 0u);
-            s = fmaf(q[v].y, y.y, fmaf(q[v].x, y.x, s));
+            for (int j = 0; j < 16; ++j)
+                o[j] = __float_as_uint(fmaf(__uint_as_float(o1[j]), r.f1, __uint_as_float(o[j]) * r.f0));
         }
+#pragma unroll 1
+        for (int32_t base = 0; base < n; base += 32) {
+            // A key per lane: those with such values in these columns.
+            const int32_t i = base + lane, mine = i < n_past ? r.past.x + i : r.next.x + i - n_past;
+            uint32_t top = 0;
+            if (i < n) {
+                const uint16_t *at = key(mine, c.v, c.v_page_stride, c.v_slot_stride, c.v_head_stride);
+                if (at) {
+                    const uint4 *v = reinterpret_cast<const uint4 *>(at + col);
+                    top = max_magnitude<kHalf>(max_magnitude<kHalf>(0, v[0]), v[1]);
+                }
+            }
+#pragma unroll 1
+            for (uint32_t found = __ballot_sync(0xffffffffu, not_finite<kHalf>(top)); found; found &= found - 1) {
+                const int32_t j = __shfl_sync(0xffffffffu, mine, __ffs(found) - 1);
+                const bool sees = j >= r.key_lo && j < r.key_hi;
+                float s = 0.f;
+                if (sees) {
+                    const uint32_t *k =
+                        reinterpret_cast<const uint32_t *>(key(j, c.k, c.k_page_stride, c.k_slot_stride, c.k_head_stride));
+                    const uint32_t *q = reinterpret_cast<const uint32_t *>(r.q);
+#pragma unroll 1
+                    for (int x = 0; x < D / 2; ++x) {
+                        const float2 a = unpack2<kHalf>(q[x]), b = unpack2<kHalf>(k[x]);
+                        s = fmaf(a.y, b.y, fmaf(a.x, b.x, s));
+                    }
+                }
+                const float p = ex2(fmaf(s, L.c, -r.mc));
+                const uint32_t *v =
+                    reinterpret_cast<const uint32_t *>(key(j, c.v, c.v_page_stride, c.v_slot_stride, c.v_head_stride) + col);
 #pragma unroll
-        for (int i = 16; i > 0; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
-        s *= L.c;
-        // (fmaxf passes over a NaN score, whose weight has to be NaN: only a score of minus infinity has none)
-        const float top = fmaxf(m, s);
-        const float f = m == top ? 1.f : ex2(m - top), p = s == -INFINITY ? 0.f : ex2(s - (top == -INFINITY ? 0.f : top));
-        m = top;
-        l = fmaf(l, f, p);
-#pragma unroll
-        for (int v = 0; v < kPairs; ++v) {
-            o[v].x = fmaf(o[v].x, f, p * x[v].x);
-            o[v].y = fmaf(o[v].y, f, p * x[v].y);
+                for (int x = 0; x < 8; ++x) {
+                    const uint32_t left = sees ? v[x] ^ finite_part<kHalf>(v[x]) : 0;  // (a zero where the product has it)
+                    const float2 y = unpack2<kHalf>(left);
+                    if (left & 0xffffu) o[2 * x] = __float_as_uint(fmaf(p, y.x, __uint_as_float(o[2 * x])));
+                    if (left >> 16) o[2 * x + 1] = __float_as_uint(fmaf(p, y.y, __uint_as_float(o[2 * x + 1])));
+                }
+            }
         }
-    }
-    if (part >= 0) {
-        if (lane == 0) L.ws.ml[part] = make_float2(m, l);
-#pragma unroll
-        for (int v = 0; v < kPairs; ++v) *reinterpret_cast<float2 *>(L.ws.o + part * D + v * 64 + lane * 2) = o[v];
-    } else {
-        const bool none = l == 0.f;
-        const float f = none ? 0.f : 1.f / l;
-#pragma unroll
-        for (int v = 0; v < kPairs; ++v)
-            *reinterpret_cast<uint32_t *>(a.o + (tok * a.h_q + head) * D + v * 64 + lane * 2) =
-                none ? 0u : pack2<kHalf>(o[v].x * f, o[v].y * f);
+        __syncwarp();
+        tc::tmem_st16(r.t_o + col, o);
     }
 }
 
@@ -1325,6 +1351,23 @@ __device__ __forceinline__ void value_rows(int32_t r0, int32_t r1, int32_t threa
 #pragma unroll 1
     for (int32_t i = r0 * kPieces + thread; i < r1 * kPieces; i += 128)
         f((i % kPieces / 8) * kPanel + i / kPieces * 128 + i % 8 * 16);
+}
+
+// Zeros for the values that are NaN or infinite in rows [next, next_end) and [first, past) of a V stage, and the item's
+// number `nth` in *mark.
+template <int D, bool kHalf>
+__device__ __noinline__ void leave_out(uint8_t *tile, uint32_t *mark, uint32_t nth, int32_t next, int32_t next_end, int32_t first,
+                                       int32_t past, int32_t thread) {
+    // (The mark first: of two row tiles' warpgroups, which look through the same values, one may find them left out by the
+    // other.)
+    *static_cast<volatile uint32_t *>(mark) = nth;
+    __threadfence_block();
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i)
+        value_rows<D>(i ? first : next, i ? past : next_end, thread, [&](uint32_t x) {
+            uint4 *p = reinterpret_cast<uint4 *>(tile + x);
+            *p = make_uint4(finite_part<kHalf>(p->x), finite_part<kHalf>(p->y), finite_part<kHalf>(p->z), finite_part<kHalf>(p->w));
+        });
 }
 
 template <int D, bool kHalf>
@@ -1342,7 +1385,7 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
     const float c = L.c;
     Ring<D> pos;
     uint32_t unit0 = 0;              // first unit of the item
-    uint32_t n_items = 0, ml_got = 0, scans = 0;
+    uint32_t n_items = 0, ml_got = 0;
     for (uint32_t n = 0;; ++n) {
         const uint32_t sl = n % kItems;
         if (!wait.all(ctl->item_full + sl, n / kItems & 1)) return;
@@ -1364,7 +1407,6 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
         visible_rows(it, a.window, &row_lo, &row_hi);
         const int32_t units = dual ? 2 * tiles : tiles;
         float m = -INFINITY, l = 0.f;
-        bool dirty = false;
         // (with one stream the second warpgroup writes an item's O while the first one is on with the next)
         for (int32_t j = part; j < units && (Sh::kStreams == 2 || group == 0); j += Sh::kStreams) {
             const uint32_t unit = unit0 + j, b = unit & 1;
@@ -1424,12 +1466,11 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
                 l += sum;
             }
             // A weight of zero does not keep a NaN or infinity out of the product.  Value rows that no token of the item
-            // sees are zeroed before it; where tokens see different keys of the tile, the rest is looked through, and an
-            // item that holds such a value is computed again, row by row (exact_rows).
+            // sees are zeroed before it; where tokens see different keys of the tile, the rest is looked through, and what
+            // is not finite there is left out (zeroed) and added to the rows that see it when O is written.
             const bool some = k0 + kKeys > row_hi || k0 < row_lo;
             const bool differ = it.n > 1 && (k0 + kKeys > it.pos + 1 || (a.window > 0 && it.pos + it.n - k0 > a.window));
             if (some || differ) {
-                uint32_t top = 0;  // largest magnitudes seen
 #pragma unroll 1
                 for (uint32_t h = 0; h < Sh::kHalves; ++h) {
                     // Two waits: a parity tells this fill from the one before only once that one has been consumed.
@@ -1441,22 +1482,17 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
                         value_rows<D>(0, row_lo - k0, row, [&](uint32_t x) { *reinterpret_cast<uint4 *>(tile + x) = make_uint4(0, 0, 0, 0); });
                     }
                     if (differ) {  // past the first token, and behind the last one's window
-                        const int32_t past = a.window > 0 ? it.pos + it.n - a.window - k0 : 0;
-                        value_rows<D>(it.pos + 1 - k0, row_hi - k0, row,
-                                      [&](uint32_t x) { top = max_magnitude<kHalf>(top, *reinterpret_cast<uint4 *>(tile + x)); });
-                        value_rows<D>(row_lo - k0, past, row,
-                                      [&](uint32_t x) { top = max_magnitude<kHalf>(top, *reinterpret_cast<uint4 *>(tile + x)); });
+                        const int32_t next = it.pos + 1 - k0, past = a.window > 0 ? it.pos + it.n - a.window - k0 : 0;
+                        uint32_t top = 0;  // largest magnitudes seen
+#pragma unroll 1
+                        for (int i = 0; i < 2; ++i)
+                            value_rows<D>(i ? row_lo - k0 : next, i ? past : row_hi - k0, row,
+                                          [&](uint32_t x) { top = max_magnitude<kHalf>(top, *reinterpret_cast<uint4 *>(tile + x)); });
+                        if (not_finite<kHalf>(top))
+                            leave_out<D, kHalf>(tile, ctl->bad + sl, n + 1, next, row_hi - k0, row_lo - k0, past, row);
                     }
                 }
-                if (some) tc::fence_proxy_async_smem();
-                if (differ) {
-                    if (not_finite<kHalf>(top)) ctl->dirty[w][scans & 1] = scans + 1;
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(ctl->scanned + w);
-                    if (!wait.all(ctl->scanned + w, scans & 1)) return;
-                    dirty = dirty || ctl->dirty[w][scans & 1] == scans + 1;
-                    ++scans;
-                }
+                tc::fence_proxy_async_smem();
             }
             tc::fence_before_sync();
             __syncwarp();
@@ -1466,14 +1502,13 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
         const bool pair = Sh::kStreams == 2 && !dual && tiles > 1;  // two warpgroups hold one row tile's parts
         if (Sh::kStreams == 1 && group == 0) {
             if (!wait.all(&ctl->ml_empty, (n_items & 1) ^ 1)) return;
-            ctl->ml[row] = make_float2(dirty ? nanf("") : m, l);  // (m itself is never NaN)
+            ctl->ml[row] = make_float2(m, l);
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(ctl->ml_full);
         } else if (Sh::kStreams == 1) {
             if (!wait.all(ctl->ml_full, n_items & 1)) return;
             m = ctl->ml[row].x;
             l = ctl->ml[row].y;
-            dirty = __any_sync(0xffffffffu, isnan(m));
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&ctl->ml_empty);
             if (!wait.all(&ctl->item_done, n_items & 1)) return;
@@ -1487,7 +1522,7 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
         float f0 = 1.f, f1 = 0.f;  // factors of this warpgroup's O and the other's
         const bool writer = Sh::kStreams == 2 ? dual || part == 0 : group == 1;
         if (pair && part == 1) {
-            ctl->ml[row] = make_float2(dirty ? nanf("") : m, l);
+            ctl->ml[row] = make_float2(m, l);
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(ctl->ml_full + w);
@@ -1495,9 +1530,7 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
             if (!wait.all(ctl->ml_full + (w ^ 1), ml_got++ & 1)) return;
             tc::fence_after_sync();
             const float2 other = ctl->ml[row];
-            dirty = __any_sync(0xffffffffu, dirty || isnan(other.x));
-            // (Both empty: factors of one.  Either half's sum may still be NaN, from scores that are, or stand for weights
-            // of a half to be computed again.)
+            // (Both empty: factors of one.  Either half's sum may still be NaN, from scores that are.)
             const float top = fmaxf(m, other.x);
             f1 = 1.f;
             if (top > -INFINITY) {
@@ -1520,18 +1553,11 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
                 const float inv = none ? 0.f : 1.f / l;
                 f0 *= inv;
                 f1 *= inv;
-            } else if (valid && !dirty) {
+            } else if (valid) {
                 L.ws.ml[prow] = make_float2(m * c, l);
             }
             uint16_t *out = a.o + ((static_cast<int64_t>(it.tok) + u) * a.h_q + head) * D;
             float *pout = L.ws.o + prow * D;
-            if (dirty) {
-                const int32_t count = rows - warp * 32 < 32 ? rows - warp * 32 : 32;
-#pragma unroll 1
-                for (int r = 0; r < count; ++r)
-                    exact_row<D, kHalf>(L, it, __shfl_sync(0xffffffffu, u, r), __shfl_sync(0xffffffffu, head, r),
-                                        split ? __shfl_sync(0xffffffffu, prow, r) : -1, lane);
-            }
             if (__any_sync(0xffffffffu, none)) {  // a row that saw no key
 #pragma unroll 1
                 for (int j = 0; valid && none && j < D; j += 8) {
@@ -1544,11 +1570,35 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
                 }
             }
             const bool writes = valid && !none;
+            bool two = pair;  // the row's O is in both accumulators
+            if (__any_sync(0xffffffffu, *static_cast<volatile uint32_t *>(ctl->bad + sl) == n + 1)) {
+                // Keys of the item's tiles that its tokens see differently, as they were looked through above: behind the
+                // last token's window, past the first token.
+                LeftOut left;
+                const int32_t end = it.hi * kKeys < row_hi ? it.hi * kKeys : row_hi;
+                left.past = make_int2(0, 0);
+                if (a.window > 0) left.past = make_int2(max(row_lo, it.lo * kKeys), min(it.pos + it.n - a.window, end));
+                left.next = make_int2(max(max(it.pos + 1, it.lo * kKeys), left.past.y), end);
+                left.key_lo = writes ? key_lo : INT_MAX;
+                left.key_hi = key_hi;
+                left.req = it.req;
+                left.head = it.head;
+                left.q = a.q + (static_cast<int64_t>(it.tok) + u) * a.q_token_stride + head * D;
+                left.mc = m == -INFINITY ? 0.f : m * c;
+                left.t_o = t_o + w * D;
+                left.t_other = t_o + (w ^ 1) * D;
+                left.two = pair;
+                left.f0 = f0;
+                left.f1 = f1;
+                add_left_out<D, kHalf>(L, left);
+                if (pair) f0 = 1.f;
+                two = false;
+            }
 #pragma unroll 1
-            for (int q = 0; q < D / 32 && !dirty; ++q) {
+            for (int q = 0; q < D / 32; ++q) {
                 uint32_t o[32];
                 tc::tmem_ld32(t_o + w * D + q * 32, o);
-                if (pair) {
+                if (two) {
                     uint32_t o1[32];
                     tc::tmem_ld32(t_o + (w ^ 1) * D + q * 32, o1);
 #pragma unroll
@@ -1560,7 +1610,7 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
 #pragma unroll
                         for (int j = 0; j < 32; j += 8) store32(pout + q * 32 + j, o + j);
                 } else if (writes) {
-                    const float f = pair ? 1.f : f0;
+                    const float f = two ? 1.f : f0;
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
                         o[j] = pack2<kHalf>(__uint_as_float(o[2 * j]) * f, __uint_as_float(o[2 * j + 1]) * f);
@@ -1614,12 +1664,11 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attention_kernel(const 
             tc::mbar_init(ctl->o_done + i, 1);
             tc::mbar_init(ctl->o_free + i, 4);
             tc::mbar_init(ctl->ml_full + i, 4);
-            tc::mbar_init(ctl->scanned + i, 4);
-            ctl->dirty[i][0] = ctl->dirty[i][1] = 0;
         }
         for (int i = 0; i < kItems; ++i) {
             tc::mbar_init(ctl->item_full + i, 1);
             tc::mbar_init(ctl->item_empty + i, 3 + 8);  // load and MMA warps, softmax warps
+            ctl->bad[i] = 0;
         }
         tc::mbar_init(&ctl->ml_empty, 4);
         tc::mbar_init(&ctl->item_done, 1);

@@ -100,3 +100,51 @@ def test_infinite_values(gdn, h_q, h_kv, d, dtype, window):
     put(c, "k", 1, 200, -INF, 2)                  # scores of either infinity beside an infinite value
     put(c, "v", 1, 200, INF, 2)
     check_tokens(gdn, c, window, step=3)
+
+
+@pytest.mark.parametrize("window", [0, 50])
+@pytest.mark.parametrize("h_q,h_kv,d,dtype", HEADS)
+def test_what_is_not_seen_changes_no_bit(gdn, h_q, h_kv, d, dtype, window):
+    lens = [(500, 60), (256, 256), (2000, 7), (900, 300)]
+    c = pu.make_case(lens, h_q, h_kv, d, dtype, page=32, seed=55)
+    want, _ = pu.run_attention(gdn, c, window)
+    where = [(0, 450), (0, 499), (1, 127), (1, 128), (2, 1995), (3, 610), (3, 896)]
+    for i, (r, j) in enumerate(where):
+        put(c, "v", r, j, (NAN, INF, -INF)[i % 3], 3)
+        put(c, "k", r, j, (INF, NAN)[i % 2])
+    got, st = pu.run_attention(gdn, c, window)
+    assert st == 0
+    t = 0
+    for r, (kv, m) in enumerate(lens):
+        pos = kv - m + torch.arange(m, device="cuda")
+        sees = torch.zeros(m, dtype=torch.bool, device="cuda")
+        for _, j in (x for x in where if x[0] == r):
+            sees |= (pos >= j) & ((pos - window < j) if window else True)
+        assert sees.any() and not sees.all()
+        assert torch.equal(got[t:t + m][~sees], want[t:t + m][~sees])
+        assert not torch.isfinite(got[t:t + m][sees]).all(-1).any()
+        t += m
+
+
+@pytest.mark.parametrize("h_q,h_kv,d", [(16, 2, 256), (32, 8, 128), (16, 16, 64)])
+def test_long_contexts_behind_values_that_are_not_finite(gdn, h_q, h_kv, d):
+    # What it costs goes by the chunk, not by the context: no wait may run out.  (Not split: 80 row items and more.)
+    c = pu.make_case([(100000, 1400), (300, 2)], h_q, h_kv, d, page=64, seed=56)
+    want, st = pu.run_attention(gdn, c)
+    assert st == 0
+    put(c, "v", 0, 99000, NAN, 3)
+    put(c, "v", 0, 99990, INF, 5)
+    got, st = pu.run_attention(gdn, c)
+    assert st == 0
+    same = torch.ones_like(got, dtype=torch.bool)
+    same[400:1400, :, 3] = False
+    same[1390:1400, :, 5] = False
+    assert torch.equal(got[same], want[same])
+    assert torch.isnan(got[400:1400, :, 3]).all() and bool((got[1390:1400, :, 5] == INF).all())
+    # all of the chunk after its first token, as a model that has diverged leaves it
+    j = torch.arange(98601, 100000, device="cuda")
+    for side in "kv":
+        c[side][c["table"][0, j // 64].long(), j % 64] = NAN
+    got, st = pu.run_attention(gdn, c)
+    assert st == 0
+    assert torch.equal(got[:1], want[:1]) and torch.equal(got[1400:], want[1400:]) and torch.isnan(got[1:1400]).all()
