@@ -1712,6 +1712,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attention_kernel(const 
             }
         } else {
             schedule<D>(L, ctl, wait, first_read);
+            // What follows this kernel in the stream relies on the counter's reset being over, and a block that took one
+            // item or none has not waited for it.
+            asm volatile("griddepcontrol.wait;" ::: "memory");
             // Tokens of no request: zeros.
             const PagedAttentionArgs &a = L.a;
             const int32_t end = a.num_reqs > 0 ? a.cu_seqlens[a.num_reqs] : 0;
