@@ -47,8 +47,9 @@
 // item for short prompts (8 of 116 to 2000 tokens: 96 us); a chain of ~10 us (lengths, page ids, first tile,
 // softmax, result, most of it instruction fetch) for a few short rows.
 //
-// Every wait is bounded: one that runs out sets GDN_DEV_TIMEOUT and a flag
-// that ends all the others; before the block leaves, its MMAs and copies in
+// Every wait is bounded (one for a whole item's end by the time that no tile
+// is asked for in): one that runs out sets GDN_DEV_TIMEOUT and a flag that
+// ends all the others; before the block leaves, its MMAs and copies in
 // flight are waited for and TMEM is freed.
 #include "paged.cuh"
 #include "tc_ptx.cuh"
@@ -318,6 +319,7 @@ struct Control {
     uint32_t bad[kItems];  // per item slot: number of the last item (from 1) with values left out of its products
     uint32_t tmem;
     int fail;
+    int32_t tile;  // the last that the load warp has begun, of its item
     // (m, l) of one warpgroup for the other; row r is only touched by the two threads of row r, in turn.
     float2 ml[kRows];
 };
@@ -380,6 +382,7 @@ constexpr long long kDrainCycles = 2000000000LL;
 // failure, and flags one when it runs out (the block reports it at its end).
 struct Waiter {
     volatile int *fail;
+    volatile const int32_t *tile;  // moves on while the block works on an item of many tiles
     // (try_wait suspends the thread for some microseconds by itself: a shorter limit asks without that)
     static __device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity) {
         return __all_sync(0xffffffffu,
@@ -398,6 +401,25 @@ struct Waiter {
         return true;
     }
     __device__ __forceinline__ bool all(uint64_t *bar, uint32_t parity) const { return all(tc::smem_u32(bar), parity); }
+    // For a whole item's end, which may be any time away: the limit begins anew while tiles go by.
+    __device__ __forceinline__ bool item(uint64_t *bar, uint32_t parity) const {
+        const uint32_t at = tc::smem_u32(bar);
+        if (poll(at, parity)) return true;
+        uint32_t start = static_cast<uint32_t>(clock());
+        int32_t seen = *tile;
+#pragma unroll 1
+        do {
+            const uint32_t now = static_cast<uint32_t>(clock());
+            const int32_t last = *tile;
+            if (last != seen) start = now;
+            seen = last;
+            if (__any_sync(0xffffffffu, *fail || now - start > kWaitCycles)) {
+                *fail = 1;
+                return false;
+            }
+        } while (!poll(at, parity));
+        return true;
+    }
 };
 __device__ __forceinline__ void drain_bar(uint64_t *bar, uint32_t parity) {
     const long long start = clock64();
@@ -466,7 +488,7 @@ __device__ void schedule(const AttentionLaunch &L, Control<D> *ctl, const Waiter
     bool counted = false;
     // The next item's number, taken when there is room for the item.
     auto advance = [&]() {
-        if (!wait.all(ctl->item_empty + n % kItems, (n / kItems & 1) ^ 1)) return false;
+        if (!wait.item(ctl->item_empty + n % kItems, (n / kItems & 1) ^ 1)) return false;
         auto pass = [&]() {  // the oldest item taken has begun
             ahead -= __reduce_max_sync(0xffffffffu, lane == 0 ? ctl->items[begun % kItems].hi - ctl->items[begun % kItems].lo : 0);
             ++begun;
@@ -474,7 +496,7 @@ __device__ void schedule(const AttentionLaunch &L, Control<D> *ctl, const Waiter
         if (n >= kItems && begun == n - kItems) pass();
 #pragma unroll 1
         while (ahead > kAheadTiles) {
-            if (!wait.all(ctl->item_empty + begun % kItems, begun / kItems & 1)) return false;
+            if (!wait.item(ctl->item_empty + begun % kItems, begun / kItems & 1)) return false;
             pass();
         }
         if (next < 0) {
@@ -722,6 +744,7 @@ __device__ void load_tiles(const AttentionLaunch &L, Control<D> *ctl, uint32_t q
         for (int32_t t = 0; ok && t < tiles; ++t) {
             int32_t page, row;
             where.place(&page, &row);
+            if (is_k && lane == 0) *static_cast<volatile int32_t *>(&ctl->tile) = t;
             if constexpr (Sh::kEarly) {
                 const auto [sk, parity] = pos.at(true, t, dual, 0);
                 const uint32_t sv = sk + Sh::kSide;
@@ -1506,7 +1529,7 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(ctl->ml_full);
         } else if (Sh::kStreams == 1) {
-            if (!wait.all(ctl->ml_full, n_items & 1)) return;
+            if (!wait.item(ctl->ml_full, n_items & 1)) return;
             m = ctl->ml[row].x;
             l = ctl->ml[row].y;
             __syncwarp();
@@ -1673,6 +1696,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attention_kernel(const 
         tc::mbar_init(&ctl->ml_empty, 4);
         tc::mbar_init(&ctl->item_done, 1);
         ctl->fail = 0;
+        ctl->tile = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     Request first_read = {0, 0, 0};  // the scheduler's first lengths, on their way while the block sets up
@@ -1692,7 +1716,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attention_kernel(const 
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = ctl->tmem;
-    const Waiter wait = {&ctl->fail};
+    const Waiter wait = {&ctl->fail, &ctl->tile};
     // 384 threads are launched with 168 registers each: 128 x 72 + 256 x 216 is the same sum.
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
