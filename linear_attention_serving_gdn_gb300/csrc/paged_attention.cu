@@ -1200,6 +1200,13 @@ __device__ __forceinline__ bool move_max(const uint32_t (&x)[kKeys], bool valid,
     return __any_sync(0xffffffffu, move);
 }
 
+// Weights are held as 2^7 times exp2(c (S - m)) in fp16: with the maximum that lags by up to 2^8 they reach 2^15, under its
+// largest value, and of a long context's small weights those down to 2^-32 of the largest stay (with the 2^-25 that a
+// largest weight of 1 would leave, 131 thousand keys could lose 0.4 % of the sum).  The factor is the same for the sums and
+// all parts of a row, and is gone in O / l.
+template <bool kHalf>
+constexpr float kWeightShift = kHalf ? 7.f : 0.f;
+
 // P = exp2(c S - mc) over S in TMEM; the sum of the row's weights, and with kTop the largest score.
 template <bool kHalf, bool kTop>
 __device__ __forceinline__ float store_weights(uint32_t t_s, const uint32_t (&x)[kKeys], float c, float mc, float *top) {
@@ -1478,7 +1485,8 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
                             scale_o<D>(t_o + w * D, f);
                         }
                     }
-                    sum = store_weights<kHalf, Sh::kBeside>(tmem + Sh::p_at(unit) + lanes, x, c, m == -INFINITY ? 0.f : m * c, &top);
+                    sum = store_weights<kHalf, Sh::kBeside>(tmem + Sh::p_at(unit) + lanes, x, c,
+                                                            (m == -INFINITY ? 0.f : m * c) - kWeightShift<kHalf>, &top);
                     if (!Sh::kBeside) break;
                     const bool up = valid && (top - m) * c > 8.f;
                     moved = __any_sync(0xffffffffu, up);
