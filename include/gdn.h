@@ -455,7 +455,8 @@ gdn_status_t gdn_paged_kv_write(const gdn_paged_cache_t *cache, int64_t num_toke
  * h / (h_q / h_kv):
  *     o[t][h] = sum_j softmax_j(scale * q[t][h] . K[j]) V[j]
  * A token that sees no key (p < 0) gets zeros, as do the tokens from
- * cu_seqlens[num_reqs] up to num_tokens (a captured step's padding).
+ * cu_seqlens[num_reqs], or the end of the last range that is sound, up to
+ * num_tokens (a captured step's padding).
  *
  *   num_tokens   rows of q and o; cu_seqlens[num_reqs] <= num_tokens.
  *   h_q          query heads, a multiple of cache->h_kv; h_q / h_kv <= 128.

@@ -1747,12 +1747,21 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attention_kernel(const 
             // What follows this kernel in the stream relies on the counter's reset being over, and a block that took one
             // item or none has not waited for it.
             asm volatile("griddepcontrol.wait;" ::: "memory");
-            // Tokens of no request: zeros.
+            // Tokens of no request: zeros.  (The last range may run backwards, into the tokens of a request before it.)
             const PagedAttentionArgs &a = L.a;
-            const int32_t end = a.num_reqs > 0 ? a.cu_seqlens[a.num_reqs] : 0;
+            int32_t end = a.num_reqs > 0 ? a.cu_seqlens[a.num_reqs] : 0;
+            if (end < a.num_tokens) {
+                int32_t served = 0;
+#pragma unroll 1
+                for (int64_t r = lane; r < a.num_reqs; r += 32) {
+                    const Request q = load_request(a, r, false);
+                    served = max(served, q.first + q.m);
+                }
+                end = max(end, __reduce_max_sync(0xffffffffu, served));
+            }
             const int64_t chunk = static_cast<int64_t>(a.h_q) * D / 8;
 #pragma unroll 1
-            for (int64_t i = (end > 0 ? end : 0) * chunk + blockIdx.x * 32 + lane; i < a.num_tokens * chunk; i += gridDim.x * 32)
+            for (int64_t i = end * chunk + blockIdx.x * 32 + lane; i < a.num_tokens * chunk; i += gridDim.x * 32)
                 reinterpret_cast<uint4 *>(a.o)[i] = make_uint4(0, 0, 0, 0);
         }
     } else {

@@ -14,6 +14,30 @@ def gdn():
     return g
 
 
+def behind_empty(c, n):
+    """The case's requests behind n empty ones."""
+    return dict(c, lens=[(0, 0)] * n + c["lens"],
+                table=torch.cat([torch.full((n, c["table"].shape[1]), -1, dtype=torch.int32, device="cuda"), c["table"]]),
+                cu=torch.cat([c["cu"][:1].expand(n), c["cu"]]), kv=torch.cat([torch.zeros_like(c["kv"][:1]).expand(n), c["kv"]]))
+
+
+@pytest.mark.parametrize("empty", [0, 50000])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("last", [3, 0, -1])
+def test_a_range_that_runs_backwards_leaves_the_others_whole(gdn, d, last, empty):
+    # The last request ends before it begins, inside or before the tokens of the one before it.  (Behind many empty ones the
+    # padding's zeros are written long after that one's result.)
+    c = pu.make_case([(150, 5), (60, 1)], 4, 2, d, page=16, seed=71, pad=3)
+    ref, tol = pu.reference(dict(c, lens=[(150, 5)]))
+    c["cu"][:] = torch.tensor([0, 5, last], dtype=torch.int32)
+    c = behind_empty(c, empty)
+    for _ in range(3):
+        o, st = pu.run_attention(gdn, c)
+        assert st == gdn.GDN_DEV_BAD_LENGTH
+        pu.assert_close(o[:5], ref[:5], tol[:5])
+        assert not o[5:].any()
+
+
 def test_a_captured_step_of_no_tokens_between_others(gdn):
     # More items than blocks by the bound, so that they are counted out, and contexts too short to be split: nothing but the
     # attention stands between the counter's reset and what follows.  All its lengths are zero in every other replay.
