@@ -490,7 +490,9 @@ gdn_status_t gdn_paged_attention(const gdn_paged_cache_t *cache, int32_t num_req
                                  size_t workspace_bytes, int32_t *dev_status, void *stream);
 
 /* Device scratch (bytes) of gdn_paged_attention for these sizes;
- * (size_t)-1 on a bad argument. */
+ * (size_t)-1 on a bad argument.  max_kv_len: the bound that the call is given
+ * (or more), or 0 for one that is enough for any block table and so for a call
+ * with 0; table_width * page_size asks for less. */
 size_t gdn_paged_attention_workspace_bytes(int32_t h_q, int32_t h_kv, int32_t d, int32_t num_reqs,
                                            int64_t num_tokens, int64_t max_kv_len);
 

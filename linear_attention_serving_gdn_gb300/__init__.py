@@ -645,7 +645,8 @@ def gdn_paged_kv_write(k, v, k_cache, v_cache, slot_map, dev_status=None, stream
 
 def gdn_paged_attention_workspace_bytes(h_q: int, h_kv: int, d: int, num_reqs: int, num_tokens: int,
                                         max_kv_len: int) -> int:
-    """Device scratch (bytes) of a ``gdn_paged_attention`` call of these sizes."""
+    """Device scratch (bytes) of a ``gdn_paged_attention`` call of these sizes.  ``max_kv_len``: the call's bound; for a
+    call without one, what its block table holds, or 0, which is enough for any table."""
     n = load_library().gdn_paged_attention_workspace_bytes(int(h_q), int(h_kv), int(d), int(num_reqs),
                                                            int(num_tokens), int(max_kv_len))
     if n == ctypes.c_size_t(-1).value:

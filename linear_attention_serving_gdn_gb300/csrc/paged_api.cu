@@ -112,7 +112,8 @@ size_t gdn_paged_attention_workspace_bytes(int32_t h_q, int32_t h_kv, int32_t d,
     if (h_q <= 0 || h_kv <= 0 || h_q % h_kv != 0 || h_q / h_kv > kMaxGroup || (d != 64 && d != 128 && d != 256) ||
         num_reqs < 0 || num_tokens < 0 || num_tokens > INT_MAX || max_kv_len < 0 || max_kv_len > kMaxKeys)
         return static_cast<size_t>(-1);
-    return gdn::paged_attention_workspace(h_q, h_kv, d, num_reqs, num_tokens, max_kv_len);
+    // The call takes 0 for what its block table holds, which is not known here: enough for any table.
+    return gdn::paged_attention_workspace(h_q, h_kv, d, num_reqs, num_tokens, max_kv_len > 0 ? max_kv_len : kMaxKeys);
 }
 
 gdn_status_t gdn_paged_attention(const gdn_paged_cache_t *cache, int32_t num_reqs, int64_t num_tokens, int32_t h_q,
