@@ -1290,6 +1290,13 @@ __device__ __forceinline__ uint32_t finite_part(uint32_t x) {
     return x;
 }
 
+// s + the products of a pair.
+template <bool kHalf>
+__device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float s) {
+    const float2 x = unpack2<kHalf>(a), y = unpack2<kHalf>(b);
+    return fmaf(x.y, y.y, fmaf(x.x, y.x, s));
+}
+
 // Adds to this thread's row of O, in TMEM, what the products left out: p V of the values that are NaN or infinite, over the
 // keys that the row sees of [past.x, past.y) and [next.x, next.y), which not all of the item's tokens see.  p is made anew
 // from the row's maximum.  At most the item's tokens and a window's edge of keys are looked at, whatever the context.  Out of
@@ -1316,59 +1323,61 @@ __device__ __noinline__ void add_left_out(const AttentionLaunch &L, const LeftOu
                           r.head * head_stride
                     : nullptr;
     };
-    const int32_t n_past = max(r.past.y - r.past.x, 0), n = n_past + max(r.next.y - r.next.x, 0);
+    if (r.two) {
 #pragma unroll 1
-    for (int col = 0; col < D; col += 16) {
-        uint32_t o[16];
-        tc::tmem_ld16(r.t_o + col, o);
-        if (r.two) {
-            uint32_t o1[16];
+        for (int col = 0; col < D; col += 16) {
+            uint32_t o[16], o1[16];
+            tc::tmem_ld16(r.t_o + col, o);
             tc::tmem_ld16(r.t_other + col, o1);
 #pragma unroll
             for (int j = 0; j < 16; ++j)
                 o[j] = __float_as_uint(fmaf(__uint_as_float(o1[j]), r.f1, __uint_as_float(o[j]) * r.f0));
+            tc::tmem_st16(r.t_o + col, o);
         }
+    }
+    const int32_t n_past = max(r.past.y - r.past.x, 0), n = n_past + max(r.next.y - r.next.x, 0);
 #pragma unroll 1
-        for (int32_t base = 0; base < n; base += 32) {
-            // A key per lane: those with such values in these columns.
-            const int32_t i = base + lane, mine = i < n_past ? r.past.x + i : r.next.x + i - n_past;
-            uint32_t top = 0;
-            if (i < n) {
-                const uint16_t *at = key(mine, c.v, c.v_page_stride, c.v_slot_stride, c.v_head_stride);
-                if (at) {
-                    const uint4 *v = reinterpret_cast<const uint4 *>(at + col);
-                    top = max_magnitude<kHalf>(max_magnitude<kHalf>(0, v[0]), v[1]);
-                }
+    for (int32_t base = 0; base < n; base += 32) {
+        // A key per lane: those with such values.
+        const int32_t i = base + lane, mine = i < n_past ? r.past.x + i : r.next.x + i - n_past;
+        const uint16_t *at = i < n ? key(mine, c.v, c.v_page_stride, c.v_slot_stride, c.v_head_stride) : nullptr;
+        uint32_t top = 0;
+#pragma unroll 4
+        for (int x = 0; x < D / 8; ++x)
+            if (at) top = max_magnitude<kHalf>(top, reinterpret_cast<const uint4 *>(at)[x]);
+#pragma unroll 1
+        for (uint32_t found = __ballot_sync(0xffffffffu, not_finite<kHalf>(top)); found; found &= found - 1) {
+            const int32_t j = __shfl_sync(0xffffffffu, mine, __ffs(found) - 1);
+            const bool sees = j >= r.key_lo && j < r.key_hi;
+            const uint4 *k = reinterpret_cast<const uint4 *>(key(j, c.k, c.k_page_stride, c.k_slot_stride, c.k_head_stride));
+            const uint4 *v = reinterpret_cast<const uint4 *>(key(j, c.v, c.v_page_stride, c.v_slot_stride, c.v_head_stride));
+            float s = 0.f;
+#pragma unroll 2
+            for (int x = 0; x < D / 8; ++x) {
+                if (!sees) continue;
+                const uint4 a = reinterpret_cast<const uint4 *>(r.q)[x], b = k[x];
+                s = dot2<kHalf>(a.w, b.w, dot2<kHalf>(a.z, b.z, dot2<kHalf>(a.y, b.y, dot2<kHalf>(a.x, b.x, s))));
             }
+            const float p = ex2(fmaf(s, L.c, -r.mc));
+            __syncwarp();
 #pragma unroll 1
-            for (uint32_t found = __ballot_sync(0xffffffffu, not_finite<kHalf>(top)); found; found &= found - 1) {
-                const int32_t j = __shfl_sync(0xffffffffu, mine, __ffs(found) - 1);
-                const bool sees = j >= r.key_lo && j < r.key_hi;
-                float s = 0.f;
-                if (sees) {
-                    const uint32_t *k =
-                        reinterpret_cast<const uint32_t *>(key(j, c.k, c.k_page_stride, c.k_slot_stride, c.k_head_stride));
-                    const uint32_t *q = reinterpret_cast<const uint32_t *>(r.q);
-#pragma unroll 1
-                    for (int x = 0; x < D / 2; ++x) {
-                        const float2 a = unpack2<kHalf>(q[x]), b = unpack2<kHalf>(k[x]);
-                        s = fmaf(a.y, b.y, fmaf(a.x, b.x, s));
-                    }
-                }
-                const float p = ex2(fmaf(s, L.c, -r.mc));
-                const uint32_t *v =
-                    reinterpret_cast<const uint32_t *>(key(j, c.v, c.v_page_stride, c.v_slot_stride, c.v_head_stride) + col);
+            for (int col = 0; col < D; col += 16) {
+                const uint4 lo = v[col / 8], hi = v[col / 8 + 1];
+                if (!not_finite<kHalf>(max_magnitude<kHalf>(max_magnitude<kHalf>(0, lo), hi))) continue;  // (as for all lanes)
+                const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                uint32_t o[16];
+                tc::tmem_ld16(r.t_o + col, o);
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
-                    const uint32_t left = sees ? v[x] ^ finite_part<kHalf>(v[x]) : 0;  // (a zero where the product has it)
+                    const uint32_t left = sees ? w[x] ^ finite_part<kHalf>(w[x]) : 0;  // (a zero where the product has it)
                     const float2 y = unpack2<kHalf>(left);
                     if (left & 0xffffu) o[2 * x] = __float_as_uint(fmaf(p, y.x, __uint_as_float(o[2 * x])));
                     if (left >> 16) o[2 * x + 1] = __float_as_uint(fmaf(p, y.y, __uint_as_float(o[2 * x + 1])));
                 }
+                __syncwarp();
+                tc::tmem_st16(r.t_o + col, o);
             }
         }
-        __syncwarp();
-        tc::tmem_st16(r.t_o + col, o);
     }
 }
 
