@@ -456,7 +456,13 @@ gdn_status_t gdn_paged_kv_write(const gdn_paged_cache_t *cache, int64_t num_toke
  *     o[t][h] = sum_j softmax_j(scale * q[t][h] . K[j]) V[j]
  * A token that sees no key (p < 0) gets zeros, as do the tokens from
  * cu_seqlens[num_reqs], or the end of the last range that is sound, up to
- * num_tokens (a captured step's padding).
+ * num_tokens (a captured step's padding), and as does a token all of whose
+ * scores are minus infinity.  A NaN score or value that a token sees is in its
+ * output.
+ * Scores, the softmax's maximum and sum, and the result's accumulation are
+ * fp32; each weight is rounded to the cache's dtype before it multiplies V (the
+ * sum takes it unrounded): in bf16 by at most 2^-8 of it, in fp16 by at most
+ * 2^-11 of it or 2^-32 of the row's largest.
  *
  *   num_tokens   rows of q and o; cu_seqlens[num_reqs] <= num_tokens.
  *   h_q          query heads, a multiple of cache->h_kv; h_q / h_kv <= 128.

@@ -35,17 +35,20 @@
 //              with the next item.
 //
 // The running maximum only moves when a score passes it by more than 8 (in
-// powers of two): weights are then at most 2^8, and O is rarely touched.  The rule is
-// per row, so a row's bits do not depend on its neighbours.
+// powers of two): weights are then at most 2^8 (2^15 in fp16, which holds them
+// times 2^7), and O is rarely touched.  The rule is per row, so a row's bits do
+// not depend on its neighbours.
 //
 // What bounds it: HBM for single tokens over long contexts (8 rows of 100 to
 // 131 thousand keys, 32/8 heads of 128: 3.68 GB in 545 us, 0.99 of the copy
 // peak; 256 rows of up to 4095 keys, 16/2 of 256: 6.3 TB/s); the tensor pipe
 // for long chunks (2048 tokens twice at 32 thousand keys, 16/2 of 256: 1450 to
-// 1560 us, 1.44 to 1.55 PF/s; a prompt of 8192 tokens, 32/8 of 128: 400 us,
-// 1.37 PF/s); the softmax warps with d = 64; the fill and drain of the pipe per
-// item for short prompts (8 of 116 to 2000 tokens: 96 us); a chain of ~10 us (lengths, page ids, first tile,
-// softmax, result, most of it instruction fetch) for a few short rows.
+// 1560 us, 1.44 to 1.55 PF/s; a prompt of 8192 tokens, 32/8 of 128: 385 to 419
+// us, 1.31 to 1.43 PF/s); the softmax warps with d = 64; the fill and drain of
+// the pipe per item for short prompts (8 of 116 to 2000 tokens: 95 us, the
+// tensor pipe 49 % busy); a chain of ~10 us (lengths, page ids, first tile,
+// softmax, result, part of it instruction fetch) for a few short rows.  (Ranges:
+// between boxes, whose clock differs.)
 //
 // Every wait is bounded (one for a whole item's end by the time that no tile
 // is asked for in): one that runs out sets GDN_DEV_TIMEOUT and a flag that
@@ -282,7 +285,7 @@ struct Shape {
     static constexpr int kStreams = streams_of(D);
     // A tile's maximum is sought beside its exponentials (softmax_rows) where a stream's softmax and products follow one
     // another: with d = 128 chunks of 1000 and 2000 tokens on 32 thousand keys take 822 -> 798 and 832 -> 807 us, a
-    // prompt of 8192 393 -> 387, sixteen prompts of 100 to 900 80 -> 81.  With d = 64 and 256 it costs 5 and 2 %.
+    // prompt of 8192 396 -> 385, sixteen prompts of 100 to 900 80 -> 81.  With d = 64 and 256 it costs 5 and 2 %.
     static constexpr bool kBeside = D == 128;
     static constexpr bool kEarly = D == 64;  // scores run ahead of the weights (struct Ring)
     static constexpr int kThreads = 384;
