@@ -43,12 +43,12 @@
 // 131 thousand keys, 32/8 heads of 128: 3.68 GB in 545 us, 0.99 of the copy
 // peak; 256 rows of up to 4095 keys, 16/2 of 256: 6.3 TB/s); the tensor pipe
 // for long chunks (2048 tokens twice at 32 thousand keys, 16/2 of 256: 1450 to
-// 1560 us, 1.44 to 1.55 PF/s; a prompt of 8192 tokens, 32/8 of 128: 385 to 419
-// us, 1.31 to 1.43 PF/s); the softmax warps with d = 64; the fill and drain of
+// 1560 us, 1.44 to 1.55 PF/s; a prompt of 8192 tokens, 32/8 of 128: 385 to 423
+// us, 1.30 to 1.43 PF/s); the softmax warps with d = 64; the fill and drain of
 // the pipe per item for short prompts (8 of 116 to 2000 tokens: 95 us, the
 // tensor pipe 49 % busy); a chain of ~10 us (lengths, page ids, first tile,
 // softmax, result, part of it instruction fetch) for a few short rows.  (Ranges:
-// between boxes, whose clock differs.)
+// calls apart and back to back, and between GPUs, by the clock they keep.)
 //
 // Every wait is bounded (one for a whole item's end by the time that no tile
 // is asked for in): one that runs out sets GDN_DEV_TIMEOUT and a flag that
