@@ -1764,10 +1764,10 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attention_kernel(const 
             int32_t end = a.num_reqs > 0 ? a.cu_seqlens[a.num_reqs] : 0;
             if (end < a.num_tokens) {
                 int32_t served = 0;
-#pragma unroll 1
+#pragma unroll 8
                 for (int64_t r = lane; r < a.num_reqs; r += 32) {
-                    const Request q = load_request(a, r, false);
-                    served = max(served, q.first + q.m);
+                    const int32_t b = a.cu_seqlens[r], e = a.cu_seqlens[r + 1];
+                    if (b >= 0 && b <= e && e <= a.num_tokens) served = max(served, e);
                 }
                 end = max(end, __reduce_max_sync(0xffffffffu, served));
             }
