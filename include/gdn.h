@@ -83,6 +83,7 @@ typedef enum {
 #define GDN_DEV_TIMEOUT 0x2  /* a bounded wait expired inside a kernel; its outputs are invalid */
 #define GDN_DEV_BAD_LENGTH 0x4 /* paged calls: a request's lengths are negative or exceed a stated bound; it was skipped */
 #define GDN_DEV_NO_PAGES 0x8   /* gdn_paged_maps: the free list ran out; the requests it could not serve were refused */
+#define GDN_DEV_BAD_PARENT 0x10 /* gdn_tree_maps: a node's parent does not stand before it; it was taken for a root */
 
 typedef struct {
     int32_t h_k;  /* query/key heads */
@@ -501,6 +502,142 @@ gdn_status_t gdn_paged_attention(const gdn_paged_cache_t *cache, int32_t num_req
  * with 0; table_width * page_size asks for less. */
 size_t gdn_paged_attention_workspace_bytes(int32_t h_q, int32_t h_kv, int32_t d, int32_t num_reqs,
                                            int64_t num_tokens, int64_t max_kv_len);
+
+/* ---- trees of drafted tokens ----------------------------------------------
+ *
+ * Speculative decoding in trees drafts several continuations of a request at
+ * once: its new tokens are the nodes of a tree (or of several) that hangs on
+ * its last cached token, each node following its parent.  A step that verifies
+ * the trees of a hybrid decoder is gdn_paged_maps (slots; the nodes' keys and
+ * values stand in the cache in node order), gdn_tree_maps, and per layer
+ * gdn_rotary, gdn_paged_kv_write and gdn_tree_attention, or gdn_tree_decode.
+ * What is accepted, one path from a root, is then committed: its keys and
+ * values with gdn_paged_kv_write to the slots of their positions, the states
+ * with gdn_decode_multi (tokens that fill up a shorter path: g = beta = 0).
+ *
+ * Nodes are numbered from 0 per request, in an order that puts every parent
+ * before its children; a request has at most 64.  A single token is a tree of
+ * one node, so rows without a draft ride along.
+ */
+
+/*
+ * Each node's path and position from the nodes' parents.
+ *   num_tokens   rows of parents, masks and positions.
+ *   parents      [num_tokens] int32: of node u of request r, at token
+ *                cu_seqlens[r] + u, the parent's number (< u), or -1 for a
+ *                child of the last cached token.
+ *   cu_seqlens   [num_reqs + 1] int32;  kv_lens [num_reqs] int32: cached
+ *                tokens, the nodes among them (as gdn_paged_maps gives both).
+ *   masks        [num_tokens] out: bit w is set if node w is the node or
+ *                stands above it.
+ *   positions    [num_tokens] int32 out: kv_lens[r] - nodes + depth, a root
+ *                having depth 0.
+ * Tokens from cu_seqlens[num_reqs] on get zeros.  A parent that is not before
+ * its node is taken for -1 (GDN_DEV_BAD_PARENT).  GDN_DEV_BAD_LENGTH: a
+ * request of more than 64 nodes gets zeros; one with fewer cached tokens than
+ * nodes gets positions of zero; one whose cu_seqlens run backwards or past
+ * cu_seqlens[num_reqs] or num_tokens is skipped.
+ */
+gdn_status_t gdn_tree_maps(int32_t num_reqs, int64_t num_tokens, const int32_t *parents, const int32_t *cu_seqlens,
+                           const int32_t *kv_lens, uint64_t *masks, int32_t *positions, int32_t *dev_status,
+                           void *stream);
+
+/*
+ * Attention of each request's nodes over its cached tokens and the nodes that
+ * their words name: gdn_paged_attention (without a window), but of the keys of
+ * the request's own nodes, at kv_lens[r] - nodes + w, node u sees those with
+ * w <= u and bit w of masks set.  Everything said there holds: arguments,
+ * workspace (gdn_paged_attention_workspace_bytes), roundings, refusals, and
+ * that what a node does not see has no part in its output.  A node that sees
+ * nothing (an empty word, no cached token) gets zeros.
+ *   masks        [num_tokens], as gdn_tree_maps gives them (any set of nodes
+ *                before the node will do).
+ * GDN_DEV_BAD_LENGTH: also a request of more than 64 tokens, whose outputs
+ * are zeros.
+ */
+gdn_status_t gdn_tree_attention(const gdn_paged_cache_t *cache, int32_t num_reqs, int64_t num_tokens, int32_t h_q,
+                                float scale, int64_t max_kv_len, const void *q, int64_t q_token_stride,
+                                const int32_t *block_table, int32_t table_width, int64_t table_stride,
+                                const int32_t *cu_seqlens, const int32_t *kv_lens, const uint64_t *masks, void *o,
+                                void *workspace, size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/*
+ * The gated delta rule along each row's tree: node u continues the state of
+ * its parent, a root that of the row's slot, and o is taken from its own:
+ *     S_u = alpha_u S_p - beta_u k_u (k_u^T (alpha_u S_p)) + beta_u k_u v_u^T,   o_u = scale * S_u^T q_u
+ * No state is written.  The path of node u is the set bits 0 .. u of its word;
+ * the words must be those of a tree (a node's word holds its parent's), as
+ * gdn_tree_maps gives them.
+ *   num_rows     requests;  max_nodes  bound on a row's nodes, 1 .. 64.
+ *   cu_seqlens   [num_rows + 1] int32: the tokens of each row;
+ *   masks        [num_tokens];  q, k [num_tokens][h_k][d_k], v, o
+ *                [num_tokens][h_v][d_v] bf16;  g, beta [num_tokens][h_v] fp32.
+ *   state        [num_slots][h_v][d_v][d_k] fp32, read at src_slot[r]; a
+ *                negative slot marks a padded row, whose outputs are zeros.
+ * Products with the state take each of its values to within 2^-15 of it, and
+ * so do those of the nodes among each other; sums are fp32, o is rounded once.
+ * Tokens from cu_seqlens[num_rows] on get zeros.  GDN_DEV_BAD_SLOT (a slot
+ * >= num_slots) and GDN_DEV_BAD_LENGTH (more nodes than max_nodes): zero
+ * outputs; GDN_DEV_BAD_LENGTH also for a row whose cu_seqlens run backwards or
+ * past cu_seqlens[num_rows] or num_tokens: it is skipped.
+ * A node's outputs depend on its path and the row's state alone, bit for bit:
+ * not on its siblings, the batch or max_nodes.  A NaN or infinity in a node
+ * shows in it and the nodes below it only.
+ */
+gdn_status_t gdn_tree_decode(const gdn_dims_t *dims, int32_t num_rows, int32_t max_nodes, int64_t num_tokens,
+                             const int32_t *cu_seqlens, const uint64_t *masks, const gdn_bf16 *q, const gdn_bf16 *k,
+                             const gdn_bf16 *v, const float *g, const float *beta, const float *state,
+                             int64_t num_slots, const int32_t *src_slot, gdn_bf16 *o, int32_t *dev_status,
+                             void *stream);
+
+/* ---- rotary positions ------------------------------------------------------- */
+
+/* How frequencies are stretched for contexts longer than those trained on. */
+typedef enum {
+    GDN_ROTARY_NONE = 0,
+    GDN_ROTARY_LINEAR = 1, /* all divided by factor */
+    GDN_ROTARY_NTK = 2,    /* base times factor^(rotary_dim / (rotary_dim - 2)): the slowest divided by factor */
+    GDN_ROTARY_YARN = 3    /* pairs that turn more than beta_fast times over original_length stay, those that turn less
+                              than beta_slow times are divided by factor, in between by a linear ramp over the pairs
+                              (Peng, Quesnelle, Fan, Shippole, "YaRN", ICLR 2024) */
+} gdn_rotary_scaling_t;
+
+/* Frequencies of the rotary_dim / 2 pairs on the host: pair i turns by
+ * base^(-2 i / rotary_dim) radians per position, scaled as said.  Each is given
+ * in turns, as a 64-bit fraction of one, so that position * frequency modulo
+ * one turn is an integer product.  base > 1; factor >= 1 (unless NONE);
+ * original_length, beta_fast >= beta_slow > 0 with YARN only. */
+gdn_status_t gdn_rotary_frequencies(int32_t rotary_dim, double base, int32_t scaling, double factor,
+                                    int64_t original_length, double beta_fast, double beta_slow, uint64_t *out);
+
+/* q or k of a rotation: element (t, h, i) of x at t * x_token_stride
+ * + h * x_head_stride + i, and the same for out (elements; any alignment; the
+ * width of its accesses is 16 bytes where addresses and strides allow).  out
+ * may be x, with the same strides; else the two do not overlap. */
+typedef struct {
+    const void *x;
+    void *out;
+    int32_t heads;
+    int64_t x_token_stride, x_head_stride;
+    int64_t out_token_stride, out_head_stride;
+} gdn_rotary_side_t;
+
+/*
+ * Rotary positions of q and k (either may be NULL): pair i of each head's
+ * first rotary_dim elements, (i, i + rotary_dim / 2) or interleaved (2 i,
+ * 2 i + 1), becomes magnitude * (a cos - b sin, b cos + a sin) with the angle
+ * positions[t] * frequencies[i]; the rest of the head is copied (nothing to do
+ * in place).  Any int32 position, negative ones turn backwards.
+ *   dtype        of q and k (gdn_dtype_t); arithmetic is fp32, the result is
+ *                rounded once.
+ *   d            <= 1024; rotary_dim even, <= d.
+ *   magnitude    finite; with YARN usually 0.1 ln(factor) + 1.
+ *   positions    [num_tokens] int32;  frequencies [rotary_dim / 2] in device
+ *                memory.
+ */
+gdn_status_t gdn_rotary(int32_t dtype, int64_t num_tokens, int32_t d, int32_t rotary_dim, int32_t interleaved,
+                        float magnitude, const int32_t *positions, const uint64_t *frequencies,
+                        const gdn_rotary_side_t *q, const gdn_rotary_side_t *k, void *stream);
 
 /* ---- host-only helpers (no device work) ------------------------------- */
 

@@ -18,6 +18,7 @@ Full-attention layers beside these (bfloat16 or float16, d = 64, 128 or 256):
   q, o        [T][h_q][d];  k, v [T][h_kv][d]
   k_cache, v_cache [pages][page_size][h_kv][d], any strides with d contiguous
   block_table [requests][width] int32 page ids
+Trees of drafted tokens: masks [T] int64, bit w of a node's word set for itself and the nodes above it
 """
 from __future__ import annotations
 
@@ -36,12 +37,15 @@ __all__ = [
     "gdn_floor_prefix_hit", "gdn_grid_emit_every_chunks", "gdn_status_string",
     "gdn_prefill_workspace_bytes", "gdn_status_from_device",
     "gdn_paged_maps", "gdn_paged_kv_write", "gdn_paged_attention", "gdn_paged_attention_workspace_bytes",
+    "gdn_tree_maps", "gdn_tree_attention", "gdn_tree_decode", "gdn_rotary", "gdn_rotary_frequencies",
     "EXPORTED_SYMBOLS", "GDN_DEV_BAD_SLOT", "GDN_DEV_TIMEOUT", "GDN_DEV_BAD_LENGTH", "GDN_DEV_NO_PAGES",
+    "GDN_DEV_BAD_PARENT",
 ]
 
 GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED, GDN_ERR_CUDA = 0, 1, 2, 3
 GDN_ERR_WORKSPACE, GDN_ERR_TIMEOUT = 4, 5
 GDN_DEV_BAD_SLOT, GDN_DEV_TIMEOUT, GDN_DEV_BAD_LENGTH, GDN_DEV_NO_PAGES = 0x1, 0x2, 0x4, 0x8
+GDN_DEV_BAD_PARENT = 0x10
 GDN_BF16, GDN_FP16 = 0, 1
 
 EXPORTED_SYMBOLS = (
@@ -50,6 +54,7 @@ EXPORTED_SYMBOLS = (
     "gdn_floor_prefix_hit", "gdn_grid_emit_every_chunks", "gdn_status_string",
     "gdn_prefill_workspace_bytes", "gdn_status_from_device",
     "gdn_paged_maps", "gdn_paged_kv_write", "gdn_paged_attention", "gdn_paged_attention_workspace_bytes",
+    "gdn_tree_maps", "gdn_tree_attention", "gdn_tree_decode", "gdn_rotary", "gdn_rotary_frequencies",
 )
 
 
@@ -69,6 +74,11 @@ class PagedCache(ctypes.Structure):
                 ("page_size", ctypes.c_int32), ("h_kv", ctypes.c_int32), ("d", ctypes.c_int32),
                 ("num_pages", ctypes.c_int64)] + [
                     (f"{s}_{n}_stride", ctypes.c_int64) for s in "kv" for n in ("page", "slot", "head")]
+
+
+class RotarySide(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("heads", ctypes.c_int32)] + [
+        (f"{t}_{n}_stride", ctypes.c_int64) for t in ("x", "out") for n in ("token", "head")]
 
 
 _P = ctypes.c_void_p
@@ -135,6 +145,21 @@ def _configure(lib: ctypes.CDLL) -> ctypes.CDLL:
                                         _P, _I64, _P, _I32, _I64, _P, _P, _P, _P, _SZ, _P, _P]
     lib.gdn_paged_attention_workspace_bytes.restype = _SZ
     lib.gdn_paged_attention_workspace_bytes.argtypes = [_I32, _I32, _I32, _I32, _I64, _I64]
+    lib.gdn_tree_maps.restype = ctypes.c_int
+    lib.gdn_tree_maps.argtypes = [_I32, _I64, _P, _P, _P, _P, _P, _P, _P]
+    lib.gdn_tree_attention.restype = ctypes.c_int
+    lib.gdn_tree_attention.argtypes = [_P, _I32, _I64, _I32, _F32, _I64, _P, _I64, _P, _I32, _I64, _P, _P, _P, _P, _P,
+                                       _SZ, _P, _P]
+    lib.gdn_tree_decode.restype = ctypes.c_int
+    lib.gdn_tree_decode.argtypes = [ctypes.POINTER(Dims), _I32, _I32, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _P, _P,
+                                    _P, _P]
+    lib.gdn_rotary.restype = ctypes.c_int
+    lib.gdn_rotary.argtypes = [_I32, _I64, _I32, _I32, _I32, _F32, _P, _P,
+                               _P, _P,  # the sides: a RotarySide by reference, its bytes, or None
+                               _P]
+    lib.gdn_rotary_frequencies.restype = ctypes.c_int
+    lib.gdn_rotary_frequencies.argtypes = [_I32, ctypes.c_double, _I32, ctypes.c_double, _I64, ctypes.c_double,
+                                           ctypes.c_double, _P]
     lib.gdn_prefill_num_emits.restype = _I64
     lib.gdn_prefill_num_emits.argtypes = [_P, _I32, _I32]
     lib.gdn_prefill_emit_offsets.restype = ctypes.c_int
@@ -683,9 +708,125 @@ def gdn_paged_attention(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, o
            "gdn_paged_attention")
 
 
+def _words(t, name):
+    if t.__class__ is _Tensor and t.dtype is torch.int64 and t.is_cuda and t.dim() == 1 and t.is_contiguous():
+        return t.data_ptr()
+    return _dev(t, name, torch.int64, 1).data_ptr()
+
+
+def gdn_tree_maps(parents, cu_seqlens, kv_lens, masks, positions, dev_status=None, stream=None) -> None:
+    """Words (``masks``, int64) and positions of the nodes of each request's
+    tree from their ``parents`` (see gdn.h); ``cu_seqlens`` and ``kv_lens`` as
+    ``gdn_paged_maps`` gives them."""
+    lib = _lib or load_library()
+    par, cu, kv = _i32_vec(parents, "parents"), _i32_vec(cu_seqlens, "cu_seqlens"), _i32_vec(kv_lens, "kv_lens")
+    words, pos = _words(masks, "masks"), _i32_vec(positions, "positions")
+    n, T = kv_lens.numel(), parents.numel()
+    if not (cu_seqlens.numel() == n + 1 and masks.numel() == T and positions.numel() == T):
+        raise ValueError("inconsistent tree-maps shapes")
+    _check(lib.gdn_tree_maps(n, T, par, cu, kv, words, pos, _i32_word(dev_status, "dev_status"), _stream(stream)),
+           "gdn_tree_maps")
+
+
+def gdn_tree_attention(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, masks, o, scale=None,
+                       max_kv_len: int = 0, workspace=None, dev_status=None, stream=None) -> None:
+    """Attention of each request's nodes over its cached tokens and the nodes
+    that their words name (see gdn.h); arguments as ``gdn_paged_attention``'s,
+    and the ``masks`` of ``gdn_tree_maps``."""
+    lib = _lib or load_library()
+    cache, shape = _paged_cache(k_cache, v_cache)
+    qs = _strided(q, "q", k_cache.dtype, 3)
+    o = _dev(o, "o", k_cache.dtype, 3)
+    table, rows, width, table_stride = _block_table(block_table)
+    cu, kv, words = _i32_vec(cu_seqlens, "cu_seqlens"), _i32_vec(kv_lens, "kv_lens"), _words(masks, "masks")
+    T, h_q, d = q.shape
+    n = kv_lens.numel()
+    if not (o.shape == q.shape and d == shape[3] and cu_seqlens.numel() == n + 1 and rows == n and masks.numel() == T):
+        raise ValueError("inconsistent tree-attention shapes")
+    if qs[1] != d and h_q > 1:
+        raise ValueError("q's heads must be adjacent")
+    ws = ws_bytes = 0
+    if workspace is not None:
+        workspace = _dev(workspace, "workspace", torch.uint8)
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel()
+    _check(lib.gdn_tree_attention(cache, n, T, h_q, d ** -0.5 if scale is None else scale, max_kv_len, q.data_ptr(),
+                                  qs[0], table, width, table_stride, cu, kv, words, o.data_ptr(), ws, ws_bytes,
+                                  _i32_word(dev_status, "dev_status"), _stream(stream)), "gdn_tree_attention")
+
+
+def gdn_tree_decode(q, k, v, g, beta, state, src_slot, cu_seqlens, masks, o, max_nodes: int = 64, dev_status=None,
+                    scale: float = 1.0, stream=None) -> None:
+    """The gated delta rule along each row's tree of drafted tokens, from the
+    state of its slot, which stays as it is (see gdn.h).  ``max_nodes`` bounds
+    a row's nodes."""
+    lib = _lib or load_library()
+    bf, f32 = torch.bfloat16, torch.float32
+    q, k, v = _dev(q, "q", bf, 3), _dev(k, "k", bf, 3), _dev(v, "v", bf, 3)
+    g, beta = _dev(g, "g", f32, 2), _dev(beta, "beta", f32, 2)
+    state, o = _dev(state, "state", f32, 4), _dev(o, "o", bf, 3)
+    slots, cu, words = _i32_vec(src_slot, "src_slot"), _i32_vec(cu_seqlens, "cu_seqlens"), _words(masks, "masks")
+    T, n = q.shape[0], src_slot.numel()
+    if not (k.shape == q.shape and v.shape[0] == T and o.shape == v.shape and g.shape == (T, v.shape[1])
+            and beta.shape == g.shape and cu_seqlens.numel() == n + 1 and masks.numel() == T
+            and state.shape[1:] == (v.shape[1], v.shape[2], q.shape[2])):
+        raise ValueError("inconsistent tree-decode shapes")
+    d = _dims(q, v, scale)
+    _check(lib.gdn_tree_decode(ctypes.byref(d), n, max_nodes, T, cu, words, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                               g.data_ptr(), beta.data_ptr(), state.data_ptr(), state.shape[0], slots, o.data_ptr(),
+                               _i32_word(dev_status, "dev_status"), _stream(stream)), "gdn_tree_decode")
+
+
+_ROTARY_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+_pack_side = struct.Struct("@PPiqqqq").pack  # RotarySide's layout
+
+
+def _rotary_side(x, out, name, dtype, T, d):
+    """The C description of one side (its bytes)."""
+    xs = _strided(x, name, dtype, 3)
+    os_ = xs if out is x else _strided(out, f"{name}_out", dtype, 3)
+    if x.shape[0] != T or x.shape[2] != d or out.shape != x.shape:
+        raise ValueError("inconsistent rotary shapes")
+    return _pack_side(x.data_ptr(), out.data_ptr(), x.shape[1], xs[0], xs[1], os_[0], os_[1])
+
+
+def gdn_rotary(q, k, positions, frequencies, q_out=None, k_out=None, interleaved: bool = False,
+               magnitude: float = 1.0, stream=None) -> None:
+    """Rotary positions of ``q`` ([T][h_q][d]) and ``k`` ([T][h_kv][d]; None: q
+    alone), into ``q_out`` and ``k_out`` or, where those are None, in place (see
+    gdn.h).  The first 2 * len(frequencies) elements of each head turn, in
+    halves or ``interleaved`` pairs; ``frequencies`` is the tensor of
+    ``gdn_rotary_frequencies``, on the device.  Any strides with a contiguous
+    last dimension."""
+    lib = _lib or load_library()
+    dtype = getattr(q, "dtype", None)
+    code = _PAGED_DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"q must be bfloat16 or float16, got {dtype}")
+    pos, freq = _i32_vec(positions, "positions"), _words(frequencies, "frequencies")
+    T, d = positions.numel(), q.shape[-1]
+    q_side = _rotary_side(q, q if q_out is None else q_out, "q", dtype, T, d)
+    k_side = None if k is None else _rotary_side(k, k if k_out is None else k_out, "k", dtype, T, d)
+    _check(lib.gdn_rotary(code, T, d, 2 * frequencies.numel(), bool(interleaved), magnitude, pos, freq, q_side, k_side,
+                          _stream(stream)), "gdn_rotary")
+
+
 # ---------------------------------------------------------------------------
 # host-only helpers
 # ---------------------------------------------------------------------------
+
+def gdn_rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                           original_length: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0) -> torch.Tensor:
+    """Frequencies of the ``rotary_dim`` / 2 pairs for ``gdn_rotary``, an int64
+    CPU tensor (bits of 64-bit fractions of a turn; move it to the device
+    once).  ``scaling``: "none", "linear", "ntk" or "yarn" (see gdn.h)."""
+    if scaling not in _ROTARY_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(_ROTARY_SCALINGS)}, got {scaling!r}")
+    out = torch.empty(max(int(rotary_dim), 0) // 2, dtype=torch.int64)
+    _check(load_library().gdn_rotary_frequencies(int(rotary_dim), float(base), _ROTARY_SCALINGS[scaling], float(factor),
+                                                 int(original_length), float(beta_fast), float(beta_slow),
+                                                 out.data_ptr() or None), "gdn_rotary_frequencies")
+    return out
+
 
 def gdn_prefill_num_emits(cu_seqlens_host, emit_every_chunks: int) -> int:
     keep, p = _host_i32(cu_seqlens_host, "cu_seqlens_host")

@@ -291,6 +291,41 @@ gdn_status_t gdn_prep_inputs(const gdn_dims_t *dims, int64_t num_tokens, const g
                                                                                              : GDN_ERR_CUDA;
 }
 
+gdn_status_t gdn_tree_decode(const gdn_dims_t *dims, int32_t num_rows, int32_t max_nodes, int64_t num_tokens,
+                             const int32_t *cu_seqlens, const uint64_t *masks, const gdn_bf16 *q, const gdn_bf16 *k,
+                             const gdn_bf16 *v, const float *g, const float *beta, const float *state,
+                             int64_t num_slots, const int32_t *src_slot, gdn_bf16 *o, int32_t *dev_status,
+                             void *stream) {
+    gdn_status_t why = GDN_OK;
+    if (!dims_ok(dims, &why)) return why;
+    if (num_rows < 0 || num_tokens < 0 || num_slots < 0 || max_nodes < 1 || max_nodes > 64) return GDN_ERR_INVALID_ARG;
+    if (num_tokens > INT_MAX || static_cast<int64_t>(num_rows) * dims->h_v > INT_MAX) return GDN_ERR_UNSUPPORTED;
+    if (num_rows == 0 || num_tokens == 0) return GDN_OK;
+    if (!cu_seqlens || !masks || !q || !k || !v || !g || !beta || !state || !src_slot || !o) return GDN_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(state) || !aligned16(o))
+        return GDN_ERR_INVALID_ARG;
+    gdn::TreeDecodeArgs a{};
+    a.num_rows = num_rows;
+    a.h_k = dims->h_k;
+    a.h_v = dims->h_v;
+    a.max_nodes = max_nodes;
+    a.scale = dims->scale;
+    a.num_tokens = num_tokens;
+    a.cu_seqlens = cu_seqlens;
+    a.masks = masks;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.g = g;
+    a.beta = beta;
+    a.state = state;
+    a.num_slots = num_slots;
+    a.src_slot = src_slot;
+    a.o = o;
+    a.dev_status = dev_status;
+    return gdn::launch_tree_decode(a, dims->d_k, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
 gdn_status_t gdn_decode_multi(const gdn_dims_t *dims, int32_t num_rows, int32_t tokens_per_row,
                               const gdn_bf16 *q, const gdn_bf16 *k, const gdn_bf16 *v,
                               const float *g, const float *beta, float *state, int64_t num_slots,

@@ -52,6 +52,22 @@ struct DecodeMultiArgs {
     int32_t *dev_status;
 };
 
+// Decode along trees of drafted tokens: the tokens of row r are its nodes, parents first.
+struct TreeDecodeArgs {
+    int32_t num_rows, h_k, h_v, max_nodes;
+    float scale;
+    int64_t num_tokens;
+    const int32_t *cu_seqlens;  // [num_rows + 1]
+    const uint64_t *masks;      // per token: its path, bit u for node u of its row
+    const uint16_t *q, *k, *v;
+    const float *g, *beta;
+    const float *state;
+    int64_t num_slots;
+    const int32_t *src_slot;
+    uint16_t *o;
+    int32_t *dev_status;
+};
+
 struct PrefillArgs {
     int32_t num_seqs, h_k, h_v;
     float scale;
@@ -96,6 +112,7 @@ int blocks_per_sm(Kernel kernel, int threads, int dev, int (&cache)[kMaxDevices]
 // Launchers (decode.cu, prefill.cu).  Arguments are validated by the caller.
 cudaError_t launch_decode(const DecodeArgs &a, int d, cudaStream_t stream);
 cudaError_t launch_decode_multi(const DecodeMultiArgs &a, int d, cudaStream_t stream);
+cudaError_t launch_tree_decode(const TreeDecodeArgs &a, int d, cudaStream_t stream);
 cudaError_t launch_prep(const PrepArgs &a, int d, cudaStream_t stream);
 // cu_host: host mirror of a.cu_seqlens (sizes the launch and orders the chains).
 cudaError_t launch_prefill(const PrefillArgs &a, int d, const int32_t *cu_host, cudaStream_t stream);
