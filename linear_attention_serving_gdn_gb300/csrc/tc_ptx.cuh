@@ -90,18 +90,6 @@ __device__ __forceinline__ void tma_load_4d(uint32_t smem_dst, const void *map, 
         : "memory");
 }
 
-// ---- untiled copies (both addresses and the size multiples of 16 bytes) ---------
-
-__device__ __forceinline__ void bulk_load(uint32_t smem_dst, const void *src, uint32_t bytes, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_dst), "l"(src),
-        "r"(bytes), "r"(smem_u32(bar))
-        : "memory");
-}
-__device__ __forceinline__ void bulk_prefetch_l2(const void *src, uint32_t bytes) {
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
-}
-
 // ---- fences -----------------------------------------------------------------
 
 // Generic-proxy shared-memory writes become visible to the tensor core.

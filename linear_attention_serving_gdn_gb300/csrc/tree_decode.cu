@@ -14,13 +14,13 @@
 //
 // One block per (request, value head), a warp per 32 rows of S^T (values), 16
 // at a time.
-//   1. Each warp asks for its rows of the state; q, k to shared memory.
+//   1. Each warp asks for its first rows of the state; q, k to shared memory.
 //   2. K K^T and Q K^T on the tensor cores (mma.sync, bf16: exact products).
-//   3. A thread per node walks its path, on numbers in shared memory: C and G.
-//      (Paths of more than 16 nodes by four lanes each.)
+//   3. A thread per node walks its path, in registers: C and G.  (Paths of more
+//      than 16 nodes by four lanes each, in shared memory.)
 //   4. S^T [K; Q] with the state's rows as the A operand, each value as the sum
-//      of two bf16 (2^-15 of it is left at most), straight from registers: the state is
-//      read once and never staged.
+//      of two bf16 (2^-15 of it is left at most), straight from registers: the
+//      state is read once and never staged.
 //   5. R = v - G S^T k in the accumulator's layout, which is the A layout of
 //      the last product: O^T += R^T C^T, both as sums of two bf16.
 // mma.sync and not tcgen05: with up to 32 nodes the products take less time
@@ -30,21 +30,13 @@
 // not finite stays with the nodes whose path it is on: it is left out of the
 // last product and added to those alone.
 #include "gdn_internal.cuh"
-#include "tc_ptx.cuh"
-
-#ifndef GDN_WAIT_CYCLES
-#define GDN_WAIT_CYCLES 2000000000LL  // about a second; under 2^32
-#endif
 
 namespace gdn {
 namespace {
 
-constexpr uint32_t kWaitCycles = GDN_WAIT_CYCLES;
-constexpr long long kDrainCycles = 2000000000LL;
-
 // D += A B, 16 x 8 x 16, bf16 with fp32 accumulators.
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -67,9 +59,12 @@ __device__ __forceinline__ void copy16(uint32_t to, const void *from, bool some)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(some ? 16 : 0) : "memory");
 }
 
-template <int kBytes>
-__device__ __forceinline__ void copy_small(uint32_t to, const void *from) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(kBytes) : "memory");
+__device__ __forceinline__ float4 load_state(const float *p) {
+    float4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "l"(p));
+    return v;
 }
 
 __device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
@@ -84,104 +79,18 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 // Sizes for up to NT * 8 nodes.
 template <int D, int NT>
 struct TreeShape {
+    static constexpr int kThreads = D;                         // a warp per 32 values
+    static constexpr int kBlocks = (NT <= 4 ? 512 : 384) / D;  // of an SM
     static constexpr int kNodes = 8 * NT;
     static constexpr int kCols = kNodes < 16 ? 16 : kNodes;  // whole steps of 16
     static constexpr int kGroups = D / 32;                   // of 32 state columns
-    static constexpr int kSlabs = D / 16;                    // of 16 values
-    // Warps: state loader, input loader, kPrep for C, kMain for the products with the state.
-    static constexpr int kWarps = 16, kMain = NT <= 4 ? 12 : 8, kPrep = kWarps - kMain - 2;
-    static constexpr int kRowK = 2 * D;           // bytes of a row of k or q
-    static constexpr int kRowF = kCols + 1;       // floats
-    static constexpr int kRowC = 2 * kCols + 16;  // bytes
-    static constexpr int kSlot = 16 * 4 * D;      // bytes of a slab, which lie together in the state as they do in the ring
-    // A unit's inputs, and what is made of them.
-    static constexpr int kQ = kCols * kRowK, kC = 2 * kQ, kCLo = kC + kNodes * kRowC, kWord = kCLo + kNodes * kRowC;
-    static constexpr int kG = kWord + 8 * kNodes, kBeta = kG + 4 * kNodes, kGamma = kBeta + 4 * kNodes;
-    static constexpr int kBuffer = kGamma + 4 * kNodes;
-    static constexpr int kBuffers = NT <= 2 ? 4 : NT <= 4 ? 3 : 2;
-    // k.k and q.k of the unit whose C is made, and its decays.
-    static constexpr int kFK = kBuffers * kBuffer, kFQ = kFK + kCols * kRowF * 4, kAlpha = kFQ + kCols * kRowF * 4;
-    static constexpr int kControl = (kAlpha + kNodes * 4 + 15) / 16 * 16, kControlBytes = 1024;
-    // The ring of slabs lies before all that.
-    static constexpr int kFit = (227 * 1024 - kControl - kControlBytes) / kSlot;
-    static constexpr int kSlots = kFit < 20 ? kFit : 20;
-    static constexpr int kSmem = kSlots * kSlot + kControl + kControlBytes;
-};
-
-// What a block works on: a request's value head.
-struct Unit {
-    int32_t b, m, head;  // first token, nodes (0: the end)
-    int32_t slot;
-};
-
-template <int D, int NT>
-struct TreeControl {
-    uint64_t in_full[TreeShape<D, NT>::kBuffers], in_empty[TreeShape<D, NT>::kBuffers], c_full[TreeShape<D, NT>::kBuffers];
-    uint64_t full[TreeShape<D, NT>::kSlots], empty[TreeShape<D, NT>::kSlots];
-    Unit unit[TreeShape<D, NT>::kBuffers];
-    int fail;
-    int refused;  // some unit of this block has no outputs but zeros
-};
-
-// Bounded wait of a whole warp: true for all lanes or for none.  Gives up as soon as any thread has flagged a failure,
-// and flags one when it runs out.
-struct TreeWait {
-    volatile int *fail;
-    static __device__ __forceinline__ bool poll(uint64_t *bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, kWaitCycles < 10000 ? tc::mbar_test_wait(bar, parity) : tc::mbar_try_wait(bar, parity));
-    }
-    __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity) const {
-        if (poll(bar, parity)) return true;
-        const uint32_t start = static_cast<uint32_t>(clock());
-#pragma unroll 1
-        do {
-            if (__any_sync(0xffffffffu, *fail || static_cast<uint32_t>(clock()) - start > kWaitCycles)) {
-                *fail = 1;
-                return false;
-            }
-        } while (!poll(bar, parity));
-        return true;
-    }
-};
-
-// A block's units, every gridDim.x-th; the lengths and slot of the one behind the last taken are asked for in time.
-struct Units {
-    const TreeDecodeArgs &a;
-    uint32_t next, count;
-    int32_t end;  // of the tokens that requests may have
-    int32_t b, e, slot;
-    __device__ __forceinline__ void look() {
-        if (next >= count) return;
-        const uint32_t req = next / static_cast<uint32_t>(a.h_v);
-        b = a.cu_seqlens[req];
-        e = a.cu_seqlens[req + 1];
-        slot = a.src_slot[req];
-    }
-    __device__ __forceinline__ explicit Units(const TreeDecodeArgs &args) : a(args), next(blockIdx.x), b(0), e(0), slot(0) {
-        count = static_cast<uint32_t>(a.num_rows) * static_cast<uint32_t>(a.h_v);  // (under 2^31)
-        end = a.cu_seqlens[a.num_rows];
-        if (end < 0 || end > a.num_tokens) end = static_cast<int32_t>(a.num_tokens);
-        look();
-    }
-    __device__ __forceinline__ bool sound() const { return b >= 0 && b <= e && e <= end; }
-    // A padded row, or one that cannot be served.
-    __device__ __forceinline__ bool refused() const { return slot < 0 || slot >= a.num_slots || e - b > a.max_nodes; }
-    // The next one with something to compute; `skip` is called for those that have not.
-    template <typename Skip>
-    __device__ __forceinline__ Unit take(Skip skip) {
-        Unit u = {0, 0, 0, 0};
-#pragma unroll 1
-        while (next < count && u.m == 0) {
-            const int32_t head = static_cast<int32_t>(next % static_cast<uint32_t>(a.h_v));
-            if (!sound() || (e > b && refused()))
-                skip(head);
-            else
-                u = {b, e - b, head, slot};
-            next += gridDim.x;
-            look();
-        }
-        return u;
-    }
+    static constexpr int kAhead = NT <= 2 ? kGroups : 2;     // groups of the state in registers
+    static constexpr int kRowK = 2 * D;                      // bytes of a row of k or q
+    // A node's row of the products is 4 kCols bytes and 16 more: 4-byte reads of 8 rows x 4 lanes meet no bank twice.  Its row
+    // of C takes the place of its q.k: upper halves, then the rests.
+    static constexpr int kRowF = kCols + 4, kRowC = 4 * kRowF, kLo = 2 * kCols;
+    static constexpr int kQ = kCols * kRowK, kFK = 2 * kQ, kFQ = kFK + kCols * kRowC, kWord = kFQ + kCols * kRowC, kGate = kWord + 8 * kNodes;
+    static constexpr int kSmem = kGate + 3 * kNodes * 4;
 };
 
 // Offset of a 16-byte piece of a row of k or q: odd rows have the halves of each 128 bytes changed over, so that eight
@@ -201,6 +110,7 @@ __device__ __forceinline__ void products(const uint8_t *sk, const uint8_t *sq, i
 #pragma unroll
     for (int g = 0; g < Sh::kGroups; ++g) {
         uint4 b[kTiles];
+        uint32_t f[2][2][4];
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) b[t] = *reinterpret_cast<const uint4 *>(sk + piece_at<D>(ct * 16 + t * 8 + r, g * 4 + c));
 #pragma unroll
@@ -208,433 +118,366 @@ __device__ __forceinline__ void products(const uint8_t *sk, const uint8_t *sq, i
             const uint8_t *rows = x ? sq : sk;
             const uint4 a0 = *reinterpret_cast<const uint4 *>(rows + piece_at<D>(rt * 16 + r, g * 4 + c));
             const uint4 a1 = *reinterpret_cast<const uint4 *>(rows + piece_at<D>(rt * 16 + r + 8, g * 4 + c));
-            const uint32_t f0[4] = {a0.x, a1.x, a0.y, a1.y}, f1[4] = {a0.z, a1.z, a0.w, a1.w};
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t) {
-                mma(acc[x][t], f0, b[t].x, b[t].y);
-                mma(acc[x][t], f1, b[t].z, b[t].w);
-            }
+            f[x][0][0] = a0.x, f[x][0][1] = a1.x, f[x][0][2] = a0.y, f[x][0][3] = a1.y;
+            f[x][1][0] = a0.z, f[x][1][1] = a1.z, f[x][1][2] = a0.w, f[x][1][3] = a1.w;
         }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int t = 0; t < kTiles; ++t) mma(acc[x][t], f[x][h], h ? b[t].z : b[t].x, h ? b[t].w : b[t].y);
     }
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
             float *p = (x ? fq : fk) + (rt * 16 + r) * Sh::kRowF + ct * 16 + t * 8 + 2 * c;
-            p[0] = acc[x][t][0];
-            p[1] = acc[x][t][1];
-            p[8 * Sh::kRowF] = acc[x][t][2];
-            p[8 * Sh::kRowF + 1] = acc[x][t][3];
+            *reinterpret_cast<float2 *>(p) = make_float2(acc[x][t][0], acc[x][t][1]);
+            *reinterpret_cast<float2 *>(p + 8 * Sh::kRowF) = make_float2(acc[x][t][2], acc[x][t][3]);
         }
 }
 
-// Node u's walk up its path: row[x] is p.k_x of the nodes x that are still above, first q_u.k_x; node w leaves its c there,
-// and p' = a (p - c k_w) changes the others by k_w.k_x.  Gives the product of the decays.  With kLanes = 4 a quad
-// takes the nodes above in turn; what one lane has written is another's c four nodes on.
+// Node u's walk up its path.  g_x is p.k_x of the nodes x that are still above, first q_u.k_x (in `row`); node w's c is
+// b_w g_w, and p' = a_w (p - c k_w) changes the others by k_w.k_x.  C[u] takes the row's place, as sums of two bf16, zeros
+// off the path.  Gives the product of the decays.
+//
+// Of up to kShortPath nodes the walk is held in registers, place by place: nothing waits but a step's c for the one
+// before.  (A quad a node with its numbers in shared memory took 4000 cycles for 64 nodes, this takes 1000.)
 constexpr int kShortPath = 16;
-template <int NT, int kLanes>
-__device__ __forceinline__ float walk(uint64_t path, float *row, const float *fk, int stride, const float *alpha,
-                                      const float *beta, int sub) {
-    constexpr uint64_t kMine = kLanes == 1 ? ~0ull : 0x1111111111111111ull;
-    const uint32_t quad = kLanes == 1 ? 0 : 0xfu << (threadIdx.x & 28);
+
+template <int D, int NT>
+__device__ __forceinline__ float walk_short(uint64_t path, int most, float *row, const float *fk, const float *alpha, const float *beta) {
+    using Sh = TreeShape<D, NT>;
+    constexpr int kMost = 8 * NT < kShortPath ? 8 * NT : kShortPath;
+    const int steps = __popcll(path);
+    int x[kMost];
+    float g[kMost];
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {  // (behind the last one: it again)
+        const int w = NT <= 4 ? 31 - __clz(static_cast<uint32_t>(path)) : 63 - __clzll(static_cast<long long>(path));
+        x[i] = path ? w : i > 0 ? x[i > 0 ? i - 1 : 0] : 0;
+        path &= ~(1ull << x[i]);
+        g[i] = row[x[i]];
+    }
+    asm volatile("" ::: "memory");  // (the row is read as floats, then written as other types)
+#pragma unroll
+    for (int i = 0; i < Sh::kCols / 4; ++i) reinterpret_cast<uint4 *>(row)[i] = make_uint4(0, 0, 0, 0);
+    asm volatile("" ::: "memory");
+    uint16_t *const hi = reinterpret_cast<uint16_t *>(row), *const lo = hi + Sh::kLo / 2;
+    float decay = 1.f;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+        if (i >= most) break;  // (the warp's longest)
+        const float a = alpha[x[i]], c = beta[x[i]] * g[i], ac = -a * c;
+        if (i < steps) {
+            hi[x[i]] = static_cast<uint16_t>(__float_as_uint(c) >> 16);
+            lo[x[i]] = float_to_bf16_bits(c - __uint_as_float(__float_as_uint(c) & 0xffff0000u));
+            decay *= a;
+        }
+#pragma unroll
+        for (int j = i + 1; j < kMost; ++j) g[j] = fmaf(ac, fk[x[i] * Sh::kRowF + x[j]], a * g[j]);
+    }
+    return decay;
+}
+
+// A path of any length, on `row` itself: a quad takes the nodes above in turn, and what one lane has written is another's c
+// four nodes on.  The same operations, and so the same bits.
+template <int D, int NT>
+__device__ __forceinline__ float walk_long(const uint64_t path, float *row, const float *fk, const float *alpha, const float *beta, int sub) {
+    using Sh = TreeShape<D, NT>;
+    const uint32_t quad = 0xfu << (threadIdx.x & 28);
     float decay = 1.f;
 #pragma unroll 1
-    while (path) {
-        const int w = NT <= 4 ? 31 - __clz(static_cast<uint32_t>(path)) : 63 - __clzll(static_cast<long long>(path));
-        path ^= 1ull << w;
+    for (uint64_t left = path; left;) {
+        const int w = 63 - __clzll(static_cast<long long>(left));
+        left ^= 1ull << w;
         const float a = alpha[w], c = beta[w] * row[w], ac = -a * c;
-        if (kLanes > 1) __syncwarp(quad);
+        __syncwarp(quad);
         if (sub == 0) row[w] = c;
         decay *= a;
-        const float *const kk = fk + w * stride;
-        uint64_t mine = path & (kMine << sub);
+        const float *const kk = fk + w * Sh::kRowF;
+        uint64_t mine = left & (0x1111111111111111ull << sub);
 #pragma unroll 1
         while (mine) {
             int x[4];
             float y[4], z[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {  // (past the last one: it again)
-                if (NT <= 4) {
-                    const uint32_t b = static_cast<uint32_t>(mine);
-                    x[i] = b ? __ffs(static_cast<int>(b)) - 1 : x[i > 0 ? i - 1 : 0];
-                    mine = b & (b - 1);
-                } else {
-                    x[i] = mine ? __ffsll(static_cast<long long>(mine)) - 1 : x[i > 0 ? i - 1 : 0];
-                    mine &= mine - 1;
-                }
+                x[i] = mine ? __ffsll(static_cast<long long>(mine)) - 1 : x[i > 0 ? i - 1 : 0];
+                mine &= mine - 1;
                 y[i] = row[x[i]];
                 z[i] = kk[x[i]];
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) row[x[i]] = fmaf(ac, z[i], a * y[i]);
         }
-        if (kLanes > 1) __syncwarp(quad);
+        __syncwarp(quad);
+    }
+    // The row to its sums of two bf16: read by the quad, then written.
+    float2 c[Sh::kCols / 8];
+#pragma unroll
+    for (int i = 0; i < Sh::kCols / 8; ++i) {
+        const int w = 2 * (sub + 4 * i);
+        c[i] = *reinterpret_cast<const float2 *>(row + w);
+        if (!(path >> w & 1)) c[i].x = 0.f;
+        if (!(path >> w & 2)) c[i].y = 0.f;
+    }
+    __syncwarp(quad);
+#pragma unroll
+    for (int i = 0; i < Sh::kCols / 8; ++i) {
+        uint32_t *const to = reinterpret_cast<uint32_t *>(row) + sub + 4 * i;
+        split2(c[i].x, c[i].y, to, to + Sh::kLo / 4);
     }
     return decay;
 }
 
-// ---- the loader of the state -----------------------------------------------------
-
 template <int D, int NT>
-__device__ void load_states(const TreeDecodeArgs &a, TreeControl<D, NT> *ctl, uint8_t *ring, const TreeWait &wait) {
+__global__ void __launch_bounds__(TreeShape<D, NT>::kThreads, TreeShape<D, NT>::kBlocks) tree_decode_kernel(const __grid_constant__ TreeDecodeArgs a) {
     using Sh = TreeShape<D, NT>;
-    const int lane = threadIdx.x & 31;
-    Units units(a);
-    uint32_t q = 0;  // slabs asked for
-    bool ok = true;
-    while (ok) {
-        const Unit u = units.take([](int32_t) {});
-        if (u.m == 0) break;
-        const float *const from = a.state + (static_cast<int64_t>(u.slot) * a.h_v + u.head) * (D * D);
-#pragma unroll 1
-        for (int slab = 0; slab < Sh::kSlabs; ++slab, ++q) {
-            const uint32_t at = q % Sh::kSlots;
-            ok = wait(ctl->empty + at, (q / Sh::kSlots & 1) ^ 1);
-            if (!ok) break;
-            if (lane == 0) {
-                tc::mbar_expect_tx(ctl->full + at, Sh::kSlot);
-                tc::bulk_load(tc::smem_u32(ring + at * Sh::kSlot), from + slab * (16 * D), Sh::kSlot, ctl->full + at);
-            }
-            __syncwarp();
+    extern __shared__ __align__(16) uint8_t smem[];
+    uint8_t *const sk = smem, *const sq = smem + Sh::kQ;
+    float *const fk = reinterpret_cast<float *>(smem + Sh::kFK), *const fq = reinterpret_cast<float *>(smem + Sh::kFQ);
+    const uint8_t *const chi = smem + Sh::kFQ, *const clo = chi + Sh::kLo;
+    uint64_t *const word = reinterpret_cast<uint64_t *>(smem + Sh::kWord);
+    float *const alpha = reinterpret_cast<float *>(smem + Sh::kGate), *const beta = alpha + Sh::kNodes, *const gamma = beta + Sh::kNodes;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
+    const int32_t req = blockIdx.x / a.h_v, head = blockIdx.x - req * a.h_v, head_k = head / (a.h_v / a.h_k);
+    const int32_t b = a.cu_seqlens[req], e = a.cu_seqlens[req + 1], slot = a.src_slot[req];
+    int32_t end = a.cu_seqlens[a.num_rows];
+    if (end < 0 || end > a.num_tokens) end = static_cast<int32_t>(a.num_tokens);
+    // Tokens behind the last request's: zeros, dealt out over the blocks.
+    if (end < a.num_tokens) {
+        const int64_t pieces = static_cast<int64_t>(a.h_v) * (D / 8);
+        for (int64_t i = end * pieces + static_cast<int64_t>(blockIdx.x) * Sh::kThreads + tid; i < a.num_tokens * pieces;
+             i += static_cast<int64_t>(gridDim.x) * Sh::kThreads)
+            reinterpret_cast<uint4 *>(a.o)[i] = make_uint4(0, 0, 0, 0);
+    }
+    if (b < 0 || b > e || e > end) {
+        if (tid == 0 && head == 0) report(a.dev_status, GDN_DEV_BAD_LENGTH);
+        return;
+    }
+    const int32_t m = e - b;
+    if (m == 0) return;
+    if (slot < 0 || slot >= a.num_slots || m > a.max_nodes) {  // a padded row, or one that cannot be served
+        if (tid == 0 && head == 0 && slot >= a.num_slots) report(a.dev_status, GDN_DEV_BAD_SLOT);
+        if (tid == 0 && head == 0 && m > a.max_nodes) report(a.dev_status, GDN_DEV_BAD_LENGTH);
+        for (int64_t i = tid; i < static_cast<int64_t>(m) * (D / 8); i += Sh::kThreads)
+            reinterpret_cast<uint4 *>(a.o + ((b + i / (D / 8)) * a.h_v + head) * D)[i % (D / 8)] = make_uint4(0, 0, 0, 0);
+        return;
+    }
+
+    // 1. The state's rows 32 warp + r and + 8, in groups of 32 columns: 8 neighbouring columns a lane.
+    const float *const s_row = a.state + ((static_cast<int64_t>(slot) * a.h_v + head) * D + warp * 32 + r) * D + c * 8;
+    float4 s[Sh::kAhead][4];
+    auto ask = [&](int g) {  // group g, counted over both 16 rows
+        float4(&x)[4] = s[g % Sh::kAhead];
+        const float *p = s_row + (g / Sh::kGroups) * (16 * D) + (g % Sh::kGroups) * 32;
+        x[0] = load_state(p);
+        x[1] = load_state(p + 4);
+        x[2] = load_state(p + 8 * D);
+        x[3] = load_state(p + 8 * D + 4);
+    };
+#pragma unroll
+    for (int g = 0; g < Sh::kAhead; ++g) ask(g);
+    {
+        // (each thread's rows are 8 apart, so their parity and the piece's place stay)
+        const int row = tid / (D / 8), piece = tid % (D / 8);
+        const int64_t first = ((static_cast<int64_t>(b) + row) * a.h_k + head_k) * D + piece * 8, step = static_cast<int64_t>(8) * a.h_k * D;
+        uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(sk + piece_at<D>(row, piece)));
+        const uint16_t *k = a.k + first, *q = a.q + first;
+        for (int u = row; u < ((m + 15) & ~15); u += 8, k += step, q += step, to += 8 * Sh::kRowK) {
+            copy16(to, u < m ? k : a.k, u < m);
+            copy16(to + Sh::kQ, u < m ? q : a.q, u < m);
         }
     }
-    if (static_cast<uint32_t>(lane) < Sh::kSlots && static_cast<uint32_t>(lane) < q) {  // copies in flight land before the block leaves
-        const uint32_t last = q - 1 - (q - 1 - lane) % Sh::kSlots;  // into slot `lane`
-        const long long start = clock64();
-        while (!tc::mbar_try_wait(ctl->full + lane, last / Sh::kSlots & 1) && clock64() - start < kDrainCycles) {}
-    }
-    __syncwarp();
-}
-
-// ---- the loader of the inputs ------------------------------------------------------
-
-template <int D, int NT>
-__device__ void load_inputs(const TreeDecodeArgs &a, TreeControl<D, NT> *ctl, uint8_t *smem, const TreeWait &wait) {
-    using Sh = TreeShape<D, NT>;
-    const int lane = threadIdx.x & 31;
-    const int32_t ratio = a.h_v / a.h_k;
-    Units units(a);
-    for (uint32_t n = 0;; ++n) {
-        const Unit u = units.take([&](int32_t head) {
-            if (lane > 0) return;
-            if (!units.sound()) {
-                if (head == 0) report(a.dev_status, GDN_DEV_BAD_LENGTH);
-                return;
-            }
-            ctl->refused = 1;
-            if (head == 0 && units.slot >= a.num_slots) report(a.dev_status, GDN_DEV_BAD_SLOT);
-            if (head == 0 && units.e - units.b > a.max_nodes) report(a.dev_status, GDN_DEV_BAD_LENGTH);
-        });
-        const uint32_t x = n % Sh::kBuffers;
-        if (!wait(ctl->in_empty + x, (n / Sh::kBuffers & 1) ^ 1)) break;
-        uint8_t *const to = smem + x * Sh::kBuffer;
-        if (lane == 0) {
-            ctl->unit[x] = u;
-            tc::mbar_arrive(ctl->in_full + x);
-        }
-        __syncwarp();
-        if (u.m > 0) {
-            constexpr int kPieces = D / 8;
-            const int row = lane / kPieces, piece = lane % kPieces;
-            const int64_t step = static_cast<int64_t>(a.h_k) * D;
-            const uint16_t *k = a.k + ((static_cast<int64_t>(u.b) + row) * a.h_k + u.head / ratio) * D + piece * 8;
-            const uint16_t *q = a.q + (k - a.k);
-            const uint32_t at = tc::smem_u32(to);
-#pragma unroll 4
-            for (int i = row; i < ((u.m + 15) & ~15); i += 32 / kPieces, k += step * (32 / kPieces), q += step * (32 / kPieces)) {
-                copy16(at + piece_at<D>(i, piece), i < u.m ? k : a.k, i < u.m);
-                copy16(at + Sh::kQ + piece_at<D>(i, piece), i < u.m ? q : a.q, i < u.m);
-            }
-            for (int i = lane; i < u.m; i += 32) {
-                const int64_t t = static_cast<int64_t>(u.b) + i;
-                copy_small<8>(at + Sh::kWord + i * 8, a.masks + t);
-                copy_small<4>(at + Sh::kG + i * 4, a.g + t * a.h_v + u.head);
-                copy_small<4>(at + Sh::kBeta + i * 4, a.beta + t * a.h_v + u.head);
-                tc::bulk_prefetch_l2(a.v + (t * a.h_v + u.head) * D, 2 * D);
-            }
-        }
-        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(ctl->in_full + x)) : "memory");
-        if (u.m == 0) break;
+    uint64_t path = 0;  // of node tid, as long as there is one (itself and nodes before it)
+    if (tid < Sh::kNodes) {
+        const int64_t at = static_cast<int64_t>(b) + tid;
+        if (tid < m) path = a.masks[at] & ((2ull << tid) - 1);
+        word[tid] = path;
+        alpha[tid] = tid < m ? expf(a.g[at * a.h_v + head]) : 0.f;
+        beta[tid] = tid < m ? a.beta[at * a.h_v + head] : 0.f;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-}
+    const bool deep = __syncthreads_or(__popcll(path) > kShortPath);
 
-// ---- the warps that make C -------------------------------------------------------------
-
-template <int D, int NT>
-__device__ void make_c(TreeControl<D, NT> *ctl, uint8_t *smem, const TreeWait &wait, int warp) {
-    using Sh = TreeShape<D, NT>;
-    constexpr int kThreads = Sh::kPrep * 32;
-    const int lane = threadIdx.x & 31, tid = warp * 32 + lane;
-    float *const fk = reinterpret_cast<float *>(smem + Sh::kFK), *const fq = reinterpret_cast<float *>(smem + Sh::kFQ);
-    float *const alpha = reinterpret_cast<float *>(smem + Sh::kAlpha);
-    auto meet = [] { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kThreads) : "memory"); };
-    // The same, and whether any warp is on its way out: then all are.
-    auto leave = [](bool out) {
-        uint32_t any;
-        asm volatile(
-            "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-            : "=r"(any)
-            : "r"(static_cast<uint32_t>(out)), "n"(kThreads)
-            : "memory");
-        return any != 0;
-    };
-    for (uint32_t n = 0;; ++n) {
-        const uint32_t x = n % Sh::kBuffers;
-        const int32_t m = wait(ctl->in_full + x, n / Sh::kBuffers & 1) ? ctl->unit[x].m : 0;
-        if (m == 0) {
-            leave(true);
-            return;
-        }
-        uint8_t *const in = smem + x * Sh::kBuffer;
-        uint64_t *const word = reinterpret_cast<uint64_t *>(in + Sh::kWord);
-        float *const beta = reinterpret_cast<float *>(in + Sh::kBeta), *const gamma = reinterpret_cast<float *>(in + Sh::kGamma);
-        for (int u = tid; u < Sh::kNodes; u += kThreads) {
-            word[u] = u < m ? word[u] & ((2ull << u) - 1) : 0;  // (itself and nodes before it)
-            alpha[u] = u < m ? expf(reinterpret_cast<const float *>(in + Sh::kG)[u]) : 0.f;
-        }
+    // 2. k.k and q.k of nodes and those before them.
+    {
         int task = warp;
 #pragma unroll 1
         for (int rt = 0; rt * 16 < m; ++rt) {
 #pragma unroll 1
-            for (; task <= rt; task += Sh::kPrep) products<D, NT>(in, in + Sh::kQ, rt, task, fk, fq, lane);
+            for (; task <= rt; task += D / 32) products<D, NT>(sk, sq, rt, task, fk, fq, lane);
             task -= rt + 1;
         }
-        if (leave(false)) return;
-        bool deep = false;
-        for (int u = lane; u < Sh::kNodes; u += 32) deep |= __popcll(word[u]) > kShortPath;
-        if (!__any_sync(0xffffffffu, deep)) {
-            for (int u = tid; u < Sh::kNodes; u += kThreads)
-                gamma[u] = u < m ? walk<NT, 1>(word[u], fq + u * Sh::kRowF, fk, Sh::kRowF, alpha, beta, 0) : 0.f;
-        } else {
-#pragma unroll 1
-            for (int u = tid >> 2; u < Sh::kNodes; u += kThreads / 4) {  // (whole quads: one node's lanes stay together)
-                const float g = u < m ? walk<NT, 4>(word[u], fq + u * Sh::kRowF, fk, Sh::kRowF, alpha, beta, lane & 3) : 0.f;
-                if ((lane & 3) == 0) gamma[u] = g;
-            }
-        }
-        meet();
-        // As sums of two bf16; zeros off the path.
-        constexpr int kPairs = Sh::kCols / 2;
-#pragma unroll 1
-        for (int i = tid; i < Sh::kNodes * kPairs; i += kThreads) {
-            const int u = i / kPairs, w = i % kPairs * 2;
-            const uint64_t on = word[u];
-            uint32_t hi, lo;
-            split2(on >> w & 1 ? fq[u * Sh::kRowF + w] : 0.f, on >> w & 2 ? fq[u * Sh::kRowF + w + 1] : 0.f, &hi, &lo);
-            *reinterpret_cast<uint32_t *>(in + Sh::kC + u * Sh::kRowC + w * 2) = hi;
-            *reinterpret_cast<uint32_t *>(in + Sh::kCLo + u * Sh::kRowC + w * 2) = lo;
-        }
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(ctl->c_full + x);
-        meet();  // the products are not written again before all are done with them
     }
-}
-
-// ---- the warps of the products with the state ----------------------------------------------
-
-template <int D, int NT>
-__device__ void multiply(const TreeDecodeArgs &a, TreeControl<D, NT> *ctl, uint8_t *smem, uint8_t *ring, const TreeWait &wait, int warp) {
-    using Sh = TreeShape<D, NT>;
-    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-    uint32_t q = warp;  // this warp's next slab, of all the block's
-    for (uint32_t n = 0;; ++n) {
-        const uint32_t buffer = n % Sh::kBuffers;
-        if (!wait(ctl->in_full + buffer, n / Sh::kBuffers & 1)) return;
-        const Unit unit = ctl->unit[buffer];
-        if (unit.m == 0) return;
-        const int32_t m = unit.m;
-        const uint8_t *const sk = smem + buffer * Sh::kBuffer, *const sq = sk + Sh::kQ;
-        const uint64_t *const word = reinterpret_cast<const uint64_t *>(sk + Sh::kWord);
-        const float *const gamma = reinterpret_cast<const float *>(sk + Sh::kGamma);
-#pragma unroll 1
-        for (; q < (n + 1) * Sh::kSlabs; q += Sh::kMain) {
-            const uint32_t slab = q - n * Sh::kSlabs, slot = q % Sh::kSlots;
-            const int64_t value = (static_cast<int64_t>(unit.b) * a.h_v + unit.head) * D + slab * 16;  // node 0's first of the slab
-            // v of node 8 t + r, values 2c and 2c + 1, and 8 further on.
-            uint32_t v[NT][2];
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                v[t][0] = v[t][1] = 0;
-                if (t * 8 + r < m) {
-                    const uint32_t *p = reinterpret_cast<const uint32_t *>(a.v + value + static_cast<int64_t>(t * 8 + r) * a.h_v * D) + c;
-                    v[t][0] = __ldg(p);
-                    v[t][1] = __ldg(p + 4);
-                }
-            }
-            if (!wait(ctl->full + slot, q / Sh::kSlots & 1)) return;
-            // S^T [K; Q]: 16 values by the nodes.
-            const float *const rows = reinterpret_cast<const float *>(ring + slot * Sh::kSlot) + r * D + c * 8;
-            float y[NT][4], o[NT][4];
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) y[t][i] = o[t][i] = 0.f;
-#pragma unroll
-            for (int g = 0; g < Sh::kGroups; ++g) {
-                const float4 x0 = *reinterpret_cast<const float4 *>(rows + g * 32), x1 = *reinterpret_cast<const float4 *>(rows + g * 32 + 4);
-                const float4 x2 = *reinterpret_cast<const float4 *>(rows + g * 32 + 8 * D), x3 = *reinterpret_cast<const float4 *>(rows + g * 32 + 8 * D + 4);
-                uint32_t hi[2][4], lo[2][4];
-                split2(x0.x, x0.y, &hi[0][0], &lo[0][0]);
-                split2(x0.z, x0.w, &hi[0][2], &lo[0][2]);
-                split2(x1.x, x1.y, &hi[1][0], &lo[1][0]);
-                split2(x1.z, x1.w, &hi[1][2], &lo[1][2]);
-                split2(x2.x, x2.y, &hi[0][1], &lo[0][1]);
-                split2(x2.z, x2.w, &hi[0][3], &lo[0][3]);
-                split2(x3.x, x3.y, &hi[1][1], &lo[1][1]);
-                split2(x3.z, x3.w, &hi[1][3], &lo[1][3]);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    if (t * 8 >= m) break;
-                    const uint4 k = *reinterpret_cast<const uint4 *>(sk + piece_at<D>(t * 8 + r, g * 4 + c));
-                    const uint4 q = *reinterpret_cast<const uint4 *>(sq + piece_at<D>(t * 8 + r, g * 4 + c));
-                    mma(y[t], hi[0], k.x, k.y);
-                    mma(o[t], hi[0], q.x, q.y);
-                    mma(y[t], lo[0], k.x, k.y);
-                    mma(o[t], lo[0], q.x, q.y);
-                    mma(y[t], hi[1], k.z, k.w);
-                    mma(o[t], hi[1], q.z, q.w);
-                    mma(y[t], lo[1], k.z, k.w);
-                    mma(o[t], lo[1], q.z, q.w);
-                }
-            }
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(ctl->empty + slot);
-            // R in y (elements 0, 1: value r, nodes 2c and 2c + 1 of the tile; 2, 3: value r + 8), G o in o.
-            // (Nodes past the last have k, v and G of zero, so R of zero, or NaN, which is left out.)
-            if (!wait(ctl->c_full + buffer, n / Sh::kBuffers & 1)) return;
-            float not_zero = 0.f;  // NaN if some R is not finite
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const float2 g = *reinterpret_cast<const float2 *>(gamma + t * 8 + 2 * c);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t vt = transpose8(v[t][i]);
-                    y[t][2 * i] = fmaf(-g.x, y[t][2 * i], __uint_as_float(vt << 16));
-                    y[t][2 * i + 1] = fmaf(-g.y, y[t][2 * i + 1], __uint_as_float(vt & 0xffff0000u));
-                    o[t][2 * i] *= g.x;
-                    o[t][2 * i + 1] *= g.y;
-                    not_zero = fmaf(y[t][2 * i], 0.f, fmaf(y[t][2 * i + 1], 0.f, not_zero));
-                }
-            }
-            const uint8_t *const chi = sk + Sh::kC, *const clo = sk + Sh::kCLo;
-            if (__any_sync(0xffffffffu, not_zero != 0.f)) {  // what is not finite, to the nodes whose path it is on
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-#pragma unroll 1
-                    for (int j = 0; j < 8 && t * 8 + j < m; ++j) {
-                        const int from = (lane & ~3) | j >> 1, w = t * 8 + j;
-                        const float x0 = __shfl_sync(0xffffffffu, j & 1 ? y[t][1] : y[t][0], from);
-                        const float x1 = __shfl_sync(0xffffffffu, j & 1 ? y[t][3] : y[t][2], from);
-                        if (!__any_sync(0xffffffffu, !finite(x0) || !finite(x1))) continue;
-#pragma unroll
-                        for (int t2 = 0; t2 < NT; ++t2)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int u = t2 * 8 + 2 * c + (i & 1), at = u * Sh::kRowC + w * 2;
-                                const float x = i & 2 ? x1 : x0;
-                                if (!finite(x) && (word[u] >> w & 1))
-                                    o[t2][i] = fmaf(bf16_bits_to_float(*reinterpret_cast<const uint16_t *>(chi + at)) +
-                                                        bf16_bits_to_float(*reinterpret_cast<const uint16_t *>(clo + at)),
-                                                    x, o[t2][i]);
-                            }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (!finite(y[t][i])) y[t][i] = 0.f;
-                }
-            }
-#pragma unroll
-            for (int kt = 0; kt < (NT + 1) / 2; ++kt) {
-                if (kt * 16 >= m) break;
-                uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    if (2 * kt + j < NT) {
-                        const float(&x)[4] = y[2 * kt + j];
-                        split2(x[0], x[1], &hi[2 * j], &lo[2 * j]);
-                        split2(x[2], x[3], &hi[2 * j + 1], &lo[2 * j + 1]);
-                    }
-#pragma unroll
-                for (int t = 2 * kt; t < NT; ++t) {
-                    if (t * 8 >= m) break;
-                    const int at = (t * 8 + r) * Sh::kRowC + kt * 32 + c * 4;
-                    const uint32_t h0 = *reinterpret_cast<const uint32_t *>(chi + at), h1 = *reinterpret_cast<const uint32_t *>(chi + at + 16);
-                    const uint32_t l0 = *reinterpret_cast<const uint32_t *>(clo + at), l1 = *reinterpret_cast<const uint32_t *>(clo + at + 16);
-                    mma(o[t], hi, h0, h1);
-                    mma(o[t], hi, l0, l1);
-                    mma(o[t], lo, h0, h1);
-                }
-            }
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                if (t * 8 >= m) break;
-                uint32_t *p = reinterpret_cast<uint32_t *>(a.o + value + static_cast<int64_t>(t * 8 + r) * a.h_v * D) + c;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t x = transpose8(pack_bf16(o[t][2 * i] * a.scale, o[t][2 * i + 1] * a.scale));
-                    if (t * 8 + r < m) p[4 * i] = x;
-                }
-            }
-        }
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(ctl->in_empty + buffer);
-    }
-}
-
-template <int D, int NT>
-__global__ void __launch_bounds__(TreeShape<D, NT>::kWarps * 32, 1) tree_decode_kernel(const __grid_constant__ TreeDecodeArgs a) {
-    using Sh = TreeShape<D, NT>;
-    extern __shared__ __align__(128) uint8_t ring[];
-    uint8_t *const smem = ring + Sh::kSlots * Sh::kSlot;
-    TreeControl<D, NT> *const ctl = reinterpret_cast<TreeControl<D, NT> *>(smem + Sh::kControl);
-    static_assert(sizeof(TreeControl<D, NT>) <= Sh::kControlBytes && Sh::kSmem <= 227 * 1024 && Sh::kSlots >= Sh::kMain, "shared memory");
-    const int warp = threadIdx.x >> 5;
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < Sh::kBuffers; ++i) {
-            tc::mbar_init(ctl->in_full + i, 33);  // the loader's copies, and its word on the unit
-            tc::mbar_init(ctl->in_empty + i, Sh::kMain);
-            tc::mbar_init(ctl->c_full + i, Sh::kPrep);
-        }
-        for (int i = 0; i < Sh::kSlots; ++i) {
-            tc::mbar_init(ctl->full + i, 1);
-            tc::mbar_init(ctl->empty + i, 1);
-        }
-        ctl->fail = 0;
-        ctl->refused = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    tc::fence_proxy_async_smem();
     __syncthreads();
-    const TreeWait wait = {&ctl->fail};
-    if (warp >= Sh::kWarps - Sh::kMain) {
-        multiply<D, NT>(a, ctl, smem, ring, wait, warp - (Sh::kWarps - Sh::kMain));
+
+    // 3. C and G.
+    if (!deep) {
+        if (warp * 32 < Sh::kNodes) {
+            const int most = __reduce_max_sync(0xffffffffu, __popcll(path));
+            float g = 0.f;
+            if (tid < m) g = walk_short<D, NT>(path, most, fq + tid * Sh::kRowF, fk, alpha, beta);
+            if (tid < Sh::kNodes) gamma[tid] = g;
+        }
     } else {
-        if (warp == 0)
-            load_states<D, NT>(a, ctl, ring, wait);
-        else if (warp == 1)
-            load_inputs<D, NT>(a, ctl, smem, wait);
-        else
-            make_c<D, NT>(ctl, smem, wait, warp - 2);
+#pragma unroll 1
+        for (int u = tid >> 2; u < Sh::kNodes; u += D / 4) {  // (whole quads: one node's lanes stay together)
+            const float g = u < m ? walk_long<D, NT>(word[u], fq + u * Sh::kRowF, fk, alpha, beta, c) : 0.f;
+            if (c == 0) gamma[u] = g;
+        }
     }
     __syncthreads();
-    if (threadIdx.x == 0 && ctl->fail) report(a.dev_status, GDN_DEV_TIMEOUT);
-    // Zeros: the tokens behind the last request's, dealt out over the blocks, and the rows that have no outputs else.
-    int32_t end = a.cu_seqlens[a.num_rows];
-    if (end < 0 || end > a.num_tokens) end = static_cast<int32_t>(a.num_tokens);
-    const int64_t pieces = static_cast<int64_t>(a.h_v) * (D / 8);
-    for (int64_t i = end * pieces + static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < a.num_tokens * pieces;
-         i += static_cast<int64_t>(gridDim.x) * blockDim.x)
-        reinterpret_cast<uint4 *>(a.o)[i] = make_uint4(0, 0, 0, 0);
-    if (ctl->refused) {
-        Units units(a);
-        for (; units.next < units.count; units.next += gridDim.x) {
-            units.look();
-            if (!units.sound() || !units.refused()) continue;
-            const int32_t head = static_cast<int32_t>(units.next % static_cast<uint32_t>(a.h_v));
-            for (int64_t i = threadIdx.x; i < static_cast<int64_t>(units.e - units.b) * (D / 8); i += blockDim.x)
-                reinterpret_cast<uint4 *>(a.o + ((units.b + i / (D / 8)) * a.h_v + head) * D)[i % (D / 8)] = make_uint4(0, 0, 0, 0);
+
+#pragma unroll 1
+    for (int slab = 0; slab < 2; ++slab) {
+        const int64_t value = (static_cast<int64_t>(b) * a.h_v + head) * D + warp * 32 + slab * 16;  // node 0's first of the slab
+        // S^T [K; Q]: 16 values by the nodes.
+        float y[NT][4], o[NT][4];
+        uint32_t v[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[t][i] = o[t][i] = 0.f;
+#pragma unroll
+        for (int g = 0; g < Sh::kGroups; ++g) {
+            const float4(&x)[4] = s[g % Sh::kAhead];
+            if (g == Sh::kGroups - 1) {  // v of node 8 t + r, values 2c and 2c + 1, and 8 further on
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    v[t][0] = v[t][1] = 0;
+                    if (t * 8 + r < m) {
+                        const uint32_t *p = reinterpret_cast<const uint32_t *>(a.v + value + static_cast<int64_t>(t * 8 + r) * a.h_v * D) + c;
+                        v[t][0] = __ldg(p);
+                        v[t][1] = __ldg(p + 4);
+                    }
+                }
+            }
+            uint32_t hi[2][4], lo[2][4];
+            split2(x[0].x, x[0].y, &hi[0][0], &lo[0][0]);
+            split2(x[0].z, x[0].w, &hi[0][2], &lo[0][2]);
+            split2(x[1].x, x[1].y, &hi[1][0], &lo[1][0]);
+            split2(x[1].z, x[1].w, &hi[1][2], &lo[1][2]);
+            split2(x[2].x, x[2].y, &hi[0][1], &lo[0][1]);
+            split2(x[2].z, x[2].w, &hi[0][3], &lo[0][3]);
+            split2(x[3].x, x[3].y, &hi[1][1], &lo[1][1]);
+            split2(x[3].z, x[3].w, &hi[1][3], &lo[1][3]);
+            // The group after those in registers.
+            if (slab == 0)
+                ask(g + Sh::kAhead);
+            else if (g + Sh::kAhead < Sh::kGroups)
+                ask(Sh::kGroups + g + Sh::kAhead);
+            // Two tiles at a time: four sums that do not wait for one another.
+            constexpr int kStep = NT == 1 ? 1 : 2;
+#pragma unroll
+            for (int t0 = 0; t0 < NT; t0 += kStep) {
+                if (t0 * 8 >= m) break;
+                uint4 kq[2][kStep];
+#pragma unroll
+                for (int t = 0; t < kStep; ++t) {
+                    kq[0][t] = *reinterpret_cast<const uint4 *>(sk + piece_at<D>((t0 + t) * 8 + r, g * 4 + c));
+                    kq[1][t] = *reinterpret_cast<const uint4 *>(sq + piece_at<D>((t0 + t) * 8 + r, g * 4 + c));
+                }
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+#pragma unroll
+                    for (int t = 0; t < kStep; ++t) {
+                        const uint32_t(&f)[4] = h & 1 ? lo[h >> 1] : hi[h >> 1];
+                        mma(y[t0 + t], f, h & 2 ? kq[0][t].z : kq[0][t].x, h & 2 ? kq[0][t].w : kq[0][t].y);
+                        mma(o[t0 + t], f, h & 2 ? kq[1][t].z : kq[1][t].x, h & 2 ? kq[1][t].w : kq[1][t].y);
+                    }
+            }
         }
+        // R in y (elements 0, 1: value r, nodes 2c and 2c + 1 of the tile; 2, 3: value r + 8), G o in o.
+        // (Nodes past the last have k, v and G of zero, so R of zero, or NaN, which is left out.)
+        float not_zero = 0.f;  // NaN if some R is not finite
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const float2 g = *reinterpret_cast<const float2 *>(gamma + t * 8 + 2 * c);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t vt = transpose8(v[t][i]);
+                y[t][2 * i] = fmaf(-g.x, y[t][2 * i], __uint_as_float(vt << 16));
+                y[t][2 * i + 1] = fmaf(-g.y, y[t][2 * i + 1], __uint_as_float(vt & 0xffff0000u));
+                o[t][2 * i] *= g.x;
+                o[t][2 * i + 1] *= g.y;
+                not_zero = fmaf(y[t][2 * i], 0.f, fmaf(y[t][2 * i + 1], 0.f, not_zero));
+            }
+        }
+        if (__any_sync(0xffffffffu, not_zero != 0.f)) {  // what is not finite, to the nodes whose path it is on
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+#pragma unroll 1
+                for (int j = 0; j < 8 && t * 8 + j < m; ++j) {
+                    const int from = (lane & ~3) | j >> 1, w = t * 8 + j;
+                    const float x0 = __shfl_sync(0xffffffffu, j & 1 ? y[t][1] : y[t][0], from);
+                    const float x1 = __shfl_sync(0xffffffffu, j & 1 ? y[t][3] : y[t][2], from);
+                    if (!__any_sync(0xffffffffu, !finite(x0) || !finite(x1))) continue;
+#pragma unroll
+                    for (int t2 = 0; t2 < NT; ++t2)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int u = t2 * 8 + 2 * c + (i & 1), at = u * Sh::kRowC + w * 2;
+                            const float x = i & 2 ? x1 : x0;
+                            if (!finite(x) && (word[u] >> w & 1))
+                                o[t2][i] = fmaf(bf16_bits_to_float(*reinterpret_cast<const uint16_t *>(chi + at)) +
+                                                    bf16_bits_to_float(*reinterpret_cast<const uint16_t *>(clo + at)),
+                                                x, o[t2][i]);
+                        }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (!finite(y[t][i])) y[t][i] = 0.f;
+            }
+        }
+#pragma unroll
+        for (int kt = 0; kt < (NT + 1) / 2; ++kt) {
+            if (kt * 16 >= m) break;
+            uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (2 * kt + j < NT) {
+                    const float(&x)[4] = y[2 * kt + j];
+                    split2(x[0], x[1], &hi[2 * j], &lo[2 * j]);
+                    split2(x[2], x[3], &hi[2 * j + 1], &lo[2 * j + 1]);
+                }
+            constexpr int kStep = NT < 4 ? NT : 4;
+#pragma unroll
+            for (int t0 = 2 * kt / kStep * kStep; t0 < NT; t0 += kStep) {
+                if (t0 * 8 >= m) break;
+                uint32_t h[kStep][2], l[kStep][2];
+#pragma unroll
+                for (int t = 0; t < kStep; ++t) {
+                    const int at = ((t0 + t) * 8 + r) * Sh::kRowC + kt * 32 + c * 4;
+                    h[t][0] = *reinterpret_cast<const uint32_t *>(chi + at), h[t][1] = *reinterpret_cast<const uint32_t *>(chi + at + 16);
+                    l[t][0] = *reinterpret_cast<const uint32_t *>(clo + at), l[t][1] = *reinterpret_cast<const uint32_t *>(clo + at + 16);
+                }
+#pragma unroll
+                for (int t = 0; t < kStep; ++t)
+                    if (t0 + t >= 2 * kt) mma(o[t0 + t], hi, h[t][0], h[t][1]);
+#pragma unroll
+                for (int t = 0; t < kStep; ++t)
+                    if (t0 + t >= 2 * kt) mma(o[t0 + t], hi, l[t][0], l[t][1]);
+#pragma unroll
+                for (int t = 0; t < kStep; ++t)
+                    if (t0 + t >= 2 * kt) mma(o[t0 + t], lo, h[t][0], h[t][1]);
+            }
+        }
+        uint32_t out[NT][2];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) out[t][i] = transpose8(pack_bf16(o[t][2 * i] * a.scale, o[t][2 * i + 1] * a.scale));
+        uint16_t *p = a.o + value + static_cast<int64_t>(r) * a.h_v * D + 2 * c;
+        const int64_t step = static_cast<int64_t>(8) * a.h_v * D;
+#pragma unroll
+        for (int t = 0; t < NT; ++t, p += step)
+            if (t * 8 + r < m) {
+                *reinterpret_cast<uint32_t *>(p) = out[t][0];
+                *reinterpret_cast<uint32_t *>(p + 8) = out[t][1];
+            }
     }
 }
 
@@ -644,14 +487,13 @@ cudaError_t launch(const TreeDecodeArgs &a, cudaStream_t stream) {
     static int set[kMaxDevices] = {};
     int dev = 0, sms = 0;
     if (!current_device(&dev, &sms)) return cudaErrorInvalidDevice;
-    if (dev < 0 || dev >= kMaxDevices || !__atomic_load_n(&set[dev], __ATOMIC_ACQUIRE)) {
+    if (Sh::kSmem > 48 * 1024 && (dev < 0 || dev >= kMaxDevices || !__atomic_load_n(&set[dev], __ATOMIC_ACQUIRE))) {
         const cudaError_t e =
             cudaFuncSetAttribute(tree_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < kMaxDevices) __atomic_store_n(&set[dev], 1, __ATOMIC_RELEASE);
     }
-    const int64_t units = static_cast<int64_t>(a.num_rows) * a.h_v;
-    tree_decode_kernel<D, NT><<<static_cast<unsigned>(units < sms ? units : sms), Sh::kWarps * 32, Sh::kSmem, stream>>>(a);
+    tree_decode_kernel<D, NT><<<static_cast<unsigned>(a.num_rows) * static_cast<unsigned>(a.h_v), Sh::kThreads, Sh::kSmem, stream>>>(a);
     return cudaGetLastError();
 }
 
