@@ -90,7 +90,10 @@ struct TreeShape {
     // of C takes the place of its q.k: upper halves, then the rests.
     static constexpr int kRowF = kCols + 4, kRowC = 4 * kRowF, kLo = 2 * kCols;
     static constexpr int kQ = kCols * kRowK, kFK = 2 * kQ, kFQ = kFK + kCols * kRowC, kWord = kFQ + kCols * kRowC, kGate = kWord + 8 * kNodes;
-    static constexpr int kSmem = kGate + 3 * kNodes * 4;
+    // v; of 64 nodes it is read where it is used, so that three blocks have room.
+    static constexpr bool kStageV = NT <= 4;
+    static constexpr int kRowV = 2 * D + 16, kV = (kGate + 3 * kNodes * 4 + 15) / 16 * 16;
+    static constexpr int kSmem = kV + (kStageV ? kNodes * kRowV : 0);
 };
 
 // Offset of a 16-byte piece of a row of k or q: odd rows have the halves of each 128 bytes changed over, so that eight
@@ -100,22 +103,24 @@ __device__ __forceinline__ int piece_at(int row, int piece) {
     return row * (2 * D) + ((piece ^ ((row & 1) << 2)) << 4);
 }
 
-// k.k and q.k of nodes [16 rt, + 16) with nodes [16 ct, + 16), exact products of bf16.
-template <int D, int NT>
-__device__ __forceinline__ void products(const uint8_t *sk, const uint8_t *sq, int rt, int ct, float *fk, float *fq, int lane) {
+// k.k and q.k of nodes [16 rt, + 16) with nodes [16 ct, + 16), exact products of bf16.  With few nodes a warp takes one of
+// them for 8 nodes (part: q.k, second 8), so that four share what there is to do.
+template <int D, int NT, int kParts>
+__device__ __forceinline__ void products(const uint8_t *sk, const uint8_t *sq, int rt, int ct, int part, float *fk, float *fq, int lane) {
     using Sh = TreeShape<D, NT>;
-    constexpr int kTiles = NT == 1 ? 1 : 2;
-    const int r = lane >> 2, c = lane & 3;
-    float acc[2][kTiles][4] = {};
+    constexpr int kTiles = NT == 1 || kParts > 1 ? 1 : 2, kSides = kParts > 1 ? 1 : 2;
+    const int r = lane >> 2, c = lane & 3, side0 = kParts > 1 ? part & 1 : 0, tile0 = kParts > 1 ? part >> 1 : 0;
+    float acc[kSides][kTiles][4] = {};
 #pragma unroll
     for (int g = 0; g < Sh::kGroups; ++g) {
         uint4 b[kTiles];
-        uint32_t f[2][2][4];
+        uint32_t f[kSides][2][4];
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) b[t] = *reinterpret_cast<const uint4 *>(sk + piece_at<D>(ct * 16 + t * 8 + r, g * 4 + c));
+        for (int t = 0; t < kTiles; ++t)
+            b[t] = *reinterpret_cast<const uint4 *>(sk + piece_at<D>(ct * 16 + (tile0 + t) * 8 + r, g * 4 + c));
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const uint8_t *rows = x ? sq : sk;
+        for (int x = 0; x < kSides; ++x) {
+            const uint8_t *rows = side0 + x ? sq : sk;
             const uint4 a0 = *reinterpret_cast<const uint4 *>(rows + piece_at<D>(rt * 16 + r, g * 4 + c));
             const uint4 a1 = *reinterpret_cast<const uint4 *>(rows + piece_at<D>(rt * 16 + r + 8, g * 4 + c));
             f[x][0][0] = a0.x, f[x][0][1] = a1.x, f[x][0][2] = a0.y, f[x][0][3] = a1.y;
@@ -124,15 +129,15 @@ __device__ __forceinline__ void products(const uint8_t *sk, const uint8_t *sq, i
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+            for (int x = 0; x < kSides; ++x)
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t) mma(acc[x][t], f[x][h], h ? b[t].z : b[t].x, h ? b[t].w : b[t].y);
     }
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+    for (int x = 0; x < kSides; ++x)
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
-            float *p = (x ? fq : fk) + (rt * 16 + r) * Sh::kRowF + ct * 16 + t * 8 + 2 * c;
+            float *p = (side0 + x ? fq : fk) + (rt * 16 + r) * Sh::kRowF + ct * 16 + (tile0 + t) * 8 + 2 * c;
             *reinterpret_cast<float2 *>(p) = make_float2(acc[x][t][0], acc[x][t][1]);
             *reinterpret_cast<float2 *>(p + 8 * Sh::kRowF) = make_float2(acc[x][t][2], acc[x][t][3]);
         }
@@ -147,7 +152,7 @@ __device__ __forceinline__ void products(const uint8_t *sk, const uint8_t *sq, i
 constexpr int kShortPath = 16;
 
 template <int D, int NT>
-__device__ __forceinline__ float walk_short(uint64_t path, int most, float *row, const float *fk, const float *alpha, const float *beta) {
+__device__ __forceinline__ float walk_short(uint64_t path, int most, float *row, const float *fk, const float2 *gates) {
     using Sh = TreeShape<D, NT>;
     constexpr int kMost = 8 * NT < kShortPath ? 8 * NT : kShortPath;
     const int steps = __popcll(path);
@@ -155,6 +160,7 @@ __device__ __forceinline__ float walk_short(uint64_t path, int most, float *row,
     float g[kMost];
 #pragma unroll
     for (int i = 0; i < kMost; ++i) {  // (behind the last one: it again)
+        if (i >= most) break;  // (the warp's longest)
         const int w = NT <= 4 ? 31 - __clz(static_cast<uint32_t>(path)) : 63 - __clzll(static_cast<long long>(path));
         x[i] = path ? w : i > 0 ? x[i > 0 ? i - 1 : 0] : 0;
         path &= ~(1ull << x[i]);
@@ -166,17 +172,22 @@ __device__ __forceinline__ float walk_short(uint64_t path, int most, float *row,
     asm volatile("" ::: "memory");
     uint16_t *const hi = reinterpret_cast<uint16_t *>(row), *const lo = hi + Sh::kLo / 2;
     float decay = 1.f;
+    float2 ab = most > 0 ? gates[x[0]] : make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < kMost; ++i) {
-        if (i >= most) break;  // (the warp's longest)
-        const float a = alpha[x[i]], c = beta[x[i]] * g[i], ac = -a * c;
+        if (i >= most) break;
+        const float a = ab.x, c = ab.y * g[i], ac = -a * c;
+        if (i + 1 < kMost && i + 1 < most) ab = gates[x[i + 1 < kMost ? i + 1 : i]];
+#pragma unroll
+        for (int j = i + 1; j < kMost; ++j) {
+            if (j >= most) break;
+            g[j] = fmaf(ac, fk[x[i] * Sh::kRowF + x[j]], a * g[j]);
+        }
         if (i < steps) {
             hi[x[i]] = static_cast<uint16_t>(__float_as_uint(c) >> 16);
             lo[x[i]] = float_to_bf16_bits(c - __uint_as_float(__float_as_uint(c) & 0xffff0000u));
             decay *= a;
         }
-#pragma unroll
-        for (int j = i + 1; j < kMost; ++j) g[j] = fmaf(ac, fk[x[i] * Sh::kRowF + x[j]], a * g[j]);
     }
     return decay;
 }
@@ -184,7 +195,7 @@ __device__ __forceinline__ float walk_short(uint64_t path, int most, float *row,
 // A path of any length, on `row` itself: a quad takes the nodes above in turn, and what one lane has written is another's c
 // four nodes on.  The same operations, and so the same bits.
 template <int D, int NT>
-__device__ __forceinline__ float walk_long(const uint64_t path, float *row, const float *fk, const float *alpha, const float *beta, int sub) {
+__device__ __forceinline__ float walk_long(const uint64_t path, float *row, const float *fk, const float2 *gates, int sub) {
     using Sh = TreeShape<D, NT>;
     const uint32_t quad = 0xfu << (threadIdx.x & 28);
     float decay = 1.f;
@@ -192,7 +203,8 @@ __device__ __forceinline__ float walk_long(const uint64_t path, float *row, cons
     for (uint64_t left = path; left;) {
         const int w = 63 - __clzll(static_cast<long long>(left));
         left ^= 1ull << w;
-        const float a = alpha[w], c = beta[w] * row[w], ac = -a * c;
+        const float2 ab = gates[w];
+        const float a = ab.x, c = ab.y * row[w], ac = -a * c;
         __syncwarp(quad);
         if (sub == 0) row[w] = c;
         decay *= a;
@@ -240,7 +252,8 @@ __global__ void __launch_bounds__(TreeShape<D, NT>::kThreads, TreeShape<D, NT>::
     float *const fk = reinterpret_cast<float *>(smem + Sh::kFK), *const fq = reinterpret_cast<float *>(smem + Sh::kFQ);
     const uint8_t *const chi = smem + Sh::kFQ, *const clo = chi + Sh::kLo;
     uint64_t *const word = reinterpret_cast<uint64_t *>(smem + Sh::kWord);
-    float *const alpha = reinterpret_cast<float *>(smem + Sh::kGate), *const beta = alpha + Sh::kNodes, *const gamma = beta + Sh::kNodes;
+    float2 *const gates = reinterpret_cast<float2 *>(smem + Sh::kGate);  // decay and beta
+    float *const gamma = reinterpret_cast<float *>(gates + Sh::kNodes);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
     const int32_t req = blockIdx.x / a.h_v, head = blockIdx.x - req * a.h_v, head_k = head / (a.h_v / a.h_k);
     const int32_t b = a.cu_seqlens[req], e = a.cu_seqlens[req + 1], slot = a.src_slot[req];
@@ -278,54 +291,78 @@ __global__ void __launch_bounds__(TreeShape<D, NT>::kThreads, TreeShape<D, NT>::
         x[2] = load_state(p + 8 * D);
         x[3] = load_state(p + 8 * D + 4);
     };
-#pragma unroll
-    for (int g = 0; g < Sh::kAhead; ++g) ask(g);
+    // (k and q first, which the block waits for; the state's rows are there when it comes to them.)
+    uint64_t path = 0;  // of node tid, as long as there is one (itself and nodes before it)
+    float my_g = 0.f, my_beta = 0.f;
+    if (tid < m) {
+        const int64_t at = static_cast<int64_t>(b) + tid;
+        path = a.masks[at] & ((2ull << tid) - 1);
+        my_g = a.g[at * a.h_v + head];
+        my_beta = a.beta[at * a.h_v + head];
+    }
     {
         // (each thread's rows are 8 apart, so their parity and the piece's place stay)
         const int row = tid / (D / 8), piece = tid % (D / 8);
         const int64_t first = ((static_cast<int64_t>(b) + row) * a.h_k + head_k) * D + piece * 8, step = static_cast<int64_t>(8) * a.h_k * D;
         uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(sk + piece_at<D>(row, piece)));
         const uint16_t *k = a.k + first, *q = a.q + first;
+#pragma unroll 2
         for (int u = row; u < ((m + 15) & ~15); u += 8, k += step, q += step, to += 8 * Sh::kRowK) {
             copy16(to, u < m ? k : a.k, u < m);
             copy16(to + Sh::kQ, u < m ? q : a.q, u < m);
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (Sh::kStageV) {
+            const uint16_t *v = a.v + ((static_cast<int64_t>(b) + row) * a.h_v + head) * D + piece * 8;
+            to = static_cast<uint32_t>(__cvta_generic_to_shared(smem + Sh::kV + row * Sh::kRowV + piece * 16));
+#pragma unroll 2
+            for (int u = row; u < m; u += 8, v += static_cast<int64_t>(8) * a.h_v * D, to += 8 * Sh::kRowV) copy16(to, v, true);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
     }
-    uint64_t path = 0;  // of node tid, as long as there is one (itself and nodes before it)
+#pragma unroll
+    for (int g = 0; g < Sh::kAhead; ++g) ask(g);
     if (tid < Sh::kNodes) {
-        const int64_t at = static_cast<int64_t>(b) + tid;
-        if (tid < m) path = a.masks[at] & ((2ull << tid) - 1);
         word[tid] = path;
-        alpha[tid] = tid < m ? expf(a.g[at * a.h_v + head]) : 0.f;
-        beta[tid] = tid < m ? a.beta[at * a.h_v + head] : 0.f;
+        gates[tid] = make_float2(expf(my_g), my_beta);
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (Sh::kStageV)
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
     const bool deep = __syncthreads_or(__popcll(path) > kShortPath);
 
     // 2. k.k and q.k of nodes and those before them.
-    {
+    if (NT <= 2) {
+#pragma unroll 1
+        for (int part = warp; part < 2 * NT; part += D / 32) products<D, NT, 4>(sk, sq, 0, 0, part, fk, fq, lane);
+    } else {
         int task = warp;
 #pragma unroll 1
         for (int rt = 0; rt * 16 < m; ++rt) {
 #pragma unroll 1
-            for (; task <= rt; task += D / 32) products<D, NT>(sk, sq, rt, task, fk, fq, lane);
+            for (; task <= rt; task += D / 32) products<D, NT, 1>(sk, sq, rt, task, 0, fk, fq, lane);
             task -= rt + 1;
         }
     }
+    if (Sh::kStageV) asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
 
     // 3. C and G.
     if (!deep) {
-        if (warp * 32 < Sh::kNodes) {
-            const int most = __reduce_max_sync(0xffffffffu, __popcll(path));
-            float g = 0.f;
-            if (tid < m) g = walk_short<D, NT>(path, most, fq + tid * Sh::kRowF, fk, alpha, beta);
-            if (tid < Sh::kNodes) gamma[tid] = g;
-        }
+        // (the nodes dealt out over the warps: reads of several rows' places meet in the same banks)
+        constexpr int kPer = Sh::kNodes / (D / 32);
+        const int u = warp * kPer + lane;
+        const bool mine = lane < kPer && u < m;
+        path = mine ? word[u] : 0;
+        const int most = __reduce_max_sync(0xffffffffu, __popcll(path));
+        float g = 0.f;
+        if (mine) g = walk_short<D, NT>(path, most, fq + u * Sh::kRowF, fk, gates);
+        if (lane < kPer) gamma[u] = g;
     } else {
 #pragma unroll 1
         for (int u = tid >> 2; u < Sh::kNodes; u += D / 4) {  // (whole quads: one node's lanes stay together)
-            const float g = u < m ? walk_long<D, NT>(word[u], fq + u * Sh::kRowF, fk, alpha, beta, c) : 0.f;
+            const float g = u < m ? walk_long<D, NT>(word[u], fq + u * Sh::kRowF, fk, gates, c) : 0.f;
             if (c == 0) gamma[u] = g;
         }
     }
@@ -344,14 +381,16 @@ __global__ void __launch_bounds__(TreeShape<D, NT>::kThreads, TreeShape<D, NT>::
 #pragma unroll
         for (int g = 0; g < Sh::kGroups; ++g) {
             const float4(&x)[4] = s[g % Sh::kAhead];
-            if (g == Sh::kGroups - 1) {  // v of node 8 t + r, values 2c and 2c + 1, and 8 further on
+            if (g == (Sh::kStageV ? Sh::kGroups - 1 : 0)) {  // v of node 8 t + r, values 2c and 2c + 1, and 8 further on
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     v[t][0] = v[t][1] = 0;
                     if (t * 8 + r < m) {
-                        const uint32_t *p = reinterpret_cast<const uint32_t *>(a.v + value + static_cast<int64_t>(t * 8 + r) * a.h_v * D) + c;
-                        v[t][0] = __ldg(p);
-                        v[t][1] = __ldg(p + 4);
+                        const uint32_t *p =
+                            (Sh::kStageV ? reinterpret_cast<const uint32_t *>(smem + Sh::kV + (t * 8 + r) * Sh::kRowV + warp * 64 + slab * 32)
+                                         : reinterpret_cast<const uint32_t *>(a.v + value + static_cast<int64_t>(t * 8 + r) * a.h_v * D)) + c;
+                        v[t][0] = *p;
+                        v[t][1] = p[4];
                     }
                 }
             }
