@@ -708,6 +708,12 @@ def gdn_paged_attention(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, o
            "gdn_paged_attention")
 
 
+def _dense(t, name, dtype, ndim):
+    if t.__class__ is _Tensor and t.dtype is dtype and t.is_cuda and t.dim() == ndim and t.is_contiguous():
+        return t.data_ptr()
+    return _dev(t, name, dtype, ndim).data_ptr()
+
+
 def _words(t, name):
     if t.__class__ is _Tensor and t.dtype is torch.int64 and t.is_cuda and t.dim() == 1 and t.is_contiguous():
         return t.data_ptr()
@@ -761,18 +767,20 @@ def gdn_tree_decode(q, k, v, g, beta, state, src_slot, cu_seqlens, masks, o, max
     a row's nodes."""
     lib = _lib or load_library()
     bf, f32 = torch.bfloat16, torch.float32
-    q, k, v = _dev(q, "q", bf, 3), _dev(k, "k", bf, 3), _dev(v, "v", bf, 3)
-    g, beta = _dev(g, "g", f32, 2), _dev(beta, "beta", f32, 2)
-    state, o = _dev(state, "state", f32, 4), _dev(o, "o", bf, 3)
+    ptrs = (_dense(q, "q", bf, 3), _dense(k, "k", bf, 3), _dense(v, "v", bf, 3), _dense(g, "g", f32, 2),
+            _dense(beta, "beta", f32, 2), _dense(state, "state", f32, 4))
+    out = _dense(o, "o", bf, 3)
     slots, cu, words = _i32_vec(src_slot, "src_slot"), _i32_vec(cu_seqlens, "cu_seqlens"), _words(masks, "masks")
-    T, n = q.shape[0], src_slot.numel()
-    if not (k.shape == q.shape and v.shape[0] == T and o.shape == v.shape and g.shape == (T, v.shape[1])
-            and beta.shape == g.shape and cu_seqlens.numel() == n + 1 and masks.numel() == T
-            and state.shape[1:] == (v.shape[1], v.shape[2], q.shape[2])):
+    n = src_slot.numel()
+    T, h_k, d = qs = q.shape
+    _, h_v, d_v = vs = v.shape
+    slots_n, *row = state.shape
+    if not (k.shape == qs and vs[0] == T and o.shape == vs and g.shape == (T, h_v) and beta.shape == (T, h_v)
+            and cu_seqlens.numel() == n + 1 and masks.numel() == T and row == [h_v, d_v, d]):
         raise ValueError("inconsistent tree-decode shapes")
-    d = _dims(q, v, scale)
-    _check(lib.gdn_tree_decode(ctypes.byref(d), n, max_nodes, T, cu, words, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                               g.data_ptr(), beta.data_ptr(), state.data_ptr(), state.shape[0], slots, o.data_ptr(),
+    key = (h_k, h_v, d, d_v, float(scale))
+    dims = _dims_cache.get(key) or _dims(q, v, scale)
+    _check(lib.gdn_tree_decode(ctypes.byref(dims), n, max_nodes, T, cu, words, *ptrs, slots_n, slots, out,
                                _i32_word(dev_status, "dev_status"), _stream(stream)), "gdn_tree_decode")
 
 
@@ -780,13 +788,19 @@ _ROTARY_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 _pack_side = struct.Struct("@PPiqqqq").pack  # RotarySide's layout
 
 
-def _rotary_side(x, out, name, dtype, T, d):
-    """The C description of one side (its bytes)."""
+def _rotary_side(x, out, name, dtype, shape):
+    """The C description of one side (its bytes); ``shape``: tokens and head size."""
     xs = _strided(x, name, dtype, 3)
-    os_ = xs if out is x else _strided(out, f"{name}_out", dtype, 3)
-    if x.shape[0] != T or x.shape[2] != d or out.shape != x.shape:
+    T, h, d = size = x.shape
+    if T != shape[0] or d != shape[1]:
         raise ValueError("inconsistent rotary shapes")
-    return _pack_side(x.data_ptr(), out.data_ptr(), x.shape[1], xs[0], xs[1], os_[0], os_[1])
+    if out is None:
+        p = x.data_ptr()
+        return _pack_side(p, p, h, xs[0], xs[1], xs[0], xs[1])
+    to = _strided(out, f"{name}_out", dtype, 3)
+    if out.shape != size:
+        raise ValueError("inconsistent rotary shapes")
+    return _pack_side(x.data_ptr(), out.data_ptr(), h, xs[0], xs[1], to[0], to[1])
 
 
 def gdn_rotary(q, k, positions, frequencies, q_out=None, k_out=None, interleaved: bool = False,
@@ -803,9 +817,9 @@ def gdn_rotary(q, k, positions, frequencies, q_out=None, k_out=None, interleaved
     if code is None:
         raise TypeError(f"q must be bfloat16 or float16, got {dtype}")
     pos, freq = _i32_vec(positions, "positions"), _words(frequencies, "frequencies")
-    T, d = positions.numel(), q.shape[-1]
-    q_side = _rotary_side(q, q if q_out is None else q_out, "q", dtype, T, d)
-    k_side = None if k is None else _rotary_side(k, k if k_out is None else k_out, "k", dtype, T, d)
+    T, d = shape = positions.numel(), q.shape[-1]
+    q_side = _rotary_side(q, q_out, "q", dtype, shape)
+    k_side = None if k is None else _rotary_side(k, k_out, "k", dtype, shape)
     _check(lib.gdn_rotary(code, T, d, 2 * frequencies.numel(), bool(interleaved), magnitude, pos, freq, q_side, k_side,
                           _stream(stream)), "gdn_rotary")
 

@@ -6,9 +6,10 @@
 // int32 position: no range reduction, no 64-bit floating point.  Its upper 32
 // bits are the turn's fraction to 2^-32; sincospif takes it from there.
 //
-// Split.  A thread takes eight pairs (two 16-byte pieces) of a token and keeps
-// their sines and cosines for all the heads it turns.  With few tokens the
-// heads are dealt out over more threads, which then compute the same angles.
+// Split.  A thread takes eight pairs (two 16-byte pieces) of a token in all or
+// some of its heads; with few tokens the heads are dealt out over more threads.
+// A block makes the angles of its tokens once, in shared memory, while the
+// first heads are on the way from memory.
 // Bound by HBM for long chunks, by the launch for decode steps.
 #include "paged.cuh"
 
@@ -20,15 +21,16 @@ namespace {
 
 constexpr int kRotaryThreads = 256;
 constexpr int kRotaryUnroll = 4;  // heads whose loads are in flight at once
+constexpr int kRotaryPairs = kRotaryThreads * 8;  // of a block: eight per turning thread
 
-// Sine and cosine of pair i at a position, times the magnitude.
-__device__ __forceinline__ void turn(const RotaryArgs &a, int64_t position, uint64_t frequency, float *c, float *s) {
+// Cosine and sine of a pair at a position, times the magnitude.
+__device__ __forceinline__ float2 turn(const RotaryArgs &a, int64_t position, uint64_t frequency) {
     const uint64_t phase = static_cast<uint64_t>(position) * frequency;
     // (the upper half as a signed number: -1/2 to 1/2 turns, in units of 2^-32; sincospi's argument is half turns)
     const float x = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f;  // 2^-31
-    sincospif(x, s, c);
-    *s *= a.magnitude;
-    *c *= a.magnitude;
+    float c, s;
+    sincospif(x, &s, &c);
+    return make_float2(c * a.magnitude, s * a.magnitude);
 }
 
 template <bool kHalf>
@@ -54,51 +56,53 @@ __device__ __forceinline__ const RotarySide &side_of(const RotaryArgs &a, int32_
 }
 
 // Lanes of a token: turns = rot / 16 of two pieces to turn, then those of two pieces to copy (where the output lies
-// elsewhere).  `splits` threads share a lane's heads.
-template <bool kHalf, bool kInterleaved>
-__global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_constant__ RotaryArgs a, int32_t turns,
-                                                                int32_t lanes, int32_t splits) {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * kRotaryThreads + threadIdx.x;
-    const uint32_t per_token = static_cast<uint32_t>(lanes) * static_cast<uint32_t>(splits);
-    const int64_t t = i / per_token;
-    if (t >= a.num_tokens) return;
-    const uint32_t rest = static_cast<uint32_t>(i - t * per_token);
-    const int32_t split = static_cast<int32_t>(rest / static_cast<uint32_t>(lanes));
-    const int32_t lane = static_cast<int32_t>(rest) - split * lanes;
+// elsewhere).  `splits` threads share a lane's heads; a block takes `tokens` tokens, lanes * splits * tokens <= its threads.
+template <bool kHalf, bool kInterleaved, bool kOnce>
+__global__ void __launch_bounds__(kRotaryThreads, kOnce ? 4 : 3) rotary_kernel(const __grid_constant__ RotaryArgs a, int32_t turns, int32_t lanes,
+                                                                   int32_t splits, int32_t tokens) {
+    __shared__ float2 angle[kRotaryPairs];  // cosine and sine of the tokens' pairs
+    const int32_t per_token = lanes * splits;
+    const int32_t token = static_cast<int32_t>(threadIdx.x) / per_token, rest = static_cast<int32_t>(threadIdx.x) - token * per_token;
+    const int32_t split = rest / lanes, lane = rest - split * lanes;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * tokens, t = first + token;
+    const bool live = token < tokens && t < a.num_tokens;
     const int32_t heads = a.side[0].h + a.side[1].h;
     const bool turning = lane < turns;
     // First elements of the two pieces; a last copy lane may have only one.
-    int32_t at0, at1;
-    float c[8], s[8];
-    if (turning) {
-        at0 = lane * (kInterleaved ? 16 : 8);
-        at1 = kInterleaved ? at0 + 8 : at0 + a.rot / 2;
-        const int64_t position = a.positions[t];
-        const ulonglong2 *f = reinterpret_cast<const ulonglong2 *>(a.frequencies + lane * 8);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const ulonglong2 two = f[j];
-            turn(a, position, two.x, c + 2 * j, s + 2 * j);
-            turn(a, position, two.y, c + 2 * j + 1, s + 2 * j + 1);
-        }
-    } else {
-        at0 = a.rot + (lane - turns) * 16;
-        at1 = at0 + 8;
-    }
+    const int32_t at0 = turning ? lane * (kInterleaved ? 16 : 8) : a.rot + (lane - turns) * 16;
+    const int32_t at1 = turning && !kInterleaved ? at0 + a.rot / 2 : at0 + 8;
     const bool two = at1 < a.d;
-#pragma unroll 1
-    for (int32_t h0 = split; h0 < heads; h0 += splits * kRotaryUnroll) {
-        uint4 x[kRotaryUnroll], y[kRotaryUnroll];
+    uint4 x[kRotaryUnroll], y[kRotaryUnroll];
+    auto load = [&](int32_t h0) {
 #pragma unroll
         for (int k = 0; k < kRotaryUnroll; ++k) {
             int32_t h = h0 + k * splits;
-            if (h >= heads) continue;
+            if (!live || h >= heads) continue;
             const RotarySide &side = side_of(a, &h);
             if (!turning && side.src == side.dst) continue;
             const uint16_t *p = side.src + t * side.token_stride + h * side.head_stride;
             x[k] = *reinterpret_cast<const uint4 *>(p + at0);
             if (two) y[k] = *reinterpret_cast<const uint4 *>(p + at1);
         }
+    };
+    if (kOnce) load(split);  // (on the way while the angles are made)
+    const int32_t pairs = a.rot / 2;
+    for (int32_t i = threadIdx.x; i < tokens * pairs; i += kRotaryThreads) {
+        const int32_t of = i / pairs;
+        if (first + of < a.num_tokens)
+            angle[i] = turn(a, a.positions[first + of], a.frequencies[i - of * pairs]);
+    }
+    __syncthreads();
+    float c[8], s[8];
+    if (turning && live)
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            const float4 cs = *reinterpret_cast<const float4 *>(angle + token * pairs + lane * 8 + j);
+            c[j] = cs.x, s[j] = cs.y, c[j + 1] = cs.z, s[j + 1] = cs.w;
+        }
+#pragma unroll 1
+    for (int32_t h0 = split; live && h0 < heads; h0 += splits * kRotaryUnroll) {
+        if (!kOnce) load(h0);
 #pragma unroll
         for (int k = 0; k < kRotaryUnroll; ++k) {
             int32_t h = h0 + k * splits;
@@ -128,6 +132,7 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const __grid_con
             *reinterpret_cast<uint4 *>(p + at0) = x[k];
             if (two) *reinterpret_cast<uint4 *>(p + at1) = y[k];
         }
+        if (kOnce) break;
     }
 }
 
@@ -149,7 +154,9 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_any_kernel(const __grid
     if (turning) {
         at0 = a.interleaved ? 2 * lane : lane;
         at1 = a.interleaved ? at0 + 1 : lane + a.rot / 2;
-        turn(a, a.positions[t], a.frequencies[lane], &c, &s);
+        const float2 cs = turn(a, a.positions[t], a.frequencies[lane]);
+        c = cs.x;
+        s = cs.y;
     }
     for (int32_t h0 = split; h0 < heads; h0 += splits) {
         int32_t h = h0;
@@ -166,6 +173,16 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_any_kernel(const __grid
         to[at0] = static_cast<uint16_t>(out);
         to[at1] = static_cast<uint16_t>(out >> 16);
     }
+}
+
+using RotaryKernel = void (*)(const RotaryArgs, int32_t, int32_t, int32_t, int32_t);
+template <bool kHalf, bool kInterleaved>
+RotaryKernel pick_once(bool once) {
+    return once ? rotary_kernel<kHalf, kInterleaved, true> : rotary_kernel<kHalf, kInterleaved, false>;
+}
+RotaryKernel pick(bool half, bool interleaved, bool once) {
+    if (half) return interleaved ? pick_once<true, true>(once) : pick_once<true, false>(once);
+    return interleaved ? pick_once<false, true>(once) : pick_once<false, false>(once);
 }
 
 bool pieces16(const RotarySide &s) {
@@ -188,17 +205,19 @@ cudaError_t launch_rotary(const RotaryArgs &a, cudaStream_t stream) {
     const int64_t have = a.num_tokens * lanes, want = static_cast<int64_t>(sms) * 2048;
     int64_t splits = (want + have - 1) / have;
     if (splits > heads) splits = heads;
-    const int64_t blocks = (have * splits + kRotaryThreads - 1) / kRotaryThreads;
-    if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
-    const dim3 grid(static_cast<unsigned>(blocks));
-    const int32_t n = static_cast<int32_t>(splits);
     const bool half = a.dtype == GDN_FP16;
-    if (!wide)
-        (half ? rotary_any_kernel<true> : rotary_any_kernel<false>)<<<grid, kRotaryThreads, 0, stream>>>(a, turns, lanes, n);
-    else if (a.interleaved)
-        (half ? rotary_kernel<true, true> : rotary_kernel<false, true>)<<<grid, kRotaryThreads, 0, stream>>>(a, turns, lanes, n);
-    else
-        (half ? rotary_kernel<true, false> : rotary_kernel<false, false>)<<<grid, kRotaryThreads, 0, stream>>>(a, turns, lanes, n);
+    if (!wide) {
+        const int64_t blocks = (have * splits + kRotaryThreads - 1) / kRotaryThreads;
+        if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
+        (half ? rotary_any_kernel<true> : rotary_any_kernel<false>)<<<static_cast<unsigned>(blocks), kRotaryThreads, 0, stream>>>(
+            a, turns, lanes, static_cast<int32_t>(splits));
+        return cudaGetLastError();
+    }
+    if (splits * lanes > kRotaryThreads) splits = kRotaryThreads / lanes;  // (at most 64 lanes: d <= 1024)
+    const int32_t n = static_cast<int32_t>(splits), tokens = kRotaryThreads / (lanes * n);
+    const dim3 grid(static_cast<unsigned>((a.num_tokens + tokens - 1) / tokens));
+    const auto kernel = pick(half, a.interleaved, n * kRotaryUnroll >= heads);
+    kernel<<<grid, kRotaryThreads, 0, stream>>>(a, turns, lanes, n, tokens);
     return cudaGetLastError();
 }
 

@@ -80,11 +80,11 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 template <int D, int NT>
 struct TreeShape {
     static constexpr int kThreads = D;                         // a warp per 32 values
-    static constexpr int kBlocks = (NT <= 4 ? 512 : 384) / D;  // of an SM
+    static constexpr int kBlocks = (NT <= 2 ? 768 : NT <= 4 ? 512 : 384) / D;  // of an SM
     static constexpr int kNodes = 8 * NT;
     static constexpr int kCols = kNodes < 16 ? 16 : kNodes;  // whole steps of 16
     static constexpr int kGroups = D / 32;                   // of 32 state columns
-    static constexpr int kAhead = NT <= 2 ? kGroups : 2;     // groups of the state in registers
+    static constexpr int kAhead = 2;     // groups of the state in registers
     static constexpr int kRowK = 2 * D;                      // bytes of a row of k or q
     // A node's row of the products is 4 kCols bytes and 16 more: 4-byte reads of 8 rows x 4 lanes meet no bank twice.  Its row
     // of C takes the place of its q.k: upper halves, then the rests.
