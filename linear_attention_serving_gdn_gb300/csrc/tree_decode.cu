@@ -80,16 +80,15 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 template <int D, int NT>
 struct TreeShape {
     static constexpr int kThreads = D;                         // a warp per 32 values
-    static constexpr int kBlocks = (NT <= 2 ? 768 : NT <= 4 ? 512 : 384) / D;  // of an SM
+    static constexpr int kBlocks = (NT <= 2 ? 768 : 512) / D;  // of an SM
     static constexpr int kNodes = 8 * NT;
     static constexpr int kCols = kNodes < 16 ? 16 : kNodes;  // whole steps of 16
     static constexpr int kGroups = D / 32;                   // of 32 state columns
-    static constexpr int kAhead = 2;     // groups of the state in registers
+    static constexpr int kAhead = NT <= 4 ? 2 : 1;           // groups of the state in registers
     static constexpr int kRowK = 2 * D;                      // bytes of a row of k or q
-    // A node's row of the products is 4 kCols bytes and 16 more: 4-byte reads of 8 rows x 4 lanes meet no bank twice.  Its row
-    // of C takes the place of its q.k: upper halves, then the rests.
-    static constexpr int kRowF = kCols + 4, kRowC = 4 * kRowF, kLo = 2 * kCols;
-    static constexpr int kQ = kCols * kRowK, kFK = 2 * kQ, kFQ = kFK + kCols * kRowC, kWord = kFQ + kCols * kRowC, kGate = kWord + 8 * kNodes;
+    // Of k.k and q.k only what lies on or below the diagonal: k.k as a triangle, q.k by tiles of 16 (struct Row).
+    static constexpr int kQ = kCols * kRowK, kFQ = 2 * kQ, kFK = kFQ + (128 * (kCols / 16) * (kCols / 16 + 1) + 64 * (kCols / 16)) * 4, kWord = kFK + (kCols * (kCols + 1) / 2 * 4 + 15) / 16 * 16,
+                         kGate = kWord + 8 * kNodes;
     // v; of 64 nodes it is read where it is used, so that three blocks have room.
     static constexpr bool kStageV = NT <= 4;
     static constexpr int kRowV = 2 * D + 16, kV = (kGate + 3 * kNodes * 4 + 15) / 16 * 16;
@@ -102,6 +101,16 @@ template <int D>
 __device__ __forceinline__ int piece_at(int row, int piece) {
     return row * (2 * D) + ((piece ^ ((row & 1) << 2)) << 4);
 }
+
+__device__ __forceinline__ int triangle(int u) { return u * (u + 1) / 2; }
+
+// Node u's row of q.k: as many floats as there are nodes up to the end of its tile of 16, and 4 more (4-byte reads of 8 rows
+// x 4 lanes meet no bank twice).  Its row of C takes that place: the upper halves, then the rests.
+struct Row {
+    int at, cols;  // first float; nodes
+    __device__ __forceinline__ explicit Row(int u) : at(128 * (u / 16) * (u / 16 + 1) + 64 * (u / 16) + u % 16 * (16 * (u / 16) + 20)), cols(16 * (u / 16) + 16) {}
+    __device__ __forceinline__ int lo() const { return 2 * cols; }  // bytes from the upper halves to the rests
+};
 
 // k.k and q.k of nodes [16 rt, + 16) with nodes [16 ct, + 16), exact products of bf16.  With few nodes a warp takes one of
 // them for 8 nodes (part: q.k, second 8), so that four share what there is to do.
@@ -137,9 +146,16 @@ __device__ __forceinline__ void products(const uint8_t *sk, const uint8_t *sq, i
     for (int x = 0; x < kSides; ++x)
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
-            float *p = (side0 + x ? fq : fk) + (rt * 16 + r) * Sh::kRowF + ct * 16 + (tile0 + t) * 8 + 2 * c;
-            *reinterpret_cast<float2 *>(p) = make_float2(acc[x][t][0], acc[x][t][1]);
-            *reinterpret_cast<float2 *>(p + 8 * Sh::kRowF) = make_float2(acc[x][t][2], acc[x][t][3]);
+            const int u = rt * 16 + r, w = ct * 16 + (tile0 + t) * 8 + 2 * c;
+            if (side0 + x) {
+                *reinterpret_cast<float2 *>(fq + Row(u).at + w) = make_float2(acc[x][t][0], acc[x][t][1]);
+                *reinterpret_cast<float2 *>(fq + Row(u + 8).at + w) = make_float2(acc[x][t][2], acc[x][t][3]);
+            } else {
+                if (w <= u) fk[triangle(u) + w] = acc[x][t][0];
+                if (w + 1 <= u) fk[triangle(u) + w + 1] = acc[x][t][1];
+                if (w <= u + 8) fk[triangle(u + 8) + w] = acc[x][t][2];
+                if (w + 1 <= u + 8) fk[triangle(u + 8) + w + 1] = acc[x][t][3];
+            }
         }
 }
 
@@ -152,7 +168,7 @@ __device__ __forceinline__ void products(const uint8_t *sk, const uint8_t *sq, i
 constexpr int kShortPath = 16;
 
 template <int D, int NT>
-__device__ __forceinline__ float walk_short(uint64_t path, int most, float *row, const float *fk, const float2 *gates) {
+__device__ __forceinline__ float walk_short(uint64_t path, int most, float *row, int cols, const float *fk, const float2 *gates) {
     using Sh = TreeShape<D, NT>;
     constexpr int kMost = 8 * NT < kShortPath ? 8 * NT : kShortPath;
     const int steps = __popcll(path);
@@ -168,20 +184,22 @@ __device__ __forceinline__ float walk_short(uint64_t path, int most, float *row,
     }
     asm volatile("" ::: "memory");  // (the row is read as floats, then written as other types)
 #pragma unroll
-    for (int i = 0; i < Sh::kCols / 4; ++i) reinterpret_cast<uint4 *>(row)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < Sh::kCols / 4; ++i)
+        if (4 * i < cols) reinterpret_cast<uint4 *>(row)[i] = make_uint4(0, 0, 0, 0);
     asm volatile("" ::: "memory");
-    uint16_t *const hi = reinterpret_cast<uint16_t *>(row), *const lo = hi + Sh::kLo / 2;
+    uint16_t *const hi = reinterpret_cast<uint16_t *>(row), *const lo = hi + cols;
     float decay = 1.f;
     float2 ab = most > 0 ? gates[x[0]] : make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < kMost; ++i) {
         if (i >= most) break;
         const float a = ab.x, c = ab.y * g[i], ac = -a * c;
+        const float *const kk = fk + triangle(x[i]);  // (places behind the last: any number)
         if (i + 1 < kMost && i + 1 < most) ab = gates[x[i + 1 < kMost ? i + 1 : i]];
 #pragma unroll
         for (int j = i + 1; j < kMost; ++j) {
             if (j >= most) break;
-            g[j] = fmaf(ac, fk[x[i] * Sh::kRowF + x[j]], a * g[j]);
+            g[j] = fmaf(ac, kk[x[j]], a * g[j]);
         }
         if (i < steps) {
             hi[x[i]] = static_cast<uint16_t>(__float_as_uint(c) >> 16);
@@ -195,7 +213,7 @@ __device__ __forceinline__ float walk_short(uint64_t path, int most, float *row,
 // A path of any length, on `row` itself: a quad takes the nodes above in turn, and what one lane has written is another's c
 // four nodes on.  The same operations, and so the same bits.
 template <int D, int NT>
-__device__ __forceinline__ float walk_long(const uint64_t path, float *row, const float *fk, const float2 *gates, int sub) {
+__device__ __forceinline__ float walk_long(const uint64_t path, float *row, int cols, const float *fk, const float2 *gates, int sub) {
     using Sh = TreeShape<D, NT>;
     const uint32_t quad = 0xfu << (threadIdx.x & 28);
     float decay = 1.f;
@@ -208,7 +226,7 @@ __device__ __forceinline__ float walk_long(const uint64_t path, float *row, cons
         __syncwarp(quad);
         if (sub == 0) row[w] = c;
         decay *= a;
-        const float *const kk = fk + w * Sh::kRowF;
+        const float *const kk = fk + triangle(w);
         uint64_t mine = left & (0x1111111111111111ull << sub);
 #pragma unroll 1
         while (mine) {
@@ -231,15 +249,16 @@ __device__ __forceinline__ float walk_long(const uint64_t path, float *row, cons
 #pragma unroll
     for (int i = 0; i < Sh::kCols / 8; ++i) {
         const int w = 2 * (sub + 4 * i);
-        c[i] = *reinterpret_cast<const float2 *>(row + w);
+        c[i] = w < cols ? *reinterpret_cast<const float2 *>(row + w) : make_float2(0.f, 0.f);
         if (!(path >> w & 1)) c[i].x = 0.f;
         if (!(path >> w & 2)) c[i].y = 0.f;
     }
     __syncwarp(quad);
 #pragma unroll
     for (int i = 0; i < Sh::kCols / 8; ++i) {
+        if (2 * (sub + 4 * i) >= cols) continue;
         uint32_t *const to = reinterpret_cast<uint32_t *>(row) + sub + 4 * i;
-        split2(c[i].x, c[i].y, to, to + Sh::kLo / 4);
+        split2(c[i].x, c[i].y, to, to + cols / 2);
     }
     return decay;
 }
@@ -250,7 +269,7 @@ __global__ void __launch_bounds__(TreeShape<D, NT>::kThreads, TreeShape<D, NT>::
     extern __shared__ __align__(16) uint8_t smem[];
     uint8_t *const sk = smem, *const sq = smem + Sh::kQ;
     float *const fk = reinterpret_cast<float *>(smem + Sh::kFK), *const fq = reinterpret_cast<float *>(smem + Sh::kFQ);
-    const uint8_t *const chi = smem + Sh::kFQ, *const clo = chi + Sh::kLo;
+    const uint8_t *const rows = smem + Sh::kFQ;  // of C
     uint64_t *const word = reinterpret_cast<uint64_t *>(smem + Sh::kWord);
     float2 *const gates = reinterpret_cast<float2 *>(smem + Sh::kGate);  // decay and beta
     float *const gamma = reinterpret_cast<float *>(gates + Sh::kNodes);
@@ -322,6 +341,11 @@ __global__ void __launch_bounds__(TreeShape<D, NT>::kThreads, TreeShape<D, NT>::
     }
 #pragma unroll
     for (int g = 0; g < Sh::kAhead; ++g) ask(g);
+    if (Sh::kAhead == 1) {  // the registers hold little of the state: the rest waits in L2
+        const float *p = a.state + (static_cast<int64_t>(slot) * a.h_v + head) * (D * D) + tid * 32;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i * (32 * Sh::kThreads)));
+    }
     if (tid < Sh::kNodes) {
         word[tid] = path;
         gates[tid] = make_float2(expf(my_g), my_beta);
@@ -357,12 +381,12 @@ __global__ void __launch_bounds__(TreeShape<D, NT>::kThreads, TreeShape<D, NT>::
         path = mine ? word[u] : 0;
         const int most = __reduce_max_sync(0xffffffffu, __popcll(path));
         float g = 0.f;
-        if (mine) g = walk_short<D, NT>(path, most, fq + u * Sh::kRowF, fk, gates);
+        if (mine) g = walk_short<D, NT>(path, most, fq + Row(u).at, Row(u).cols, fk, gates);
         if (lane < kPer) gamma[u] = g;
     } else {
 #pragma unroll 1
         for (int u = tid >> 2; u < Sh::kNodes; u += D / 4) {  // (whole quads: one node's lanes stay together)
-            const float g = u < m ? walk_long<D, NT>(word[u], fq + u * Sh::kRowF, fk, gates, c) : 0.f;
+            const float g = u < m ? walk_long<D, NT>(word[u], fq + Row(u).at, Row(u).cols, fk, gates, c) : 0.f;
             if (c == 0) gamma[u] = g;
         }
     }
@@ -381,7 +405,7 @@ __global__ void __launch_bounds__(TreeShape<D, NT>::kThreads, TreeShape<D, NT>::
 #pragma unroll
         for (int g = 0; g < Sh::kGroups; ++g) {
             const float4(&x)[4] = s[g % Sh::kAhead];
-            if (g == (Sh::kStageV ? Sh::kGroups - 1 : 0)) {  // v of node 8 t + r, values 2c and 2c + 1, and 8 further on
+            if (g == Sh::kGroups - 1) {  // v of node 8 t + r, values 2c and 2c + 1, and 8 further on
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     v[t][0] = v[t][1] = 0;
@@ -409,7 +433,7 @@ __global__ void __launch_bounds__(TreeShape<D, NT>::kThreads, TreeShape<D, NT>::
             else if (g + Sh::kAhead < Sh::kGroups)
                 ask(Sh::kGroups + g + Sh::kAhead);
             // Two tiles at a time: four sums that do not wait for one another.
-            constexpr int kStep = NT == 1 ? 1 : 2;
+            constexpr int kStep = NT == 1 || NT == 8 ? 1 : 2;
 #pragma unroll
             for (int t0 = 0; t0 < NT; t0 += kStep) {
                 if (t0 * 8 >= m) break;
@@ -458,11 +482,11 @@ __global__ void __launch_bounds__(TreeShape<D, NT>::kThreads, TreeShape<D, NT>::
                     for (int t2 = 0; t2 < NT; ++t2)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            const int u = t2 * 8 + 2 * c + (i & 1), at = u * Sh::kRowC + w * 2;
+                            const int u = t2 * 8 + 2 * c + (i & 1), at = Row(u).at * 4 + w * 2;
                             const float x = i & 2 ? x1 : x0;
                             if (!finite(x) && (word[u] >> w & 1))
-                                o[t2][i] = fmaf(bf16_bits_to_float(*reinterpret_cast<const uint16_t *>(chi + at)) +
-                                                    bf16_bits_to_float(*reinterpret_cast<const uint16_t *>(clo + at)),
+                                o[t2][i] = fmaf(bf16_bits_to_float(*reinterpret_cast<const uint16_t *>(rows + at)) +
+                                                    bf16_bits_to_float(*reinterpret_cast<const uint16_t *>(rows + at + Row(u).lo())),
                                                 x, o[t2][i]);
                         }
                 }
@@ -489,9 +513,11 @@ __global__ void __launch_bounds__(TreeShape<D, NT>::kThreads, TreeShape<D, NT>::
                 uint32_t h[kStep][2], l[kStep][2];
 #pragma unroll
                 for (int t = 0; t < kStep; ++t) {
-                    const int at = ((t0 + t) * 8 + r) * Sh::kRowC + kt * 32 + c * 4;
-                    h[t][0] = *reinterpret_cast<const uint32_t *>(chi + at), h[t][1] = *reinterpret_cast<const uint32_t *>(chi + at + 16);
-                    l[t][0] = *reinterpret_cast<const uint32_t *>(clo + at), l[t][1] = *reinterpret_cast<const uint32_t *>(clo + at + 16);
+                    if (t0 + t < 2 * kt) continue;
+                    const Row row(8 * (t0 + t));
+                    const uint8_t *const p = rows + row.at * 4 + r * (4 * row.cols + 16) + kt * 32 + c * 4;
+                    h[t][0] = *reinterpret_cast<const uint32_t *>(p), h[t][1] = *reinterpret_cast<const uint32_t *>(p + 16);
+                    l[t][0] = *reinterpret_cast<const uint32_t *>(p + row.lo()), l[t][1] = *reinterpret_cast<const uint32_t *>(p + row.lo() + 16);
                 }
 #pragma unroll
                 for (int t = 0; t < kStep; ++t)
