@@ -69,6 +69,7 @@
 #include <cudaTypedefs.h>
 #include <limits.h>
 #include <stddef.h>
+#include <type_traits>
 
 #ifndef GDN_WAIT_CYCLES
 #define GDN_WAIT_CYCLES 2000000000LL  // about a second; under 2^32
@@ -280,12 +281,12 @@ struct Item {
     int32_t req, head;  // request, K/V head
     int32_t tok, n;     // first token (row of q) and tokens
     int32_t pos;        // position of the first token
-    int32_t ctx;        // keys before the request's new tokens (negative: as many of those have none)
     int32_t lo, hi;     // key tiles
     // Of a request that is split (rows >= 0): its row items' places among the rows to join (first token, head 0); the
     // first token's first partial, partials from one token to the next, parts of the row item, which one this is.
     int64_t rows, partial;
     int32_t splits, parts, part;
+    int32_t ctx;  // with kTree: keys before the request's new tokens (negative: as many of those have none)
 };
 
 template <int D>
@@ -599,7 +600,7 @@ __device__ void schedule(const AttentionLaunch &L, Control<D> *ctl, const Waiter
             it.n = m - u < p.item_tokens ? m - u : p.item_tokens;
             it.tok = first + u;
             it.pos = kv - m + u;
-            it.ctx = kv - m;
+            if (kTree) it.ctx = kv - m;
             int32_t lo, hi;
             key_tiles(kv, m, u, it.n, a.window, &lo, &hi);
             int32_t split_lo = 0, split_hi = splits - 1;
@@ -1338,8 +1339,6 @@ __device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float s) {
 struct LeftOut {
     int2 past, next;
     int32_t key_lo, key_hi;  // what the row sees
-    int32_t ctx;             // in a tree: first new token's key
-    uint64_t word;           // and which of those keys
     int64_t req, head;       // request, K/V head
     const uint16_t *q;       // of the row
     float mc;                // its maximum times c
@@ -1347,8 +1346,12 @@ struct LeftOut {
     bool two;
     float f0, f1;
 };
+struct TreeLeftOut : LeftOut {
+    int32_t ctx;    // the first new token's key,
+    uint64_t word;  // and which of theirs the row sees
+};
 template <int D, bool kHalf, bool kTree>
-__device__ __noinline__ void add_left_out(const AttentionLaunch &L, const LeftOut r) {
+__device__ __noinline__ void add_left_out(const AttentionLaunch &L, const std::conditional_t<kTree, TreeLeftOut, LeftOut> r) {
     const gdn_paged_cache_t &c = L.a.cache;
     const int lane = threadIdx.x & 31;
     // Element 0 of key j's K or V; null: a bad page, whose keys are zeros.
@@ -1384,7 +1387,8 @@ __device__ __noinline__ void add_left_out(const AttentionLaunch &L, const LeftOu
 #pragma unroll 1
         for (uint32_t found = __ballot_sync(0xffffffffu, not_finite<kHalf>(top)); found; found &= found - 1) {
             const int32_t j = __shfl_sync(0xffffffffu, mine, __ffs(found) - 1);
-            const bool sees = j >= r.key_lo && j < r.key_hi && (!kTree || j < r.ctx || (r.word >> (j - r.ctx) & 1));
+            bool sees = j >= r.key_lo && j < r.key_hi;
+            if constexpr (kTree) sees = sees && (j < r.ctx || (r.word >> (j - r.ctx) & 1));
             const uint4 *k = reinterpret_cast<const uint4 *>(key(j, c.k, c.k_page_stride, c.k_slot_stride, c.k_head_stride));
             const uint4 *v = reinterpret_cast<const uint4 *>(key(j, c.v, c.v_page_stride, c.v_slot_stride, c.v_head_stride));
             float s = 0.f;
@@ -1656,13 +1660,15 @@ __device__ void softmax_rows(const AttentionLaunch &L, Control<D> *ctl, uint8_t 
             if (__any_sync(0xffffffffu, *static_cast<volatile uint32_t *>(ctl->bad + sl) == n + 1)) {
                 // Keys of the item's tiles that its tokens see differently, as they were looked through above: behind the
                 // last token's window, past the first token.
-                LeftOut left;
+                std::conditional_t<kTree, TreeLeftOut, LeftOut> left;
                 const int32_t end = it.hi * kKeys < row_hi ? it.hi * kKeys : row_hi;
                 left.past = make_int2(0, 0);
                 if (a.window > 0) left.past = make_int2(max(row_lo, it.lo * kKeys), min(it.pos + it.n - a.window, end));
                 left.next = make_int2(max(max(kTree ? it.ctx : it.pos + 1, it.lo * kKeys), left.past.y), end);
-                left.ctx = it.ctx;
-                left.word = word;
+                if constexpr (kTree) {
+                    left.ctx = it.ctx;
+                    left.word = word;
+                }
                 left.key_lo = writes ? key_lo : INT_MAX;
                 left.key_hi = key_hi;
                 left.req = it.req;
