@@ -572,8 +572,9 @@ gdn_status_t gdn_tree_attention(const gdn_paged_cache_t *cache, int32_t num_reqs
  *   cu_seqlens   [num_rows + 1] int32: the tokens of each row;
  *   masks        [num_tokens];  q, k [num_tokens][h_k][d_k], v, o
  *                [num_tokens][h_v][d_v] bf16;  g, beta [num_tokens][h_v] fp32.
- *   state        [num_slots][h_v][d_v][d_k] fp32, read at src_slot[r]; a
- *                negative slot marks a padded row, whose outputs are zeros.
+ *   state        [num_slots][h_v][d_v][d_k] fp32, 32-byte aligned, read at
+ *                src_slot[r]; a negative slot marks a padded row, whose outputs
+ *                are zeros.
  * Products with the state take each of its values to within 2^-15 of it, and
  * so do those of the nodes among each other; sums are fp32, o is rounded once.
  * Tokens from cu_seqlens[num_rows] on get zeros.  GDN_DEV_BAD_SLOT (a slot

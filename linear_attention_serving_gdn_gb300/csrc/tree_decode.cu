@@ -59,10 +59,14 @@ __device__ __forceinline__ void copy16(uint32_t to, const void *from, bool some)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(some ? 16 : 0) : "memory");
 }
 
-__device__ __forceinline__ float4 load_state(const float *p) {
-    float4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+// 8 values, read once: whole sectors.
+struct Eight {
+    float x[8];
+};
+__device__ __forceinline__ Eight load_state(const float *p) {
+    Eight v;
+    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(v.x[0]), "=f"(v.x[1]), "=f"(v.x[2]), "=f"(v.x[3]), "=f"(v.x[4]), "=f"(v.x[5]), "=f"(v.x[6]), "=f"(v.x[7])
                  : "l"(p));
     return v;
 }
@@ -299,16 +303,16 @@ __global__ void __launch_bounds__(TreeShape<D, NT>::kThreads, TreeShape<D, NT>::
         return;
     }
 
-    // 1. The state's rows 32 warp + r and + 8, in groups of 32 columns: 8 neighbouring columns a lane.
-    const float *const s_row = a.state + ((static_cast<int64_t>(slot) * a.h_v + head) * D + warp * 32 + r) * D + c * 8;
-    float4 s[Sh::kAhead][4];
+    // 1. The state's rows, of 16 those that make row r of a product's tile and row r + 8, in groups of 32 columns: 8
+    // neighbouring columns a lane.  Rows 2c, 2c + 1, 2c + 8 and 2c + 9 of a tile are values 4c to 4c + 3, so that a lane has
+    // four neighbouring values of v and o.
+    const float *const s_row =
+        a.state + ((static_cast<int64_t>(slot) * a.h_v + head) * D + warp * 32 + (r >> 1) * 4 + (r & 1)) * D + c * 8;
+    Eight s[Sh::kAhead][2];
     auto ask = [&](int g) {  // group g, counted over both 16 rows
-        float4(&x)[4] = s[g % Sh::kAhead];
         const float *p = s_row + (g / Sh::kGroups) * (16 * D) + (g % Sh::kGroups) * 32;
-        x[0] = load_state(p);
-        x[1] = load_state(p + 4);
-        x[2] = load_state(p + 8 * D);
-        x[3] = load_state(p + 8 * D + 4);
+        s[g % Sh::kAhead][0] = load_state(p);
+        s[g % Sh::kAhead][1] = load_state(p + 2 * D);
     };
     // (k and q first, which the block waits for; the state's rows are there when it comes to them.)
     uint64_t path = 0;  // of node tid, as long as there is one (itself and nodes before it)
@@ -342,9 +346,9 @@ __global__ void __launch_bounds__(TreeShape<D, NT>::kThreads, TreeShape<D, NT>::
 #pragma unroll
     for (int g = 0; g < Sh::kAhead; ++g) ask(g);
     if (Sh::kAhead == 1) {  // the registers hold little of the state: the rest waits in L2
-        const float *p = a.state + (static_cast<int64_t>(slot) * a.h_v + head) * (D * D) + tid * 32;
+        const float *p = a.state + (static_cast<int64_t>(slot) * a.h_v + head) * (D * D) + tid * 64;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i * (32 * Sh::kThreads)));
+        for (int i = 0; i < D / 64; ++i) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i * (64 * Sh::kThreads)));
     }
     if (tid < Sh::kNodes) {
         word[tid] = path;
@@ -397,43 +401,35 @@ __global__ void __launch_bounds__(TreeShape<D, NT>::kThreads, TreeShape<D, NT>::
         const int64_t value = (static_cast<int64_t>(b) * a.h_v + head) * D + warp * 32 + slab * 16;  // node 0's first of the slab
         // S^T [K; Q]: 16 values by the nodes.
         float y[NT][4], o[NT][4];
-        uint32_t v[NT][2];
+        uint2 v[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) y[t][i] = o[t][i] = 0.f;
 #pragma unroll
         for (int g = 0; g < Sh::kGroups; ++g) {
-            const float4(&x)[4] = s[g % Sh::kAhead];
-            if (g == Sh::kGroups - 1) {  // v of node 8 t + r, values 2c and 2c + 1, and 8 further on
+            const Eight(&x)[2] = s[g % Sh::kAhead];
+            if (g == Sh::kGroups - 1) {  // v of node 8 t + r, values 4c to 4c + 3
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    v[t][0] = v[t][1] = 0;
-                    if (t * 8 + r < m) {
-                        const uint32_t *p =
-                            (Sh::kStageV ? reinterpret_cast<const uint32_t *>(smem + Sh::kV + (t * 8 + r) * Sh::kRowV + warp * 64 + slab * 32)
-                                         : reinterpret_cast<const uint32_t *>(a.v + value + static_cast<int64_t>(t * 8 + r) * a.h_v * D)) + c;
-                        v[t][0] = *p;
-                        v[t][1] = p[4];
-                    }
+                    v[t] = make_uint2(0, 0);
+                    if (t * 8 + r < m)
+                        v[t] = Sh::kStageV ? *reinterpret_cast<const uint2 *>(smem + Sh::kV + (t * 8 + r) * Sh::kRowV + warp * 64 + slab * 32 + c * 8)
+                                           : __ldg(reinterpret_cast<const uint2 *>(a.v + value + static_cast<int64_t>(t * 8 + r) * a.h_v * D + c * 4));
                 }
             }
-            uint32_t hi[2][4], lo[2][4];
-            split2(x[0].x, x[0].y, &hi[0][0], &lo[0][0]);
-            split2(x[0].z, x[0].w, &hi[0][2], &lo[0][2]);
-            split2(x[1].x, x[1].y, &hi[1][0], &lo[1][0]);
-            split2(x[1].z, x[1].w, &hi[1][2], &lo[1][2]);
-            split2(x[2].x, x[2].y, &hi[0][1], &lo[0][1]);
-            split2(x[2].z, x[2].w, &hi[0][3], &lo[0][3]);
-            split2(x[3].x, x[3].y, &hi[1][1], &lo[1][1]);
-            split2(x[3].z, x[3].w, &hi[1][3], &lo[1][3]);
+            uint32_t hi[2][4], lo[2][4];  // of columns 0 to 3 and 4 to 7; element 2 j + i: row r + 8 i, columns 2 j and 2 j + 1 of them
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) split2(x[i & 1].x[4 * h + (i & 2)], x[i & 1].x[4 * h + (i & 2) + 1], &hi[h][i], &lo[h][i]);
             // The group after those in registers.
             if (slab == 0)
                 ask(g + Sh::kAhead);
             else if (g + Sh::kAhead < Sh::kGroups)
                 ask(Sh::kGroups + g + Sh::kAhead);
             // Two tiles at a time: four sums that do not wait for one another.
-            constexpr int kStep = NT == 1 || NT == 8 ? 1 : 2;
+            constexpr int kStep = NT == 1 ? 1 : 2;
 #pragma unroll
             for (int t0 = 0; t0 < NT; t0 += kStep) {
                 if (t0 * 8 >= m) break;
@@ -453,7 +449,7 @@ __global__ void __launch_bounds__(TreeShape<D, NT>::kThreads, TreeShape<D, NT>::
                     }
             }
         }
-        // R in y (elements 0, 1: value r, nodes 2c and 2c + 1 of the tile; 2, 3: value r + 8), G o in o.
+        // R in y (elements 0, 1: row r, nodes 2c and 2c + 1 of the tile; 2, 3: row r + 8), G o in o.
         // (Nodes past the last have k, v and G of zero, so R of zero, or NaN, which is left out.)
         float not_zero = 0.f;  // NaN if some R is not finite
 #pragma unroll
@@ -461,7 +457,7 @@ __global__ void __launch_bounds__(TreeShape<D, NT>::kThreads, TreeShape<D, NT>::
             const float2 g = *reinterpret_cast<const float2 *>(gamma + t * 8 + 2 * c);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const uint32_t vt = transpose8(v[t][i]);
+                const uint32_t vt = transpose8(i ? v[t].y : v[t].x);
                 y[t][2 * i] = fmaf(-g.x, y[t][2 * i], __uint_as_float(vt << 16));
                 y[t][2 * i + 1] = fmaf(-g.y, y[t][2 * i + 1], __uint_as_float(vt & 0xffff0000u));
                 o[t][2 * i] *= g.x;
@@ -535,14 +531,11 @@ __global__ void __launch_bounds__(TreeShape<D, NT>::kThreads, TreeShape<D, NT>::
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < 2; ++i) out[t][i] = transpose8(pack_bf16(o[t][2 * i] * a.scale, o[t][2 * i + 1] * a.scale));
-        uint16_t *p = a.o + value + static_cast<int64_t>(r) * a.h_v * D + 2 * c;
+        uint16_t *p = a.o + value + static_cast<int64_t>(r) * a.h_v * D + 4 * c;
         const int64_t step = static_cast<int64_t>(8) * a.h_v * D;
 #pragma unroll
         for (int t = 0; t < NT; ++t, p += step)
-            if (t * 8 + r < m) {
-                *reinterpret_cast<uint32_t *>(p) = out[t][0];
-                *reinterpret_cast<uint32_t *>(p + 8) = out[t][1];
-            }
+            if (t * 8 + r < m) *reinterpret_cast<uint2 *>(p) = make_uint2(out[t][0], out[t][1]);
     }
 }
 

@@ -81,7 +81,7 @@ def test_bad_attention_arguments(gdn, args, status):
     (dict(most=65), INVALID), (dict(slots=-1), INVALID), (dict(T=1 << 31), UNSUPPORTED), (dict(n=1 << 29), UNSUPPORTED),
     (dict(cu=None), INVALID), (dict(masks=None), INVALID), (dict(q=None), INVALID), (dict(k=ODD), INVALID),
     (dict(v=None), INVALID), (dict(g=None), INVALID), (dict(beta=None), INVALID), (dict(state=ODD), INVALID),
-    (dict(src=None), INVALID), (dict(o=ODD), INVALID)])
+    (dict(state=ctypes.c_void_p(0x10010)), INVALID), (dict(src=None), INVALID), (dict(o=ODD), INVALID)])
 def test_bad_decode_arguments(gdn, args, status):
     assert decode(gdn, **args) == status
     assert decode(gdn, T=0) == 0 and decode(gdn, n=0) == 0
