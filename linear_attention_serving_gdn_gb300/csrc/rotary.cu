@@ -6,8 +6,10 @@
 // int32 position: no range reduction, no 64-bit floating point.  Its upper 32
 // bits are the turn's fraction to 2^-32; sincospif takes it from there.
 //
-// Split.  A thread takes eight pairs (two 16-byte pieces) of a token in all or
-// some of its heads; with few tokens the heads are dealt out over more threads.
+// Split.  A thread takes eight pairs (two 16-byte pieces; four or two, or a
+// pair alone, where sizes, strides or addresses do not allow them) of a token
+// in all or some of its heads; with few tokens the heads are dealt out over
+// more threads.
 // A block makes the angles of its tokens once, in shared memory, while the
 // first heads are on the way from memory.
 // Bound by HBM for long chunks, by the launch for decode steps.
@@ -21,7 +23,6 @@ namespace {
 
 constexpr int kRotaryThreads = 256;
 constexpr int kRotaryUnroll = 4;  // heads whose loads are in flight at once
-constexpr int kRotaryPairs = kRotaryThreads * 8;  // of a block: eight per turning thread
 
 // Cosine and sine of a pair at a position, times the magnitude.
 __device__ __forceinline__ float2 turn(const RotaryArgs &a, int64_t position, uint64_t frequency) {
@@ -55,12 +56,42 @@ __device__ __forceinline__ const RotarySide &side_of(const RotaryArgs &a, int32_
     return a.side[1];
 }
 
-// Lanes of a token: turns = rot / 16 of two pieces to turn, then those of two pieces to copy (where the output lies
+// A piece of kWide elements.
+template <int kWide>
+struct Piece {
+    uint32_t w[kWide / 2];
+};
+template <int kWide>
+__device__ __forceinline__ Piece<kWide> load_piece(const uint16_t *p) {
+    Piece<kWide> x;
+    if constexpr (kWide == 8) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        x.w[0] = v.x, x.w[1] = v.y, x.w[2] = v.z, x.w[3] = v.w;
+    } else if constexpr (kWide == 4) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        x.w[0] = v.x, x.w[1] = v.y;
+    } else {
+        x.w[0] = *reinterpret_cast<const uint32_t *>(p);
+    }
+    return x;
+}
+template <int kWide>
+__device__ __forceinline__ void store_piece(uint16_t *p, const Piece<kWide> &x) {
+    if constexpr (kWide == 8)
+        *reinterpret_cast<uint4 *>(p) = make_uint4(x.w[0], x.w[1], x.w[2], x.w[3]);
+    else if constexpr (kWide == 4)
+        *reinterpret_cast<uint2 *>(p) = make_uint2(x.w[0], x.w[1]);
+    else
+        *reinterpret_cast<uint32_t *>(p) = x.w[0];
+}
+
+// Lanes of a token: turns = rot / (2 kWide) of two pieces to turn, then those of two pieces to copy (where the output lies
 // elsewhere).  `splits` threads share a lane's heads; a block takes `tokens` tokens, lanes * splits * tokens <= its threads.
-template <bool kHalf, bool kInterleaved, bool kOnce>
-__global__ void __launch_bounds__(kRotaryThreads, kOnce ? 4 : 3) rotary_kernel(const __grid_constant__ RotaryArgs a, int32_t turns, int32_t lanes,
-                                                                   int32_t splits, int32_t tokens) {
-    __shared__ float2 angle[kRotaryPairs];  // cosine and sine of the tokens' pairs
+// With kOnce a thread's heads are all asked for at once, before the angles are made.
+template <int kWide, bool kHalf, bool kInterleaved, bool kOnce>
+__global__ void __launch_bounds__(kRotaryThreads, kOnce ? 4 : 3) rotary_kernel(const __grid_constant__ RotaryArgs a, int32_t turns,
+                                                                              int32_t lanes, int32_t splits, int32_t tokens) {
+    __shared__ float2 angle[kRotaryThreads * kWide];  // cosine and sine of the tokens' pairs
     const int32_t per_token = lanes * splits;
     const int32_t token = static_cast<int32_t>(threadIdx.x) / per_token, rest = static_cast<int32_t>(threadIdx.x) - token * per_token;
     const int32_t split = rest / lanes, lane = rest - split * lanes;
@@ -69,10 +100,10 @@ __global__ void __launch_bounds__(kRotaryThreads, kOnce ? 4 : 3) rotary_kernel(c
     const int32_t heads = a.side[0].h + a.side[1].h;
     const bool turning = lane < turns;
     // First elements of the two pieces; a last copy lane may have only one.
-    const int32_t at0 = turning ? lane * (kInterleaved ? 16 : 8) : a.rot + (lane - turns) * 16;
-    const int32_t at1 = turning && !kInterleaved ? at0 + a.rot / 2 : at0 + 8;
+    const int32_t at0 = turning ? lane * (kInterleaved ? 2 * kWide : kWide) : a.rot + (lane - turns) * (2 * kWide);
+    const int32_t at1 = turning && !kInterleaved ? at0 + a.rot / 2 : at0 + kWide;
     const bool two = at1 < a.d;
-    uint4 x[kRotaryUnroll], y[kRotaryUnroll];
+    Piece<kWide> x[kRotaryUnroll], y[kRotaryUnroll];
     auto load = [&](int32_t h0) {
 #pragma unroll
         for (int k = 0; k < kRotaryUnroll; ++k) {
@@ -81,11 +112,11 @@ __global__ void __launch_bounds__(kRotaryThreads, kOnce ? 4 : 3) rotary_kernel(c
             const RotarySide &side = side_of(a, &h);
             if (!turning && side.src == side.dst) continue;
             const uint16_t *p = side.src + t * side.token_stride + h * side.head_stride;
-            x[k] = *reinterpret_cast<const uint4 *>(p + at0);
-            if (two) y[k] = *reinterpret_cast<const uint4 *>(p + at1);
+            x[k] = load_piece<kWide>(p + at0);
+            if (two) y[k] = load_piece<kWide>(p + at1);
         }
     };
-    if (kOnce) load(split);  // (on the way while the angles are made)
+    if (kOnce) load(split);
     const int32_t pairs = a.rot / 2;
     for (int32_t i = threadIdx.x; i < tokens * pairs; i += kRotaryThreads) {
         const int32_t of = i / pairs;
@@ -93,13 +124,10 @@ __global__ void __launch_bounds__(kRotaryThreads, kOnce ? 4 : 3) rotary_kernel(c
             angle[i] = turn(a, a.positions[first + of], a.frequencies[i - of * pairs]);
     }
     __syncthreads();
-    float c[8], s[8];
+    float2 cs[kWide];
     if (turning && live)
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-            const float4 cs = *reinterpret_cast<const float4 *>(angle + token * pairs + lane * 8 + j);
-            c[j] = cs.x, s[j] = cs.y, c[j + 1] = cs.z, s[j + 1] = cs.w;
-        }
+        for (int j = 0; j < kWide; ++j) cs[j] = angle[token * pairs + lane * kWide + j];
 #pragma unroll 1
     for (int32_t h0 = split; live && h0 < heads; h0 += splits * kRotaryUnroll) {
         if (!kOnce) load(h0);
@@ -110,27 +138,23 @@ __global__ void __launch_bounds__(kRotaryThreads, kOnce ? 4 : 3) rotary_kernel(c
             const RotarySide &side = side_of(a, &h);
             if (!turning && side.src == side.dst) continue;
             if (turning) {
-                uint32_t u[8] = {x[k].x, x[k].y, x[k].z, x[k].w, y[k].x, y[k].y, y[k].z, y[k].w};
-                if (kInterleaved) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float2 v = unpack<kHalf>(u[j]);
-                        u[j] = pack<kHalf>(v.x * c[j] - v.y * s[j], v.y * c[j] + v.x * s[j]);
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 v = unpack<kHalf>(u[j]), w = unpack<kHalf>(u[j + 4]);
-                        u[j] = pack<kHalf>(v.x * c[2 * j] - w.x * s[2 * j], v.y * c[2 * j + 1] - w.y * s[2 * j + 1]);
-                        u[j + 4] = pack<kHalf>(w.x * c[2 * j] + v.x * s[2 * j], w.y * c[2 * j + 1] + v.y * s[2 * j + 1]);
+                for (int j = 0; j < kWide / 2; ++j) {
+                    const float2 v = unpack<kHalf>(x[k].w[j]), w = unpack<kHalf>(y[k].w[j]);
+                    if (kInterleaved) {
+                        const float2 e = cs[j], f = cs[kWide / 2 + j];
+                        x[k].w[j] = pack<kHalf>(v.x * e.x - v.y * e.y, v.y * e.x + v.x * e.y);
+                        y[k].w[j] = pack<kHalf>(w.x * f.x - w.y * f.y, w.y * f.x + w.x * f.y);
+                    } else {
+                        const float2 e = cs[2 * j], f = cs[2 * j + 1];
+                        x[k].w[j] = pack<kHalf>(v.x * e.x - w.x * e.y, v.y * f.x - w.y * f.y);
+                        y[k].w[j] = pack<kHalf>(w.x * e.x + v.x * e.y, w.y * f.x + v.y * f.y);
                     }
                 }
-                x[k] = make_uint4(u[0], u[1], u[2], u[3]);
-                y[k] = make_uint4(u[4], u[5], u[6], u[7]);
             }
             uint16_t *p = side.dst + t * side.dst_token_stride + h * side.dst_head_stride;
-            *reinterpret_cast<uint4 *>(p + at0) = x[k];
-            if (two) *reinterpret_cast<uint4 *>(p + at1) = y[k];
+            store_piece<kWide>(p + at0, x[k]);
+            if (two) store_piece<kWide>(p + at1, y[k]);
         }
         if (kOnce) break;
     }
@@ -176,18 +200,20 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_any_kernel(const __grid
 }
 
 using RotaryKernel = void (*)(const RotaryArgs, int32_t, int32_t, int32_t, int32_t);
-template <bool kHalf, bool kInterleaved>
+template <int kWide, bool kHalf, bool kInterleaved>
 RotaryKernel pick_once(bool once) {
-    return once ? rotary_kernel<kHalf, kInterleaved, true> : rotary_kernel<kHalf, kInterleaved, false>;
+    return once ? rotary_kernel<kWide, kHalf, kInterleaved, true> : rotary_kernel<kWide, kHalf, kInterleaved, false>;
 }
+template <int kWide>
 RotaryKernel pick(bool half, bool interleaved, bool once) {
-    if (half) return interleaved ? pick_once<true, true>(once) : pick_once<true, false>(once);
-    return interleaved ? pick_once<false, true>(once) : pick_once<false, false>(once);
+    if (half) return interleaved ? pick_once<kWide, true, true>(once) : pick_once<kWide, true, false>(once);
+    return interleaved ? pick_once<kWide, false, true>(once) : pick_once<kWide, false, false>(once);
 }
 
-bool pieces16(const RotarySide &s) {
-    return ((reinterpret_cast<uintptr_t>(s.src) | reinterpret_cast<uintptr_t>(s.dst)) & 15u) == 0 &&
-           ((s.token_stride | s.head_stride | s.dst_token_stride | s.dst_head_stride) & 7) == 0;
+// Whether pieces of `wide` elements lie at multiples of their size.
+bool pieces_of(const RotarySide &s, int32_t wide) {
+    return ((reinterpret_cast<uintptr_t>(s.src) | reinterpret_cast<uintptr_t>(s.dst)) & (2 * wide - 1)) == 0 &&
+           ((s.token_stride | s.head_stride | s.dst_token_stride | s.dst_head_stride) & (wide - 1)) == 0;
 }
 
 }  // namespace
@@ -196,28 +222,31 @@ cudaError_t launch_rotary(const RotaryArgs &a, cudaStream_t stream) {
     int dev = 0, sms = 0;
     if (!current_device(&dev, &sms)) return cudaErrorInvalidDevice;
     const bool copies = a.side[0].src != a.side[0].dst || a.side[1].src != a.side[1].dst;
-    const bool wide = a.rot % 16 == 0 && a.d % 8 == 0 && pieces16(a.side[0]) && pieces16(a.side[1]) &&
-                      (reinterpret_cast<uintptr_t>(a.frequencies) & 15u) == 0;
-    const int32_t turns = wide ? a.rot / 16 : a.rot / 2;
-    const int32_t lanes = turns + (!copies ? 0 : wide ? (a.d - a.rot + 15) / 16 : a.d - a.rot);
+    int32_t wide = 8;  // elements of a piece, 1: single pairs
+    while (wide > 1 && (a.rot % (2 * wide) != 0 || a.d % wide != 0 || !pieces_of(a.side[0], wide) || !pieces_of(a.side[1], wide)))
+        wide /= 2;
+    const int32_t turns = a.rot / (2 * wide);
+    const int32_t lanes = turns + (!copies ? 0 : wide > 1 ? (a.d - a.rot + 2 * wide - 1) / (2 * wide) : a.d - a.rot);
     // Heads are dealt out until the GPU's threads are all used: each keeps as many as it can, for the angles' sake.
     const int32_t heads = a.side[0].h + a.side[1].h;
     const int64_t have = a.num_tokens * lanes, want = static_cast<int64_t>(sms) * 2048;
     int64_t splits = (want + have - 1) / have;
     if (splits > heads) splits = heads;
     const bool half = a.dtype == GDN_FP16;
-    if (!wide) {
+    if (wide == 1) {
         const int64_t blocks = (have * splits + kRotaryThreads - 1) / kRotaryThreads;
         if (blocks > INT_MAX) return cudaErrorInvalidConfiguration;
         (half ? rotary_any_kernel<true> : rotary_any_kernel<false>)<<<static_cast<unsigned>(blocks), kRotaryThreads, 0, stream>>>(
             a, turns, lanes, static_cast<int32_t>(splits));
         return cudaGetLastError();
     }
-    if (splits * lanes > kRotaryThreads) splits = kRotaryThreads / lanes;  // (at most 64 lanes: d <= 1024)
+    if (splits * lanes > kRotaryThreads) splits = kRotaryThreads / lanes;  // (at most 256 lanes: d <= 1024)
     const int32_t n = static_cast<int32_t>(splits), tokens = kRotaryThreads / (lanes * n);
-    const dim3 grid(static_cast<unsigned>((a.num_tokens + tokens - 1) / tokens));
-    const auto kernel = pick(half, a.interleaved, n * kRotaryUnroll >= heads);
-    kernel<<<grid, kRotaryThreads, 0, stream>>>(a, turns, lanes, n, tokens);
+    const bool once = n * kRotaryUnroll >= heads;
+    const RotaryKernel kernel = wide == 8   ? pick<8>(half, a.interleaved, once)
+                                : wide == 4 ? pick<4>(half, a.interleaved, once)
+                                            : pick<2>(half, a.interleaved, once);
+    kernel<<<static_cast<unsigned>((a.num_tokens + tokens - 1) / tokens), kRotaryThreads, 0, stream>>>(a, turns, lanes, n, tokens);
     return cudaGetLastError();
 }
 
