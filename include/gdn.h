@@ -577,8 +577,8 @@ gdn_status_t gdn_tree_attention(const gdn_paged_cache_t *cache, int32_t num_reqs
  *                are zeros.
  * Products with the state take each of its values to within 2^-15 of it, and
  * so do those of the nodes among each other; sums are fp32, o is rounded once.
- * Tokens from cu_seqlens[num_rows] on get zeros.  GDN_DEV_BAD_SLOT (a slot
- * >= num_slots) and GDN_DEV_BAD_LENGTH (more nodes than max_nodes): zero
+ * Tokens from cu_seqlens[num_rows] on get zeros (with num_rows = 0 nothing is
+ * written).  GDN_DEV_BAD_SLOT (a slot >= num_slots) and GDN_DEV_BAD_LENGTH (more nodes than max_nodes): zero
  * outputs; GDN_DEV_BAD_LENGTH also for a row whose cu_seqlens run backwards or
  * past cu_seqlens[num_rows] or num_tokens: it is skipped.
  * A node's outputs depend on its path and the row's state alone, bit for bit:
@@ -612,8 +612,8 @@ gdn_status_t gdn_rotary_frequencies(int32_t rotary_dim, double base, int32_t sca
                                     int64_t original_length, double beta_fast, double beta_slow, uint64_t *out);
 
 /* q or k of a rotation: element (t, h, i) of x at t * x_token_stride
- * + h * x_head_stride + i, and the same for out (elements; any alignment; the
- * width of its accesses is 16 bytes where addresses and strides allow).  out
+ * + h * x_head_stride + i, and the same for out (elements; any alignment:
+ * accesses are as wide as sizes, addresses and strides allow, 16 bytes at most).  out
  * may be x, with the same strides; else the two do not overlap. */
 typedef struct {
     const void *x;

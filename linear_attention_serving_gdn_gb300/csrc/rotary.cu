@@ -49,6 +49,11 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     return r;
 }
 
+// The pair (a, b), turned; written out so that every kernel gives the same bits.
+__device__ __forceinline__ float2 rotate(float a, float b, float2 cs) {
+    return make_float2(fmaf(a, cs.x, -(b * cs.y)), fmaf(b, cs.x, a * cs.y));
+}
+
 // The heads of both sides are counted on: q's, then k's.
 __device__ __forceinline__ const RotarySide &side_of(const RotaryArgs &a, int32_t *head) {
     if (*head < a.side[0].h) return a.side[0];
@@ -142,13 +147,13 @@ __global__ void __launch_bounds__(kRotaryThreads, kOnce ? 4 : 3) rotary_kernel(c
                 for (int j = 0; j < kWide / 2; ++j) {
                     const float2 v = unpack<kHalf>(x[k].w[j]), w = unpack<kHalf>(y[k].w[j]);
                     if (kInterleaved) {
-                        const float2 e = cs[j], f = cs[kWide / 2 + j];
-                        x[k].w[j] = pack<kHalf>(v.x * e.x - v.y * e.y, v.y * e.x + v.x * e.y);
-                        y[k].w[j] = pack<kHalf>(w.x * f.x - w.y * f.y, w.y * f.x + w.x * f.y);
+                        const float2 e = rotate(v.x, v.y, cs[j]), f = rotate(w.x, w.y, cs[kWide / 2 + j]);
+                        x[k].w[j] = pack<kHalf>(e.x, e.y);
+                        y[k].w[j] = pack<kHalf>(f.x, f.y);
                     } else {
-                        const float2 e = cs[2 * j], f = cs[2 * j + 1];
-                        x[k].w[j] = pack<kHalf>(v.x * e.x - w.x * e.y, v.y * f.x - w.y * f.y);
-                        y[k].w[j] = pack<kHalf>(w.x * e.x + v.x * e.y, w.y * f.x + v.y * f.y);
+                        const float2 e = rotate(v.x, w.x, cs[2 * j]), f = rotate(v.y, w.y, cs[2 * j + 1]);
+                        x[k].w[j] = pack<kHalf>(e.x, f.x);
+                        y[k].w[j] = pack<kHalf>(e.y, f.y);
                     }
                 }
             }
@@ -174,13 +179,11 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_any_kernel(const __grid
     const int32_t heads = a.side[0].h + a.side[1].h;
     const bool turning = lane < turns;
     int32_t at0 = a.rot + lane - turns, at1 = at0;
-    float c = 1.f, s = 0.f;
+    float2 cs = make_float2(1.f, 0.f);
     if (turning) {
         at0 = a.interleaved ? 2 * lane : lane;
         at1 = a.interleaved ? at0 + 1 : lane + a.rot / 2;
-        const float2 cs = turn(a, a.positions[t], a.frequencies[lane]);
-        c = cs.x;
-        s = cs.y;
+        cs = turn(a, a.positions[t], a.frequencies[lane]);
     }
     for (int32_t h0 = split; h0 < heads; h0 += splits) {
         int32_t h = h0;
@@ -193,7 +196,8 @@ __global__ void __launch_bounds__(kRotaryThreads) rotary_any_kernel(const __grid
             continue;
         }
         const float2 v = unpack<kHalf>(p[at0] | static_cast<uint32_t>(p[at1]) << 16);
-        const uint32_t out = pack<kHalf>(v.x * c - v.y * s, v.y * c + v.x * s);
+        const float2 e = rotate(v.x, v.y, cs);
+        const uint32_t out = pack<kHalf>(e.x, e.y);
         to[at0] = static_cast<uint16_t>(out);
         to[at1] = static_cast<uint16_t>(out >> 16);
     }

@@ -165,3 +165,35 @@ def test_capture_on_another_stream(gdn):
     torch.cuda.synchronize()
     assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
     gdn.gdn_rotary(q[:0], k[:0], positions[:0], freq)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("pad,start", [(4, 4), (2, 2), (6, 0), (4, 0), (1, 0)])
+def test_pieces_of_any_width_give_the_same_bits(gdn, pad, start, interleaved):
+    q, k = tensors(41, 5, 2, 96, "fp16", seed=6)
+    positions = torch.arange(41, device="cuda", dtype=torch.int32) * 777
+    freq = gdn.gdn_rotary_frequencies(64).cuda()
+    want_q, want_k = check(gdn, q, k, positions, freq, interleaved)
+    wide = torch.zeros((41, 7, 96 + pad + start), dtype=torch.float16, device="cuda")
+    view = wide[..., start:start + 96]
+    view.copy_(torch.cat([q, k], 1))
+    got = check(gdn, view[:, :5], view[:, 5:], positions, freq, interleaved)  # from there, into 16-byte rows
+    assert torch.equal(got[0], want_q) and torch.equal(got[1], want_k)
+    check(gdn, view[:, :5], view[:, 5:], positions, freq, interleaved, in_place=True)
+    assert torch.equal(view[:, :5], want_q) and torch.equal(view[:, 5:], want_k)
+    assert not wide[..., :start].any() and not wide[..., start + 96:].any()
+
+
+@pytest.mark.parametrize("d,rot", [(80, 20), (100, 16), (128, 128), (96, 32), (70, 68)])
+def test_many_tokens(gdn, d, rot):
+    T = 40000
+    q, k = tensors(T, 3, 1, d, "bf16", seed=7)
+    positions = torch.randint(0, 1 << 20, (T,), device="cuda", dtype=torch.int32)
+    freq = gdn.gdn_rotary_frequencies(rot).cuda()
+    outs = [torch.full(x.shape, float("nan"), dtype=x.dtype, device="cuda") for x in (q, k)]
+    gdn.gdn_rotary(q, k, positions, freq, *outs)
+    at = torch.cat([torch.arange(200), torch.randint(0, T, (200,)), torch.arange(T - 200, T)]).cuda()
+    for x, out in zip((q, k), outs):
+        assert torch.isfinite(out).all()
+        assert_close(out[at], *reference(x[at], positions[at], freq, False, 1.0))
+        assert torch.equal(out[..., rot:], x[..., rot:])

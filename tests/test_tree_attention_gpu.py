@@ -185,3 +185,44 @@ def test_replays_for_other_trees(gdn, heads):
     pu.assert_close(o, *tu.attention_reference(c, masks))
     other, st = tu.run_tree_attention(gdn, c, masks, max_kv_len=2000, stream=torch.cuda.Stream())
     assert st == 0 and torch.equal(other, o)
+
+
+@pytest.mark.parametrize("heads", [HEADS[0], HEADS[2], HEADS[5]])
+def test_pages_far_apart(gdn, heads):
+    # a cache whose offsets pass 2^31 elements
+    c, masks = case([(300, 20), (90, 64)], heads, page=64, seed=20)
+    want, _ = tu.run_tree_attention(gdn, c, masks)
+    used = c["k"].shape[0]
+    n = (1 << 31) // c["k"][0].numel() + used + 1
+    for x in "kv":
+        far = torch.empty((n,) + tuple(c[x].shape[1:]), dtype=c[x].dtype, device="cuda")
+        far[n - used:] = c[x]
+        c[x] = far
+    c["table"] = torch.where(c["table"] >= 0, c["table"] + (n - used), c["table"])
+    o, st = tu.run_tree_attention(gdn, c, masks)
+    assert st == 0 and torch.equal(o, want)
+
+
+@pytest.mark.parametrize("heads", [HEADS[0], HEADS[2]])
+def test_two_calls_at_once(gdn, heads):
+    cs = [case([(5000, 30), (700, 64), (9000, 3)] * 3, heads, shape, page=64, seed=21 + i) for i, shape in enumerate(("mixed", "flat"))]
+    wants = [tu.run_tree_attention(gdn, c, masks)[0] for c, masks in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    jobs = []
+    for (c, masks), want in zip(cs, wants):
+        T, h_q, d = c["q"].shape
+        n = gdn.gdn_paged_attention_workspace_bytes(h_q, c["k"].shape[2], d, len(c["lens"]), T, c["table"].shape[1] * 64)
+        jobs.append((torch.empty(n, dtype=torch.uint8, device="cuda"), [torch.empty_like(want) for _ in range(6)]))
+    torch.cuda.synchronize()
+    for i in range(6):
+        for (c, masks), (ws, outs), s in zip(cs, jobs, streams):
+            gdn.gdn_tree_attention(c["q"], c["k"], c["v"], c["table"], c["cu"], c["kv"], masks, outs[i], workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for (_, outs), w in zip(jobs, wants) for o in outs)
+
+
+def test_requests_that_share_pages(gdn):
+    # a common prefix, and one request drafted twice in one call (its own pages read by both)
+    c, masks = case([(500, 12), (500, 40)], HEADS[0], page=64, seed=23)
+    c["table"][1, :7] = c["table"][0, :7]
+    check(gdn, c, masks)

@@ -178,3 +178,58 @@ def test_replays_for_other_trees(gdn):
     tu.assert_close(o, *tu.delta_reference(c))
     other, st = tu.run_delta(gdn, c, stream=torch.cuda.Stream())
     assert st == 0 and torch.equal(other, o)
+
+
+@pytest.mark.parametrize("h_k,h_v,d", [HEADS[1], HEADS[3]])
+def test_a_long_path_beside_short_ones_changes_no_bit(gdn, h_k, h_v, d):
+    # paths of up to 16 nodes and longer ones are walked in different ways
+    short = tu.parents_of(20, "mixed", seed=3)
+    assert max(len(tu.path_of(short, u)) for u in range(20)) <= 16
+    both = short + [19] + list(range(20, 50))
+    c = tu.make_delta([both], h_k, h_v, d, seed=12)
+    o = check(gdn, c)
+    c.update(trees=[short], masks=c["masks"][:20].contiguous(), cu=tu.i32([0, 20]))
+    c.update({x: c[x][:20].contiguous() for x in ("q", "k", "v", "g", "beta")})
+    alone, st = tu.run_delta(gdn, c)
+    assert st == 0 and torch.equal(alone, o[:20])
+
+
+def test_rows_that_share_a_slot(gdn):
+    c = tu.make_delta(trees_of([12, 12, 40], "mixed"), 2, 4, 128, seed=13)
+    c["slot"][:] = c["slot"][0].clone()
+    check(gdn, c)
+
+
+def test_two_calls_at_once(gdn):
+    sizes = [30] * 40
+    cs = [tu.make_delta(trees_of(sizes, shape), 4, 8, 128, seed=14 + i) for i, shape in enumerate(("mixed", "forest"))]
+    wants = [tu.run_delta(gdn, c)[0] for c in cs]
+    outs, streams = [[torch.empty_like(w) for _ in range(8)] for w in wants], [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    for i in range(8):
+        for c, out, s in zip(cs, outs, streams):
+            gdn.gdn_tree_decode(c["q"], c["k"], c["v"], c["g"], c["beta"], c["state"], c["slot"], c["cu"], c["masks"],
+                                out[i], max_nodes=32, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for out, w in zip(outs, wants) for o in out)
+
+
+def test_states_far_apart(gdn):
+    # slots whose offsets pass 2^31 elements and 2^33 bytes
+    c = tu.make_delta(trees_of([9, 33], "mixed"), 16, 32, 128, seed=16)
+    want, _ = tu.run_delta(gdn, c)
+    n = (1 << 31) // (32 * 128 * 128) + 3
+    far = torch.empty((n, 32, 128, 128), device="cuda")
+    far[0], far[n - 1] = c["state"][int(c["slot"][0])], c["state"][int(c["slot"][1])]
+    c.update(state=far, slot=tu.i32([0, n - 1]))
+    o, st = tu.run_delta(gdn, c)
+    assert st == 0 and torch.equal(o, want)
+
+
+def test_a_state_off_its_boundary_is_refused(gdn):
+    c = tu.make_delta([[-1, 0]], 2, 2, 64, seed=17)
+    flat = torch.zeros(c["state"].numel() + 4, device="cuda")
+    c["state"] = flat[4:].view(c["state"].shape)
+    assert c["state"].data_ptr() % 32 == 16
+    with pytest.raises(RuntimeError):
+        tu.run_delta(gdn, c)
