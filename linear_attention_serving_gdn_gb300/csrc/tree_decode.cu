@@ -80,6 +80,9 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return y;
 }
 
+// First float of node u's row of k.k, with nodes 0 to u: 16-byte pieces, rows of 4, 4, 4, 4, 8, 8, ... floats.
+__host__ __device__ constexpr int key_row(int u) { return 4 * (u / 4 + 1) * (u - 2 * (u / 4)); }
+
 // Sizes for up to NT * 8 nodes.
 template <int D, int NT>
 struct TreeShape {
@@ -87,12 +90,13 @@ struct TreeShape {
     static constexpr int kBlocks = (NT <= 2 ? 768 : 512) / D;  // of an SM
     static constexpr int kNodes = 8 * NT;
     static constexpr int kCols = kNodes < 16 ? 16 : kNodes;  // whole steps of 16
+    static constexpr int kPer = kNodes / (D / 32);  // nodes whose paths a warp walks
     static constexpr int kGroups = D / 32;                   // of 32 state columns
     static constexpr int kAhead = NT <= 4 ? 2 : 1;           // groups of the state in registers
     static constexpr int kRowK = 2 * D;                      // bytes of a row of k or q
-    // Of k.k and q.k only what lies on or below the diagonal: k.k as a triangle, q.k by tiles of 16 (struct Row).
-    static constexpr int kQ = kCols * kRowK, kFQ = 2 * kQ, kFK = kFQ + (128 * (kCols / 16) * (kCols / 16 + 1) + 64 * (kCols / 16)) * 4, kWord = kFK + (kCols * (kCols + 1) / 2 * 4 + 15) / 16 * 16,
-                         kGate = kWord + 8 * kNodes;
+    // Of k.k and q.k only what lies on or below the diagonal: k.k as a triangle (key_row), q.k by tiles of 16 (struct Row).
+    static constexpr int kQ = kCols * kRowK, kFQ = 2 * kQ, kFK = kFQ + (128 * (kCols / 16) * (kCols / 16 + 1) + 64 * (kCols / 16)) * 4,
+                         kWord = kFK + key_row(kCols) * 4, kGate = kWord + 8 * kNodes;
     // v; of 64 nodes it is read where it is used, so that three blocks have room.
     static constexpr bool kStageV = NT <= 4;
     static constexpr int kRowV = 2 * D + 16, kV = (kGate + 3 * kNodes * 4 + 15) / 16 * 16;
@@ -105,8 +109,6 @@ template <int D>
 __device__ __forceinline__ int piece_at(int row, int piece) {
     return row * (2 * D) + ((piece ^ ((row & 1) << 2)) << 4);
 }
-
-__device__ __forceinline__ int triangle(int u) { return u * (u + 1) / 2; }
 
 // Node u's row of q.k: as many floats as there are nodes up to the end of its tile of 16, and 4 more (4-byte reads of 8 rows
 // x 4 lanes meet no bank twice).  Its row of C takes that place: the upper halves, then the rests.
@@ -155,10 +157,10 @@ __device__ __forceinline__ void products(const uint8_t *sk, const uint8_t *sq, i
                 *reinterpret_cast<float2 *>(fq + Row(u).at + w) = make_float2(acc[x][t][0], acc[x][t][1]);
                 *reinterpret_cast<float2 *>(fq + Row(u + 8).at + w) = make_float2(acc[x][t][2], acc[x][t][3]);
             } else {
-                if (w <= u) fk[triangle(u) + w] = acc[x][t][0];
-                if (w + 1 <= u) fk[triangle(u) + w + 1] = acc[x][t][1];
-                if (w <= u + 8) fk[triangle(u + 8) + w] = acc[x][t][2];
-                if (w + 1 <= u + 8) fk[triangle(u + 8) + w + 1] = acc[x][t][3];
+                if (w <= u) fk[key_row(u) + w] = acc[x][t][0];
+                if (w + 1 <= u) fk[key_row(u) + w + 1] = acc[x][t][1];
+                if (w <= u + 8) fk[key_row(u + 8) + w] = acc[x][t][2];
+                if (w + 1 <= u + 8) fk[key_row(u + 8) + w + 1] = acc[x][t][3];
             }
         }
 }
@@ -198,7 +200,7 @@ __device__ __forceinline__ float walk_short(uint64_t path, int most, float *row,
     for (int i = 0; i < kMost; ++i) {
         if (i >= most) break;
         const float a = ab.x, c = ab.y * g[i], ac = -a * c;
-        const float *const kk = fk + triangle(x[i]);  // (places behind the last: any number)
+        const float *const kk = fk + key_row(x[i]);  // (places behind the last: any number)
         if (i + 1 < kMost && i + 1 < most) ab = gates[x[i + 1 < kMost ? i + 1 : i]];
 #pragma unroll
         for (int j = i + 1; j < kMost; ++j) {
@@ -214,57 +216,72 @@ __device__ __forceinline__ float walk_short(uint64_t path, int most, float *row,
     return decay;
 }
 
-// A path of any length, on `row` itself: a quad takes the nodes above in turn, and what one lane has written is another's c
-// four nodes on.  The same operations, and so the same bits.
+// Paths of any length, of a pass of 16 nodes or the warp's, each with 32 / pass lanes: node by node from the last to the
+// first, so that k.k is read by whole lines for all nodes whose path the node is on.  A node's lanes hold its g_x in turns
+// of four neighbouring nodes x, those behind the current ones shifted down.  The same operations, and so the same bits.
+// (A quad a node, each with its own place and its numbers in shared memory: a chain of 64 nodes 71 us, 64 of them with 32
+// heads 248; so 19 and 100.)
+constexpr int pass_of(int per) { return per < 16 ? per : 16; }
+
 template <int D, int NT>
-__device__ __forceinline__ float walk_long(const uint64_t path, float *row, int cols, const float *fk, const float2 *gates, int sub) {
+__device__ __forceinline__ void walk_long(int first, int m, const uint64_t *word, float *fq, const float *fk, const float2 *gates,
+                                          float *gamma, int lane) {
     using Sh = TreeShape<D, NT>;
-    const uint32_t quad = 0xfu << (threadIdx.x & 28);
+    constexpr int kSplit = 32 / pass_of(Sh::kPer), kSteps = 4 * kSplit, kTurns = Sh::kNodes / kSteps;
+    const int u = first + lane / kSplit, sub = lane % kSplit;
+    const Row at(u);
+    float *const row = fq + at.at;
+    const uint64_t path = u < m ? word[u] : 0;
+    const uint64_t all = static_cast<uint64_t>(__reduce_or_sync(0xffffffffu, static_cast<uint32_t>(path >> 32))) << 32 |
+                         __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(path));
+    int b = all ? (63 - __clzll(static_cast<long long>(all))) / kSteps : -1;
+    float g[kTurns][4];  // of nodes kSteps (b - i) + 4 sub and the next three
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+        const int x = (b - i) * kSteps + 4 * sub;
+        const float4 v = i <= b && x < at.cols ? *reinterpret_cast<const float4 *>(row + x) : make_float4(0.f, 0.f, 0.f, 0.f);
+        g[i][0] = v.x, g[i][1] = v.y, g[i][2] = v.z, g[i][3] = v.w;
+    }
+    asm volatile("" ::: "memory");  // (the row is read as floats, then written as other types)
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < Sh::kCols / 4; i += kSplit)
+        if (4 * (i + sub) < at.cols) reinterpret_cast<uint4 *>(row)[i + sub] = make_uint4(0, 0, 0, 0);
+    __syncwarp();
+    asm volatile("" ::: "memory");
+    uint16_t *const hi = reinterpret_cast<uint16_t *>(row), *const lo = hi + at.cols;
     float decay = 1.f;
 #pragma unroll 1
-    for (uint64_t left = path; left;) {
-        const int w = 63 - __clzll(static_cast<long long>(left));
-        left ^= 1ull << w;
-        const float2 ab = gates[w];
-        const float a = ab.x, c = ab.y * row[w], ac = -a * c;
-        __syncwarp(quad);
-        if (sub == 0) row[w] = c;
-        decay *= a;
-        const float *const kk = fk + triangle(w);
-        uint64_t mine = left & (0x1111111111111111ull << sub);
-#pragma unroll 1
-        while (mine) {
-            int x[4];
-            float y[4], z[4];
+    for (; b >= 0; --b) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {  // (past the last one: it again)
-                x[i] = mine ? __ffsll(static_cast<long long>(mine)) - 1 : x[i > 0 ? i - 1 : 0];
-                mine &= mine - 1;
-                y[i] = row[x[i]];
-                z[i] = kk[x[i]];
+        for (int j = kSteps - 1; j >= 0; --j) {
+            const int w = b * kSteps + j;
+            if (!(all >> w & 1)) continue;
+            const float2 ab = gates[w];
+            const float a = ab.x, c = ab.y * __shfl_sync(0xffffffffu, g[0][j % 4], (lane & -kSplit) | j / 4), ac = -a * c;
+            if (!(path >> w & 1)) continue;
+            if (sub == j / 4) {
+                hi[w] = static_cast<uint16_t>(__float_as_uint(c) >> 16);
+                lo[w] = float_to_bf16_bits(c - __uint_as_float(__float_as_uint(c) & 0xffff0000u));
             }
+            decay *= a;
+            const float *const kk = fk + key_row(w) + b * kSteps + 4 * sub;  // (of nodes from w on: any number)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) row[x[i]] = fmaf(ac, z[i], a * y[i]);
+            for (int i = 0; i < kTurns; ++i) {
+                if (i > b) break;
+                const float4 z = *reinterpret_cast<const float4 *>(kk - i * kSteps);
+                g[i][0] = fmaf(ac, z.x, a * g[i][0]);
+                g[i][1] = fmaf(ac, z.y, a * g[i][1]);
+                g[i][2] = fmaf(ac, z.z, a * g[i][2]);
+                g[i][3] = fmaf(ac, z.w, a * g[i][3]);
+            }
         }
-        __syncwarp(quad);
-    }
-    // The row to its sums of two bf16: read by the quad, then written.
-    float2 c[Sh::kCols / 8];
 #pragma unroll
-    for (int i = 0; i < Sh::kCols / 8; ++i) {
-        const int w = 2 * (sub + 4 * i);
-        c[i] = w < cols ? *reinterpret_cast<const float2 *>(row + w) : make_float2(0.f, 0.f);
-        if (!(path >> w & 1)) c[i].x = 0.f;
-        if (!(path >> w & 2)) c[i].y = 0.f;
-    }
-    __syncwarp(quad);
+        for (int i = 0; i + 1 < kTurns; ++i)
 #pragma unroll
-    for (int i = 0; i < Sh::kCols / 8; ++i) {
-        if (2 * (sub + 4 * i) >= cols) continue;
-        uint32_t *const to = reinterpret_cast<uint32_t *>(row) + sub + 4 * i;
-        split2(c[i].x, c[i].y, to, to + cols / 2);
+            for (int j = 0; j < 4; ++j) g[i][j] = g[i + 1][j];
     }
-    return decay;
+    if (sub == 0) gamma[u] = decay;
 }
 
 template <int D, int NT>
@@ -358,7 +375,7 @@ __global__ void __launch_bounds__(TreeShape<D, NT>::kThreads, TreeShape<D, NT>::
         asm volatile("cp.async.wait_group 1;" ::: "memory");
     else
         asm volatile("cp.async.wait_group 0;" ::: "memory");
-    const bool deep = __syncthreads_or(__popcll(path) > kShortPath);
+    __syncthreads();
 
     // 2. k.k and q.k of nodes and those before them.
     if (NT <= 2) {
@@ -376,22 +393,19 @@ __global__ void __launch_bounds__(TreeShape<D, NT>::kThreads, TreeShape<D, NT>::
     if (Sh::kStageV) asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
 
-    // 3. C and G.
-    if (!deep) {
-        // (the nodes dealt out over the warps: reads of several rows' places meet in the same banks)
-        constexpr int kPer = Sh::kNodes / (D / 32);
-        const int u = warp * kPer + lane;
-        const bool mine = lane < kPer && u < m;
+    // 3. C and G, the nodes dealt out over the warps.
+    {
+        const int first = warp * Sh::kPer, u = first + lane;
+        const bool mine = lane < Sh::kPer && u < m;
         path = mine ? word[u] : 0;
         const int most = __reduce_max_sync(0xffffffffu, __popcll(path));
-        float g = 0.f;
-        if (mine) g = walk_short<D, NT>(path, most, fq + Row(u).at, Row(u).cols, fk, gates);
-        if (lane < kPer) gamma[u] = g;
-    } else {
+        if (NT <= 2 || most <= kShortPath) {
+            float g = 0.f;
+            if (mine) g = walk_short<D, NT>(path, most, fq + Row(u).at, Row(u).cols, fk, gates);
+            if (lane < Sh::kPer) gamma[u] = g;
+        } else if constexpr (NT > 2) {
 #pragma unroll 1
-        for (int u = tid >> 2; u < Sh::kNodes; u += D / 4) {  // (whole quads: one node's lanes stay together)
-            const float g = u < m ? walk_long<D, NT>(word[u], fq + Row(u).at, Row(u).cols, fk, gates, c) : 0.f;
-            if (c == 0) gamma[u] = g;
+            for (int i = 0; i < Sh::kPer; i += pass_of(Sh::kPer)) walk_long<D, NT>(first + i, m, word, fq, fk, gates, gamma, lane);
         }
     }
     __syncthreads();
