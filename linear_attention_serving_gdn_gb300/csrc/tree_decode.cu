@@ -169,14 +169,15 @@ __device__ __forceinline__ void products(const uint8_t *sk, const uint8_t *sq, i
 // b_w g_w, and p' = a_w (p - c k_w) changes the others by k_w.k_x.  C[u] takes the row's place, as sums of two bf16, zeros
 // off the path.  Gives the product of the decays.
 //
-// Of up to kShortPath nodes the walk is held in registers, place by place: nothing waits but a step's c for the one
-// before.  (A quad a node with its numbers in shared memory took 4000 cycles for 64 nodes, this takes 1000.)
-constexpr int kShortPath = 16;
+// Of up to 8 nodes (with room for no more than 16: of all) the walk is held in registers, place by place, a thread a node.
+// (41 requests of 15 to 26 nodes in a chain, 32 heads: with up to 16 nodes so 39 us, 10 32.8, 8 and 6 31.9; trees 29.7, and
+// 32 with none so.)
+constexpr int short_path(int nt) { return nt == 2 ? 16 : 8; }
 
 template <int D, int NT>
 __device__ __forceinline__ float walk_short(uint64_t path, int most, float *row, int cols, const float *fk, const float2 *gates) {
     using Sh = TreeShape<D, NT>;
-    constexpr int kMost = 8 * NT < kShortPath ? 8 * NT : kShortPath;
+    constexpr int kMost = short_path(NT);
     const int steps = __popcll(path);
     int x[kMost];
     float g[kMost];
@@ -249,32 +250,41 @@ __device__ __forceinline__ void walk_long(int first, int m, const uint64_t *word
         if (4 * (i + sub) < at.cols) reinterpret_cast<uint4 *>(row)[i + sub] = make_uint4(0, 0, 0, 0);
     __syncwarp();
     asm volatile("" ::: "memory");
-    uint16_t *const hi = reinterpret_cast<uint16_t *>(row), *const lo = hi + at.cols;
     float decay = 1.f;
 #pragma unroll 1
     for (; b >= 0; --b) {
+        float mine[4] = {0.f, 0.f, 0.f, 0.f};  // c of the lane's own four nodes
 #pragma unroll
         for (int j = kSteps - 1; j >= 0; --j) {
             const int w = b * kSteps + j;
             if (!(all >> w & 1)) continue;
             const float2 ab = gates[w];
+            const float *const kk = fk + key_row(w) + b * kSteps + 4 * sub;  // (of nodes from w on: any number)
+            constexpr int kFirst = kTurns < 4 ? kTurns : 4;  // lines asked for before c is there
+            float4 z[kFirst];
+#pragma unroll
+            for (int i = 0; i < kFirst; ++i) z[i] = *reinterpret_cast<const float4 *>(kk - (i <= b ? i : 0) * kSteps);
             const float a = ab.x, c = ab.y * __shfl_sync(0xffffffffu, g[0][j % 4], (lane & -kSplit) | j / 4), ac = -a * c;
             if (!(path >> w & 1)) continue;
-            if (sub == j / 4) {
-                hi[w] = static_cast<uint16_t>(__float_as_uint(c) >> 16);
-                lo[w] = float_to_bf16_bits(c - __uint_as_float(__float_as_uint(c) & 0xffff0000u));
-            }
+            if (sub == j / 4) mine[j % 4] = c;
             decay *= a;
-            const float *const kk = fk + key_row(w) + b * kSteps + 4 * sub;  // (of nodes from w on: any number)
 #pragma unroll
             for (int i = 0; i < kTurns; ++i) {
-                if (i > b) break;
-                const float4 z = *reinterpret_cast<const float4 *>(kk - i * kSteps);
-                g[i][0] = fmaf(ac, z.x, a * g[i][0]);
-                g[i][1] = fmaf(ac, z.y, a * g[i][1]);
-                g[i][2] = fmaf(ac, z.z, a * g[i][2]);
-                g[i][3] = fmaf(ac, z.w, a * g[i][3]);
+                if (i >= kFirst && i % 2 == 0 && i > b) break;
+                const float4 y = i < kFirst ? z[i < kFirst ? i : 0] : *reinterpret_cast<const float4 *>(kk - (i <= b ? i : 0) * kSteps);
+                g[i][0] = fmaf(ac, y.x, a * g[i][0]);
+                g[i][1] = fmaf(ac, y.y, a * g[i][1]);
+                g[i][2] = fmaf(ac, y.z, a * g[i][2]);
+                g[i][3] = fmaf(ac, y.w, a * g[i][3]);
             }
+        }
+        const int x = b * kSteps + 4 * sub;
+        if (x < at.cols) {
+            uint2 h, l;
+            split2(mine[0], mine[1], &h.x, &l.x);
+            split2(mine[2], mine[3], &h.y, &l.y);
+            *reinterpret_cast<uint2 *>(row + x / 2) = h;
+            *reinterpret_cast<uint2 *>(row + x / 2 + at.cols / 2) = l;
         }
 #pragma unroll
         for (int i = 0; i + 1 < kTurns; ++i)
@@ -399,7 +409,7 @@ __global__ void __launch_bounds__(TreeShape<D, NT>::kThreads, TreeShape<D, NT>::
         const bool mine = lane < Sh::kPer && u < m;
         path = mine ? word[u] : 0;
         const int most = __reduce_max_sync(0xffffffffu, __popcll(path));
-        if (NT <= 2 || most <= kShortPath) {
+        if (NT <= 2 || most <= short_path(NT)) {
             float g = 0.f;
             if (mine) g = walk_short<D, NT>(path, most, fq + Row(u).at, Row(u).cols, fk, gates);
             if (lane < Sh::kPer) gamma[u] = g;
