@@ -14,17 +14,39 @@
 //
 // One block per (request, value head), a warp per 32 rows of S^T (values), 16
 // at a time.
-//   1. Each warp asks for its first rows of the state; q, k to shared memory.
-//   2. K K^T and Q K^T on the tensor cores (mma.sync, bf16: exact products).
-//   3. A thread per node walks its path, in registers: C and G.  (Paths of more
-//      than 16 nodes by four lanes each, in shared memory.)
+//   1. k, q (and v of up to 32 nodes) to shared memory; each warp asks for its
+//      first rows of the state.
+//   2. K K^T and Q K^T on the tensor cores (mma.sync, bf16: exact products),
+//      what lies on or below the diagonal.
+//   3. The walks, in registers: C and G.  Short paths place by place, a thread
+//      a node; longer ones node by node, several lanes a node.
 //   4. S^T [K; Q] with the state's rows as the A operand, each value as the sum
 //      of two bf16 (2^-15 of it is left at most), straight from registers: the
 //      state is read once and never staged.
 //   5. R = v - G S^T k in the accumulator's layout, which is the A layout of
 //      the last product: O^T += R^T C^T, both as sums of two bf16.
-// mma.sync and not tcgen05: with up to 32 nodes the products take less time
-// than the state's 64 KB, and the state goes through no shared memory.
+//
+// What bounds it.  Up to 16 nodes: the state's 64 KB per head.  256 requests of
+// 4 to 12 nodes, 16 heads: 303 MB in 55.5 us, 5.5 TB/s, 0.80 of the copy peak,
+// the tensor pipe 29 % busy; what is missing are the loads that a block does not
+// have in flight while it walks.  With 33 to 64 nodes (64 requests, 32 heads:
+// 76 us) a block's phases: 9000 cycles until k and q are there, 4000 for their
+// products, 3000 for the walks, 10000 for each slab's product with the state and
+// 2500 for the rest of it, four blocks of an SM in turn: the tensor pipe is 46 %
+// busy (712 products a warp, 2 cycles each of the SM, are 36 us), the shared
+// memory's pipe 55 %, and neither is the bound alone.  One tree: 5.2 us, the
+// chain of these phases.
+//
+// Why mma.sync and not tcgen05.  Up to 16 nodes the products hide behind the
+// state.  A tcgen05 product takes the state as two bf16 operands out of shared
+// memory (64 KB a block) or TMEM: two blocks per SM instead of four to six, and
+// one more trip of 64 KB, for a pipe that is not the bound; and with one
+// arithmetic for every size a request's bits do not depend on max_nodes.
+//
+// Tried and worse (256 small trees / 64 large ones, us, at 61 / 91): blocks that
+// take several (request, head) in turn 65 / 98, the state of the next block to
+// L2 65 / 91, the block's own state to L2 for up to 16 nodes 63, k and q by 8-byte
+// pieces 61 / 97.
 //
 // A node's bits depend on its own path and the state alone.  A value that is
 // not finite stays with the nodes whose path it is on: it is left out of the
@@ -59,7 +81,7 @@ __device__ __forceinline__ void copy16(uint32_t to, const void *from, bool some)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(some ? 16 : 0) : "memory");
 }
 
-// 8 values, read once: whole sectors.
+// 8 values, read once: whole sectors (in 16-byte pieces: 64 large trees 84 us, so 76).
 struct Eight {
     float x[8];
 };
@@ -87,17 +109,20 @@ __host__ __device__ constexpr int key_row(int u) { return 4 * (u / 4 + 1) * (u -
 template <int D, int NT>
 struct TreeShape {
     static constexpr int kThreads = D;                         // a warp per 32 values
-    static constexpr int kBlocks = (NT <= 2 ? 768 : 512) / D;  // of an SM
+    // Blocks of an SM (D = 128), as many as registers allow without spilling to matter: six for up to 16 nodes (256 small
+    // trees 57 us, with four 61), else four (of up to 32 nodes, 256 trees of 17 to 20 / one of 24: 83 / 7.0 us, with five
+    // 80 / 8.0, with six 96 / 9.9).
+    static constexpr int kBlocks = (NT <= 2 ? 768 : 512) / D;
     static constexpr int kNodes = 8 * NT;
     static constexpr int kCols = kNodes < 16 ? 16 : kNodes;  // whole steps of 16
     static constexpr int kPer = kNodes / (D / 32);  // nodes whose paths a warp walks
     static constexpr int kGroups = D / 32;                   // of 32 state columns
-    static constexpr int kAhead = NT <= 4 ? 2 : 1;           // groups of the state in registers
+    static constexpr int kAhead = NT <= 4 ? 2 : 1;           // groups of the state in registers (of 64 nodes the sums take the rest)
     static constexpr int kRowK = 2 * D;                      // bytes of a row of k or q
     // Of k.k and q.k only what lies on or below the diagonal: k.k as a triangle (key_row), q.k by tiles of 16 (struct Row).
     static constexpr int kQ = kCols * kRowK, kFQ = 2 * kQ, kFK = kFQ + (128 * (kCols / 16) * (kCols / 16 + 1) + 64 * (kCols / 16)) * 4,
                          kWord = kFK + key_row(kCols) * 4, kGate = kWord + 8 * kNodes;
-    // v; of 64 nodes it is read where it is used, so that three blocks have room.
+    // v; of 64 nodes it is read where it is used, so that four blocks have room.
     static constexpr bool kStageV = NT <= 4;
     static constexpr int kRowV = 2 * D + 16, kV = (kGate + 3 * kNodes * 4 + 15) / 16 * 16;
     static constexpr int kSmem = kV + (kStageV ? kNodes * kRowV : 0);
@@ -372,7 +397,7 @@ __global__ void __launch_bounds__(TreeShape<D, NT>::kThreads, TreeShape<D, NT>::
     }
 #pragma unroll
     for (int g = 0; g < Sh::kAhead; ++g) ask(g);
-    if (Sh::kAhead == 1) {  // the registers hold little of the state: the rest waits in L2
+    if (Sh::kAhead == 1) {  // the registers hold little of the state: the rest waits in L2 (64 large trees 91 -> 84 us)
         const float *p = a.state + (static_cast<int64_t>(slot) * a.h_v + head) * (D * D) + tid * 64;
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i * (64 * Sh::kThreads)));
