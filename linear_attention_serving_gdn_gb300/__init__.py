@@ -708,10 +708,10 @@ def gdn_paged_attention(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, o
            "gdn_paged_attention")
 
 
-def _dense(t, name, dtype, ndim):
-    if t.__class__ is _Tensor and t.dtype is dtype and t.is_cuda and t.dim() == ndim and t.is_contiguous():
-        return t.data_ptr()
-    return _dev(t, name, dtype, ndim).data_ptr()
+# The calls on trees and gdn_rotary are made for steps of a few microseconds, so the checks of a good call are one
+# expression for all of its tensors; where it does not hold, the slow way names what is wrong.
+_i64, _bf16, _f32, _one = torch.int64, torch.bfloat16, torch.float32, (1,)
+_dims_refs = {}
 
 
 def _words(t, name):
@@ -725,13 +725,20 @@ def gdn_tree_maps(parents, cu_seqlens, kv_lens, masks, positions, dev_status=Non
     tree from their ``parents`` (see gdn.h); ``cu_seqlens`` and ``kv_lens`` as
     ``gdn_paged_maps`` gives them."""
     lib = _lib or load_library()
-    par, cu, kv = _i32_vec(parents, "parents"), _i32_vec(cu_seqlens, "cu_seqlens"), _i32_vec(kv_lens, "kv_lens")
-    words, pos = _words(masks, "masks"), _i32_vec(positions, "positions")
+    if not (parents.__class__ is cu_seqlens.__class__ is kv_lens.__class__ is masks.__class__ is positions.__class__ is _Tensor
+            and parents.dtype is cu_seqlens.dtype is kv_lens.dtype is positions.dtype is _i32 and masks.dtype is _i64
+            and parents.is_cuda and cu_seqlens.is_cuda and kv_lens.is_cuda and masks.is_cuda and positions.is_cuda
+            and parents.stride() == cu_seqlens.stride() == kv_lens.stride() == masks.stride() == positions.stride() == _one):
+        _i32_vec(parents, "parents"), _i32_vec(cu_seqlens, "cu_seqlens"), _i32_vec(kv_lens, "kv_lens")
+        _words(masks, "masks"), _i32_vec(positions, "positions")
     n, T = kv_lens.numel(), parents.numel()
     if not (cu_seqlens.numel() == n + 1 and masks.numel() == T and positions.numel() == T):
         raise ValueError("inconsistent tree-maps shapes")
-    _check(lib.gdn_tree_maps(n, T, par, cu, kv, words, pos, _i32_word(dev_status, "dev_status"), _stream(stream)),
-           "gdn_tree_maps")
+    status = lib.gdn_tree_maps(n, T, parents.data_ptr(), cu_seqlens.data_ptr(), kv_lens.data_ptr(), masks.data_ptr(),
+                               positions.data_ptr(), None if dev_status is None else _i32_word(dev_status, "dev_status"),
+                               _raw_stream(_current_device()) if stream is None and _raw_stream else _stream(stream))
+    if status:
+        raise GdnError(status, "gdn_tree_maps")
 
 
 def gdn_tree_attention(q, k_cache, v_cache, block_table, cu_seqlens, kv_lens, masks, o, scale=None,
@@ -766,41 +773,69 @@ def gdn_tree_decode(q, k, v, g, beta, state, src_slot, cu_seqlens, masks, o, max
     state of its slot, which stays as it is (see gdn.h).  ``max_nodes`` bounds
     a row's nodes."""
     lib = _lib or load_library()
-    bf, f32 = torch.bfloat16, torch.float32
-    ptrs = (_dense(q, "q", bf, 3), _dense(k, "k", bf, 3), _dense(v, "v", bf, 3), _dense(g, "g", f32, 2),
-            _dense(beta, "beta", f32, 2), _dense(state, "state", f32, 4))
-    out = _dense(o, "o", bf, 3)
-    slots, cu, words = _i32_vec(src_slot, "src_slot"), _i32_vec(cu_seqlens, "cu_seqlens"), _words(masks, "masks")
+    bf, f32 = _bf16, _f32
+    if not (q.__class__ is k.__class__ is v.__class__ is o.__class__ is g.__class__ is beta.__class__ is state.__class__
+            is src_slot.__class__ is cu_seqlens.__class__ is masks.__class__ is _Tensor
+            and q.dtype is k.dtype is v.dtype is o.dtype is bf and g.dtype is beta.dtype is state.dtype is f32
+            and src_slot.dtype is cu_seqlens.dtype is _i32 and masks.dtype is _i64
+            and q.is_cuda and k.is_cuda and v.is_cuda and o.is_cuda and g.is_cuda and beta.is_cuda and state.is_cuda
+            and src_slot.is_cuda and cu_seqlens.is_cuda and masks.is_cuda
+            and q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and o.is_contiguous() and g.is_contiguous()
+            and beta.is_contiguous() and state.is_contiguous()
+            and src_slot.stride() == cu_seqlens.stride() == masks.stride() == _one):
+        for t, name, dtype, ndim in ((q, "q", bf, 3), (k, "k", bf, 3), (v, "v", bf, 3), (g, "g", f32, 2), (beta, "beta", f32, 2),
+                                     (state, "state", f32, 4), (o, "o", bf, 3), (src_slot, "src_slot", _i32, 1),
+                                     (cu_seqlens, "cu_seqlens", _i32, 1), (masks, "masks", _i64, 1)):
+            _dev(t, name, dtype, ndim)
     n = src_slot.numel()
-    T, h_k, d = qs = q.shape
-    _, h_v, d_v = vs = v.shape
-    slots_n, *row = state.shape
-    if not (k.shape == qs and vs[0] == T and o.shape == vs and g.shape == (T, h_v) and beta.shape == (T, h_v)
-            and cu_seqlens.numel() == n + 1 and masks.numel() == T and row == [h_v, d_v, d]):
+    qs, vs, ss = q.shape, v.shape, state.shape
+    if not (len(qs) == len(vs) == 3 and len(ss) == 4):
+        _dev(q, "q", bf, 3), _dev(v, "v", bf, 3), _dev(state, "state", f32, 4)
+    T, h_k, d = qs
+    _, h_v, d_v = vs
+    slots_n = ss[0]
+    gates = (T, h_v)
+    if not (k.shape == qs and vs[0] == T and o.shape == vs and g.shape == gates and beta.shape == gates
+            and cu_seqlens.numel() == n + 1 and masks.numel() == T and ss == (slots_n, h_v, d_v, d)):
         raise ValueError("inconsistent tree-decode shapes")
     key = (h_k, h_v, d, d_v, float(scale))
-    dims = _dims_cache.get(key) or _dims(q, v, scale)
-    _check(lib.gdn_tree_decode(ctypes.byref(dims), n, max_nodes, T, cu, words, *ptrs, slots_n, slots, out,
-                               _i32_word(dev_status, "dev_status"), _stream(stream)), "gdn_tree_decode")
+    dims = _dims_refs.get(key)
+    if dims is None:
+        dims = _dims_refs[key] = ctypes.byref(_dims(q, v, scale))
+    status = lib.gdn_tree_decode(dims, n, max_nodes, T, cu_seqlens.data_ptr(), masks.data_ptr(), q.data_ptr(), k.data_ptr(),
+                                 v.data_ptr(), g.data_ptr(), beta.data_ptr(), state.data_ptr(), slots_n, src_slot.data_ptr(),
+                                 o.data_ptr(), None if dev_status is None else _i32_word(dev_status, "dev_status"),
+                                 _raw_stream(_current_device()) if stream is None and _raw_stream else _stream(stream))
+    if status:
+        raise GdnError(status, "gdn_tree_decode")
 
 
 _ROTARY_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
 _pack_side = struct.Struct("@PPiqqqq").pack  # RotarySide's layout
 
 
-def _rotary_side(x, out, name, dtype, shape):
-    """The C description of one side (its bytes); ``shape``: tokens and head size."""
-    xs = _strided(x, name, dtype, 3)
-    T, h, d = size = x.shape
-    if T != shape[0] or d != shape[1]:
+def _rotary_side(x, out, name, dtype, T, d):
+    """The C description of one side (its bytes)."""
+    if x.__class__ is _Tensor and x.is_cuda and x.dtype is dtype:
+        xt, xh, one = x.stride() if x.dim() == 3 else (0, 0, 0)
+    else:
+        one = 0
+    if one != 1:
+        xt, xh, _ = _strided(x, name, dtype, 3)
+    tokens, h, size = shape = x.shape
+    if tokens != T or size != d:
         raise ValueError("inconsistent rotary shapes")
+    p = x.data_ptr()
     if out is None:
-        p = x.data_ptr()
-        return _pack_side(p, p, h, xs[0], xs[1], xs[0], xs[1])
-    to = _strided(out, f"{name}_out", dtype, 3)
-    if out.shape != size:
+        return _pack_side(p, p, h, xt, xh, xt, xh)
+    if out.__class__ is _Tensor and out.is_cuda and out.dtype is dtype and out.shape == shape:
+        ot, oh, one = out.stride()
+        if one == 1:
+            return _pack_side(p, out.data_ptr(), h, xt, xh, ot, oh)
+    ot, oh, _ = _strided(out, f"{name}_out", dtype, 3)
+    if out.shape != shape:
         raise ValueError("inconsistent rotary shapes")
-    return _pack_side(x.data_ptr(), out.data_ptr(), h, xs[0], xs[1], to[0], to[1])
+    return _pack_side(p, out.data_ptr(), h, xt, xh, ot, oh)
 
 
 def gdn_rotary(q, k, positions, frequencies, q_out=None, k_out=None, interleaved: bool = False,
@@ -816,12 +851,16 @@ def gdn_rotary(q, k, positions, frequencies, q_out=None, k_out=None, interleaved
     code = _PAGED_DTYPES.get(dtype)
     if code is None:
         raise TypeError(f"q must be bfloat16 or float16, got {dtype}")
-    pos, freq = _i32_vec(positions, "positions"), _words(frequencies, "frequencies")
-    T, d = shape = positions.numel(), q.shape[-1]
-    q_side = _rotary_side(q, q_out, "q", dtype, shape)
-    k_side = None if k is None else _rotary_side(k, k_out, "k", dtype, shape)
-    _check(lib.gdn_rotary(code, T, d, 2 * frequencies.numel(), bool(interleaved), magnitude, pos, freq, q_side, k_side,
-                          _stream(stream)), "gdn_rotary")
+    if not (positions.__class__ is frequencies.__class__ is _Tensor and positions.dtype is _i32 and frequencies.dtype is _i64
+            and positions.is_cuda and frequencies.is_cuda and positions.stride() == frequencies.stride() == _one):
+        _i32_vec(positions, "positions"), _words(frequencies, "frequencies")
+    T, d = positions.numel(), q.shape[-1]
+    status = lib.gdn_rotary(code, T, d, 2 * frequencies.numel(), 1 if interleaved else 0, magnitude, positions.data_ptr(),
+                            frequencies.data_ptr(), _rotary_side(q, q_out, "q", dtype, T, d),
+                            None if k is None else _rotary_side(k, k_out, "k", dtype, T, d),
+                            _raw_stream(_current_device()) if stream is None and _raw_stream else _stream(stream))
+    if status:
+        raise GdnError(status, "gdn_rotary")
 
 
 # ---------------------------------------------------------------------------
