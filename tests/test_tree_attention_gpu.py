@@ -226,3 +226,20 @@ def test_requests_that_share_pages(gdn):
     c, masks = case([(500, 12), (500, 40)], HEADS[0], page=64, seed=23)
     c["table"][1, :7] = c["table"][0, :7]
     check(gdn, c, masks)
+
+
+@pytest.mark.parametrize("heads", HEADS)
+def test_a_part_of_which_a_node_sees_nothing(gdn, heads):
+    # contexts that end where a part of the keys ends, and nodes that see no node: their last part is empty
+    lens = [(ctx + m, m) for ctx, m in ((2048, 20), (2048, 64), (1920, 1), (1920, 5), (384, 3), (0, 7))]
+    c, masks = case(lens, heads, page=64, seed=24)
+    masks[::2] = 0
+    want = check(gdn, c, masks)
+    # and what they do not see has no part in it
+    for r, (kv, m) in enumerate(lens):
+        for j in range(kv - m, kv):
+            c["k"][c["table"][r, j // 64].long(), j % 64] = NAN
+            c["v"][c["table"][r, j // 64].long(), j % 64] = INF
+    o, st = tu.run_tree_attention(gdn, c, masks)
+    blind = masks == 0
+    assert st == 0 and torch.equal(o[blind], want[blind])
