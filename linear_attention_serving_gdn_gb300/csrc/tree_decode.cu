@@ -109,15 +109,14 @@ __host__ __device__ constexpr int key_row(int u) { return 4 * (u / 4 + 1) * (u -
 template <int D, int NT>
 struct TreeShape {
     static constexpr int kThreads = D;                         // a warp per 32 values
-    // Blocks of an SM (D = 128), as many as registers allow without spilling to matter: six for up to 16 nodes (256 small
-    // trees 57 us, with four 61), else four (of up to 32 nodes, 256 trees of 17 to 20 / one of 24: 83 / 7.0 us, with five
-    // 80 / 8.0, with six 96 / 9.9).
-    static constexpr int kBlocks = (NT <= 2 ? 768 : 512) / D;
+    // Blocks of an SM (D = 128), and groups of the state that a lane holds in registers, by what these allow without spilling
+    // to matter: up to 16 nodes six and two (256 small trees 57 us; four and two 61); up to 32 five and one (256 trees of 17 to
+    // 20 / one of 24: 75.5 / 6.9 us; four and two 83 / 6.9; five and two 80 / 8.0; six and one 81 / 8.2); 64 four and one.
+    static constexpr int kBlocks = (NT <= 2 ? 768 : NT <= 4 ? 640 : 512) / D, kAhead = NT <= 2 ? 2 : 1;
     static constexpr int kNodes = 8 * NT;
     static constexpr int kCols = kNodes < 16 ? 16 : kNodes;  // whole steps of 16
     static constexpr int kPer = kNodes / (D / 32);  // nodes whose paths a warp walks
     static constexpr int kGroups = D / 32;                   // of 32 state columns
-    static constexpr int kAhead = NT <= 4 ? 2 : 1;           // groups of the state in registers (of 64 nodes the sums take the rest)
     static constexpr int kRowK = 2 * D;                      // bytes of a row of k or q
     // Of k.k and q.k only what lies on or below the diagonal: k.k as a triangle (key_row), q.k by tiles of 16 (struct Row).
     static constexpr int kQ = kCols * kRowK, kFQ = 2 * kQ, kFK = kFQ + (128 * (kCols / 16) * (kCols / 16 + 1) + 64 * (kCols / 16)) * 4,
@@ -397,7 +396,7 @@ __global__ void __launch_bounds__(TreeShape<D, NT>::kThreads, TreeShape<D, NT>::
     }
 #pragma unroll
     for (int g = 0; g < Sh::kAhead; ++g) ask(g);
-    if (Sh::kAhead == 1) {  // the registers hold little of the state: the rest waits in L2 (64 large trees 91 -> 84 us)
+    if (NT > 4) {  // the walks are long: the rest of the state waits in L2 (64 large trees 91 -> 84 us; up to 32 nodes no change)
         const float *p = a.state + (static_cast<int64_t>(slot) * a.h_v + head) * (D * D) + tid * 64;
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i * (64 * Sh::kThreads)));
