@@ -110,12 +110,15 @@ template <int D, int NT>
 struct TreeShape {
     static constexpr int kThreads = D;                         // a warp per 32 values
     // Blocks of an SM (D = 128), and groups of the state that a lane holds in registers, by what these allow without spilling
-    // to matter: up to 16 nodes six and two (256 small trees 57 us; four and two 61); up to 32 five and one (256 trees of 17 to
-    // 20 / one of 24: 75.5 / 6.9 us; four and two 83 / 6.9; five and two 80 / 8.0; six and one 81 / 8.2); 64 four and one.
-    static constexpr int kBlocks = (NT <= 2 ? 768 : NT <= 4 ? 640 : 512) / D, kAhead = NT <= 2 ? 2 : 1;
+    // to matter.  Up to 8 nodes six and two (256 trees / one 49.0 / 4.8 us, seven and two 48.6 / 4.9, six and one - / 5.1); up
+    // to 16 seven and one (256 trees of 12 to 16 / one of 16: 54.7 / 5.5; six and two 57.3 / 5.6, eight and one 58.0 / 6.1); up
+    // to 32 five and one (256 trees of 17 to 20 / one of 24: 75.5 / 6.9; four and two 83 / 6.9, five and two 80 / 8.0, six and
+    // one 81 / 8.2); 64 four and one.
+    static constexpr int kBlocks = (NT == 1 ? 768 : NT == 2 ? 896 : NT == 4 ? 640 : 512) / D, kAhead = NT == 1 ? 2 : 1;
     static constexpr int kNodes = 8 * NT;
     static constexpr int kCols = kNodes < 16 ? 16 : kNodes;  // whole steps of 16
-    static constexpr int kPer = kNodes / (D / 32);  // nodes whose paths a warp walks
+    // Nodes whose paths a warp walks: at least 8 where they may be long, so that four lanes at most have one.
+    static constexpr int kPer = NT > 1 && kNodes / (D / 32) < 8 ? 8 : kNodes / (D / 32);
     static constexpr int kGroups = D / 32;                   // of 32 state columns
     static constexpr int kRowK = 2 * D;                      // bytes of a row of k or q
     // Of k.k and q.k only what lies on or below the diagonal: k.k as a triangle (key_row), q.k by tiles of 16 (struct Row).
@@ -193,15 +196,15 @@ __device__ __forceinline__ void products(const uint8_t *sk, const uint8_t *sq, i
 // b_w g_w, and p' = a_w (p - c k_w) changes the others by k_w.k_x.  C[u] takes the row's place, as sums of two bf16, zeros
 // off the path.  Gives the product of the decays.
 //
-// Of up to 8 nodes (with room for no more than 16: of all) the walk is held in registers, place by place, a thread a node.
-// (41 requests of 15 to 26 nodes in a chain, 32 heads: with up to 16 nodes so 39 us, 10 32.8, 8 and 6 31.9; trees 29.7, and
-// 32 with none so.)
-constexpr int short_path(int nt) { return nt == 2 ? 16 : 8; }
+// Of up to kShortPath nodes the walk is held in registers, place by place, a thread a node.  (41 requests of 15 to 26 nodes
+// in a chain, 32 heads: with up to 16 nodes so 39 us, 10 32.8, 8 and 6 31.9; trees 29.7, and 32 with none so.  256 chains of 12
+// to 16: with 16 66.8, 8 58.4.)
+constexpr int kShortPath = 8;
 
 template <int D, int NT>
 __device__ __forceinline__ float walk_short(uint64_t path, int most, float *row, int cols, const float *fk, const float2 *gates) {
     using Sh = TreeShape<D, NT>;
-    constexpr int kMost = short_path(NT);
+    constexpr int kMost = kShortPath;
     const int steps = __popcll(path);
     int x[kMost];
     float g[kMost];
@@ -428,16 +431,16 @@ __global__ void __launch_bounds__(TreeShape<D, NT>::kThreads, TreeShape<D, NT>::
     __syncthreads();
 
     // 3. C and G, the nodes dealt out over the warps.
-    {
+    if (warp * Sh::kPer < Sh::kNodes) {
         const int first = warp * Sh::kPer, u = first + lane;
         const bool mine = lane < Sh::kPer && u < m;
         path = mine ? word[u] : 0;
         const int most = __reduce_max_sync(0xffffffffu, __popcll(path));
-        if (NT <= 2 || most <= short_path(NT)) {
+        if (NT == 1 || most <= kShortPath) {
             float g = 0.f;
             if (mine) g = walk_short<D, NT>(path, most, fq + Row(u).at, Row(u).cols, fk, gates);
             if (lane < Sh::kPer) gamma[u] = g;
-        } else if constexpr (NT > 2) {
+        } else if constexpr (NT > 1) {
 #pragma unroll 1
             for (int i = 0; i < Sh::kPer; i += pass_of(Sh::kPer)) walk_long<D, NT>(first + i, m, word, fq, fk, gates, gamma, lane);
         }
