@@ -27,8 +27,8 @@
 //      the last product: O^T += R^T C^T, both as sums of two bf16.
 //
 // What bounds it.  Up to 16 nodes: the state's 64 KB per head.  256 requests of
-// 4 to 12 nodes, 16 heads: 303 MB in 55.5 us, 5.5 TB/s, 0.80 of the copy peak,
-// the tensor pipe 29 % busy; what is missing are the loads that a block does not
+// 4 to 12 nodes, 16 heads: 303 MB in 53.3 us, 5.7 TB/s, 0.84 of the copy peak,
+// the tensor pipe 30 % busy; what is missing are the loads that a block does not
 // have in flight while it walks.  With 33 to 64 nodes (64 requests, 32 heads:
 // 76 us) a block's phases: 9000 cycles until k and q are there, 4000 for their
 // products, 3000 for the walks, 10000 for each slab's product with the state and
@@ -39,7 +39,7 @@
 //
 // Why mma.sync and not tcgen05.  Up to 16 nodes the products hide behind the
 // state.  A tcgen05 product takes the state as two bf16 operands out of shared
-// memory (64 KB a block) or TMEM: two blocks per SM instead of four to six, and
+// memory (64 KB a block) or TMEM: two blocks per SM instead of four to seven, and
 // one more trip of 64 KB, for a pipe that is not the bound; and with one
 // arithmetic for every size a request's bits do not depend on max_nodes.
 //
