@@ -182,7 +182,7 @@ def test_replays_for_other_trees(gdn):
 
 @pytest.mark.parametrize("h_k,h_v,d", [HEADS[1], HEADS[3]])
 def test_a_long_path_beside_short_ones_changes_no_bit(gdn, h_k, h_v, d):
-    # paths of up to 16 nodes and longer ones are walked in different ways
+    # short paths and long ones are walked in different ways
     short = tu.parents_of(20, "mixed", seed=3)
     assert max(len(tu.path_of(short, u)) for u in range(20)) <= 16
     both = short + [19] + list(range(20, 50))
