@@ -494,6 +494,7 @@ __global__ void __launch_bounds__(TreeShape<D, NT>::kThreads, TreeShape<D, NT>::
                 for (int h = 0; h < 4; ++h)
 #pragma unroll
                     for (int t = 0; t < kStep; ++t) {
+                        if (t > 0 && (t0 + t) * 8 >= m) continue;
                         const uint32_t(&f)[4] = h & 1 ? lo[h >> 1] : hi[h >> 1];
                         mma(y[t0 + t], f, h & 2 ? kq[0][t].z : kq[0][t].x, h & 2 ? kq[0][t].w : kq[0][t].y);
                         mma(o[t0 + t], f, h & 2 ? kq[1][t].z : kq[1][t].x, h & 2 ? kq[1][t].w : kq[1][t].y);
