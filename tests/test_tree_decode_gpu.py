@@ -233,3 +233,29 @@ def test_a_state_off_its_boundary_is_refused(gdn):
     assert c["state"].data_ptr() % 32 == 16
     with pytest.raises(RuntimeError):
         tu.run_delta(gdn, c)
+
+
+@pytest.mark.parametrize("h_k,h_v,d", HEADS)
+def test_a_node_beside_a_long_path_does_not_show(gdn, h_k, h_v, d):
+    # a chain with a leaf at each of its nodes; NaN and infinities in a leaf, and in a node of the chain
+    sizes = [14, 32, 64]
+    trees = [[max(-1, u - 2 if u % 2 == 0 else u - 1) for u in range(m)] for m in sizes]
+    assert max(len(tu.path_of(trees[-1], u)) for u in range(64)) == 33
+    c = tu.make_delta(trees, h_k, h_v, d, seed=18)
+    want = check(gdn, c)
+    cu = c["cu"].tolist()
+    for r, m in enumerate(sizes):
+        for w in (m // 2 + 1 - m // 2 % 2, m // 2 - m // 2 % 2):  # odd: a leaf; even: on the chain
+            below = torch.tensor([w in tu.path_of(trees[r], u) for u in range(m)], device="cuda")
+            assert int(below.sum()) == 1 if w % 2 else below.any() and not below.all()
+            rows = torch.zeros(len(want), dtype=torch.bool, device="cuda")
+            rows[cu[r]:cu[r + 1]] = below
+            for name, value in (("k", NAN), ("k", INF), ("v", NAN), ("v", INF), ("q", NAN), ("g", NAN), ("beta", INF)):
+                keep = c[name][cu[r] + w].clone()
+                c[name][cu[r] + w] = value
+                got, st = tu.run_delta(gdn, c)
+                c[name][cu[r] + w] = keep
+                assert st == 0 and torch.equal(got[~rows], want[~rows]), (r, w, name, value)
+                assert not torch.isfinite(got[cu[r] + w]).any()
+                if name != "q":
+                    assert not torch.isfinite(got[rows]).any()
