@@ -76,17 +76,18 @@ class TreeBlock(HybridBlock):
     def commit(self, kept, buf, path, context):
         """Accepts path [n][L] of node numbers, -1 behind its end: the states go on over it, its keys and values move up
         behind the context, which grows by it."""
-        n, L = path.shape
-        live = path >= 0
-        cu = buf["cu"][:-1].long()[:, None]
-        tok = (cu + path.clamp(min=0)).flatten()
+        L = path.shape[1]
+        if L == 0 or kept[0].shape[0] == 0:
+            return
+        live, cu = path >= 0, buf["cu"][:-1].long()[:, None]
+        # (behind a path's end token 0, which is always there: a request may have no nodes)
+        tok = torch.where(live, cu + path, 0).flatten()
         q, k, v, g, beta = (t[tok] for t in kept)
         for gate in (g, beta):  # tokens that fill up a shorter path leave the state as it is
             gate.masked_fill_(~live.flatten()[:, None], 0.0)
         gdn.gdn_decode_multi(L, q, k, v, g, beta, self.state, buf["rows"], torch.empty_like(v), dev_status=self.status)
-        # (a tree may have fewer nodes than L: what lies behind its path is not written)
-        place = torch.where(live, cu + torch.arange(L, device=path.device), cu)
-        to = torch.where(live, buf["slots"][place], -1).flatten()
+        place = torch.where(live, cu + torch.arange(L, device=path.device), 0)
+        to = torch.where(live, buf["slots"][place], -1).flatten()  # (not written behind a path's end)
         slots = buf["slots"][tok].long()
         k, v = (c[slots // self.page, slots % self.page] for c in (self.k_cache, self.v_cache))
         gdn.gdn_paged_kv_write(k, v, self.k_cache, self.v_cache, to, dev_status=self.status)
