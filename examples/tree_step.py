@@ -82,9 +82,8 @@ class TreeBlock(HybridBlock):
         live, cu = path >= 0, buf["cu"][:-1].long()[:, None]
         # (behind a path's end token 0, which is always there: a request may have no nodes)
         tok = torch.where(live, cu + path, 0).flatten()
-        q, k, v, g, beta = (t[tok] for t in kept)
-        for gate in (g, beta):  # tokens that fill up a shorter path leave the state as it is
-            gate.masked_fill_(~live.flatten()[:, None], 0.0)
+        # (zeros throughout: with g = beta = 0 the state stays as it is, but for 0 times a k or v that is not finite)
+        q, k, v, g, beta = (t[tok].masked_fill_(~live.flatten().view(-1, *[1] * (t.dim() - 1)), 0.0) for t in kept)
         gdn.gdn_decode_multi(L, q, k, v, g, beta, self.state, buf["rows"], torch.empty_like(v), dev_status=self.status)
         place = torch.where(live, cu + torch.arange(L, device=path.device), 0)
         to = torch.where(live, buf["slots"][place], -1).flatten()  # (not written behind a path's end)

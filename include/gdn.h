@@ -513,7 +513,8 @@ size_t gdn_paged_attention_workspace_bytes(int32_t h_q, int32_t h_kv, int32_t d,
  * gdn_rotary, gdn_paged_kv_write and gdn_tree_attention, or gdn_tree_decode.
  * What is accepted, one path from a root, is then committed: its keys and
  * values with gdn_paged_kv_write to the slots of their positions, the states
- * with gdn_decode_multi (tokens that fill up a shorter path: g = beta = 0).
+ * with gdn_decode_multi (tokens that fill up a shorter path: g = beta = 0, and
+ * q, k and v of zeros or other finite numbers, since 0 times a NaN is one).
  *
  * Nodes are numbered from 0 per request, in an order that puts every parent
  * before its children; a request has at most 64.  A single token is a tree of

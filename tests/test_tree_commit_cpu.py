@@ -93,3 +93,10 @@ def commit(example, sizes, paths, spoil=()):
     ([0, 0], [[], []]), ([3, 1], [[], []]), ([1], [[0]])])
 def test_paths_of_any_length(example, sizes, paths):
     commit(example, sizes, paths)
+
+
+@pytest.mark.parametrize("sizes,paths,spoil", [
+    ([5, 7], [[1, 2], [0, 3, 5]], [0]), ([5, 7], [[], [0, 3, 5]], [0, 3]), ([0, 4, 3], [[], [1], [2, 1]], [0, 2, 4])])
+def test_rejected_nodes_that_are_not_finite(example, sizes, paths, spoil):
+    # a token that fills up a shorter path is no accepted one, whatever that holds
+    commit(example, sizes, paths, spoil)

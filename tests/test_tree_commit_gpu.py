@@ -40,3 +40,23 @@ def test_requests_without_nodes(sizes, lengths):
     outs, _ = block.step(x, context, new, block.buffers(3, 21), parents=tu.i32(sum(trees, [])))
     ex.check(block)
     verified_against_prompts(ex, outs, x, trees, before)
+
+
+def test_a_rejected_node_that_is_not_finite():
+    ex = load_example()
+    prompts, sizes = [70, 33], [5, 7]
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    x0 = torch.randn((sum(prompts), 512), generator=gen, device="cuda").bfloat16()
+    x = torch.randn((sum(sizes), 512), generator=gen, device="cuda").bfloat16()
+    trees, states = [[-1, -1, 1, 0, 2], [-1] * 7], []
+    for spoil in (False, True):
+        block, _ = prompts_of(ex, x0, prompts)
+        context, buf = tu.i32(prompts), block.buffers(2, sum(sizes))
+        fed = x.clone()
+        if spoil:
+            fed[0], fed[6:] = float("nan"), float("inf")
+        _, kept = block.step(fed, context, tu.i32(sizes), buf, parents=tu.i32(sum(trees, [])))
+        block.commit(kept, buf, torch.tensor([[1, 2, 4], [0, -1, -1]], device="cuda"), context)
+        ex.check(block)
+        states.append(block.state[:2].clone())
+    assert torch.isfinite(states[1]).all() and torch.equal(*states)
