@@ -518,7 +518,8 @@ size_t gdn_paged_attention_workspace_bytes(int32_t h_q, int32_t h_kv, int32_t d,
  *
  * Nodes are numbered from 0 per request, in an order that puts every parent
  * before its children; a request has at most 64.  A single token is a tree of
- * one node, so rows without a draft ride along.
+ * one node, so rows without a draft ride along.  The words (masks) are 8-byte
+ * aligned.
  */
 
 /*
@@ -635,7 +636,7 @@ typedef struct {
  *   d            <= 1024; rotary_dim even, <= d.
  *   magnitude    finite; with YARN usually 0.1 ln(factor) + 1.
  *   positions    [num_tokens] int32;  frequencies [rotary_dim / 2] in device
- *                memory.
+ *                memory, 8-byte aligned.
  */
 gdn_status_t gdn_rotary(int32_t dtype, int64_t num_tokens, int32_t d, int32_t rotary_dim, int32_t interleaved,
                         float magnitude, const int32_t *positions, const uint64_t *frequencies,

@@ -42,6 +42,7 @@ bool dims_ok(const gdn_dims_t *d, gdn_status_t *why) {
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 
 // Validates a host cu_seqlens mirror: starts at 0, non-decreasing.
 bool cu_ok(const int32_t *cu, int32_t n) {
@@ -302,7 +303,8 @@ gdn_status_t gdn_tree_decode(const gdn_dims_t *dims, int32_t num_rows, int32_t m
     if (num_tokens > INT_MAX || static_cast<int64_t>(num_rows) * dims->h_v > INT_MAX) return GDN_ERR_UNSUPPORTED;
     if (num_rows == 0 || num_tokens == 0) return GDN_OK;
     if (!cu_seqlens || !masks || !q || !k || !v || !g || !beta || !state || !src_slot || !o) return GDN_ERR_INVALID_ARG;
-    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || (reinterpret_cast<uintptr_t>(state) & 31u) != 0)
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned8(masks) ||
+        (reinterpret_cast<uintptr_t>(state) & 31u) != 0)
         return GDN_ERR_INVALID_ARG;
     gdn::TreeDecodeArgs a{};
     a.num_rows = num_rows;

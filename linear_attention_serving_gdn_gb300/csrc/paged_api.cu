@@ -13,6 +13,7 @@ constexpr int32_t kMaxHeads = 65536;              // K/V heads: pieces of a toke
 constexpr int32_t kMaxGroup = 128;  // query heads per K/V head: one token's heads fit a 128-row tile
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 
 // A stride matters only where its dimension has more than one entry; an unused
 // one is replaced by the row length, so that tensor maps always see a valid value.
@@ -59,7 +60,7 @@ gdn_status_t attention_impl(const gdn_paged_cache_t *cache, int32_t num_reqs, in
     if (max_kv_len > kMaxKeys) return GDN_ERR_UNSUPPORTED;
     if (num_tokens == 0) return GDN_OK;
     if (!q || !o || !cu_seqlens || !aligned16(q) || !aligned16(o)) return GDN_ERR_INVALID_ARG;
-    if (tree && !masks) return GDN_ERR_INVALID_ARG;
+    if (tree && (!masks || !aligned8(masks))) return GDN_ERR_INVALID_ARG;
     if (num_reqs > 0 && (!kv_lens || (table_width > 0 && (!block_table || table_stride < table_width))))
         return GDN_ERR_INVALID_ARG;
     const int64_t q_row = static_cast<int64_t>(h_q) * c.d;
@@ -219,6 +220,7 @@ gdn_status_t gdn_tree_maps(int32_t num_reqs, int64_t num_tokens, const int32_t *
     if (num_tokens > INT_MAX) return GDN_ERR_UNSUPPORTED;
     if (num_tokens == 0) return GDN_OK;
     if (!parents || !masks || !positions || (num_reqs > 0 && (!cu_seqlens || !kv_lens))) return GDN_ERR_INVALID_ARG;
+    if (!aligned8(masks)) return GDN_ERR_INVALID_ARG;
     gdn::TreeMapsArgs a{};
     a.num_reqs = num_reqs;
     a.num_tokens = num_tokens;
@@ -247,7 +249,7 @@ gdn_status_t gdn_rotary(int32_t dtype, int64_t num_tokens, int32_t d, int32_t ro
         }
     if (a.side[0].h + a.side[1].h == 0) return q || k ? GDN_OK : GDN_ERR_INVALID_ARG;
     if (num_tokens == 0) return GDN_OK;
-    if (!positions || !frequencies) return GDN_ERR_INVALID_ARG;
+    if (!positions || !frequencies || !aligned8(frequencies)) return GDN_ERR_INVALID_ARG;
     a.num_tokens = num_tokens;
     a.d = d;
     a.rot = rotary_dim;
