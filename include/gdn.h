@@ -615,8 +615,9 @@ gdn_status_t gdn_rotary_frequencies(int32_t rotary_dim, double base, int32_t sca
 
 /* q or k of a rotation: element (t, h, i) of x at t * x_token_stride
  * + h * x_head_stride + i, and the same for out (elements; any alignment:
- * accesses are as wide as sizes, addresses and strides allow, 16 bytes at most).  out
- * may be x, with the same strides; else the two do not overlap. */
+ * accesses are as wide as sizes, addresses and strides allow, 16 bytes at most).
+ * Rows of x may share elements (strides of 0), rows of out may not.  out may be
+ * x, with the same strides; else the two do not overlap. */
 typedef struct {
     const void *x;
     void *out;

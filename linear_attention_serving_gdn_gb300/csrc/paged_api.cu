@@ -91,6 +91,19 @@ gdn_status_t attention_impl(const gdn_paged_cache_t *cache, int32_t num_reqs, in
 constexpr int32_t kMaxRotaryDim = 1024;
 constexpr int64_t kMaxRotaryStride = int64_t{1} << 39;
 
+// Whether no two of the rows of d elements at t * token_stride + h * head_stride share one; strides of d to kMaxRotaryStride.
+// Rows h heads apart meet those of a token whose distance is nearest to theirs, or none.  (The products stay under 2^56.)
+bool rows_apart(int64_t tokens, int64_t token_stride, int64_t heads, int64_t head_stride, int64_t d) {
+    if (tokens <= 1 || heads <= 1 || token_stride >= (heads - 1) * head_stride + d) return true;
+    if ((head_stride - d) / token_stride >= tokens - 1) return true;
+    for (int64_t h = 1; h < heads; ++h) {
+        const int64_t far = h * head_stride, t = far / token_stride;  // t tokens are that far or nearer, t + 1 farther
+        if ((t > 0 && t < tokens && far - t * token_stride < d) || (t + 1 < tokens && (t + 1) * token_stride - far < d))
+            return false;
+    }
+    return true;
+}
+
 // One side of a rotation; strides that matter only.
 gdn_status_t rotary_side_ok(const gdn_rotary_side_t &in, int64_t num_tokens, int32_t d, gdn::RotarySide *out) {
     if (in.heads < 0) return GDN_ERR_INVALID_ARG;
@@ -108,7 +121,7 @@ gdn_status_t rotary_side_ok(const gdn_rotary_side_t &in, int64_t num_tokens, int
     };
     // Inputs may be shared by tokens or heads (stride 0); outputs may not.
     if (bad(s.token_stride, num_tokens, 0) || bad(s.head_stride, in.heads, 0) || bad(s.dst_token_stride, num_tokens, d) ||
-        bad(s.dst_head_stride, in.heads, d))
+        bad(s.dst_head_stride, in.heads, d) || !rows_apart(num_tokens, s.dst_token_stride, in.heads, s.dst_head_stride, d))
         return GDN_ERR_INVALID_ARG;
     if (s.src == s.dst && (s.token_stride != s.dst_token_stride || s.head_stride != s.dst_head_stride))
         return GDN_ERR_INVALID_ARG;
