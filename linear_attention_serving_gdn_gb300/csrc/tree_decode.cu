@@ -21,10 +21,11 @@
 //   3. The walks, in registers: C and G.  Short paths place by place, a thread
 //      a node; longer ones node by node, several lanes a node.
 //   4. S^T [K; Q] with the state's rows as the A operand, each value as the sum
-//      of two bf16 (2^-15 of it is left at most), straight from registers: the
+//      of two bf16 (2^-16 of it is left at most), straight from registers: the
 //      state is read once and never staged.
 //   5. R = v - G S^T k in the accumulator's layout, which is the A layout of
-//      the last product: O^T += R^T C^T, both as sums of two bf16.
+//      the last product: O^T += R^T C^T, both as sums of two bf16, rounded so
+//      that 2^-15 of a product is left at most.
 //
 // What bounds it.  Up to 16 nodes: the state's 64 KB per head.  256 requests of
 // 4 to 12 nodes, 16 heads: 303 MB in 53.3 us, 5.7 TB/s, 0.84 of the copy peak,
@@ -69,11 +70,17 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// x and y as sums of two bf16: the upper halves cut off, and the rest rounded.
+// x and y as sums of two bf16: the upper halves cut off, and the rest, under 2^-7 of it, rounded: within 2^-16.
 __device__ __forceinline__ void split2(float x, float y, uint32_t *hi, uint32_t *lo) {
     const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
     *hi = __byte_perm(a, b, 0x7632);
     *lo = pack_bf16(x - __uint_as_float(a & 0xffff0000u), y - __uint_as_float(b & 0xffff0000u));
+}
+// The same with the upper halves rounded to the nearest (never up to infinity), so that the rests are at most 2^-8 of the
+// number: of a product of two such sums, without that of the rests, 2^-15 is missing at most (cut off 2^-14 and more).
+__device__ __forceinline__ void split2_near(float x, float y, uint32_t *hi, uint32_t *lo) {
+    asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(*hi) : "f"(y), "f"(x));
+    *lo = pack_bf16(x - __uint_as_float(*hi << 16), y - __uint_as_float(*hi & 0xffff0000u));
 }
 
 // 16 bytes from global to shared memory, or zeros.
@@ -236,8 +243,10 @@ __device__ __forceinline__ float walk_short(uint64_t path, int most, float *row,
             g[j] = fmaf(ac, kk[x[j]], a * g[j]);
         }
         if (i < steps) {
-            hi[x[i]] = static_cast<uint16_t>(__float_as_uint(c) >> 16);
-            lo[x[i]] = float_to_bf16_bits(c - __uint_as_float(__float_as_uint(c) & 0xffff0000u));
+            uint32_t h, l;
+            split2_near(c, 0.f, &h, &l);
+            hi[x[i]] = static_cast<uint16_t>(h);
+            lo[x[i]] = static_cast<uint16_t>(l);
             decay *= a;
         }
     }
@@ -308,8 +317,8 @@ __device__ __forceinline__ void walk_long(int first, int m, const uint64_t *word
         const int x = b * kSteps + 4 * sub;
         if (x < at.cols) {
             uint2 h, l;
-            split2(mine[0], mine[1], &h.x, &l.x);
-            split2(mine[2], mine[3], &h.y, &l.y);
+            split2_near(mine[0], mine[1], &h.x, &l.x);
+            split2_near(mine[2], mine[3], &h.y, &l.y);
             *reinterpret_cast<uint2 *>(row + x / 2) = h;
             *reinterpret_cast<uint2 *>(row + x / 2 + at.cols / 2) = l;
         }
@@ -551,8 +560,8 @@ __global__ void __launch_bounds__(TreeShape<D, NT>::kThreads, TreeShape<D, NT>::
             for (int j = 0; j < 2; ++j)
                 if (2 * kt + j < NT) {
                     const float(&x)[4] = y[2 * kt + j];
-                    split2(x[0], x[1], &hi[2 * j], &lo[2 * j]);
-                    split2(x[2], x[3], &hi[2 * j + 1], &lo[2 * j + 1]);
+                    split2_near(x[0], x[1], &hi[2 * j], &lo[2 * j]);
+                    split2_near(x[2], x[3], &hi[2 * j + 1], &lo[2 * j + 1]);
                 }
             constexpr int kStep = NT < 4 ? NT : 4;
 #pragma unroll
