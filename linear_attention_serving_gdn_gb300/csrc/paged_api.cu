@@ -281,7 +281,7 @@ gdn_status_t gdn_rotary_frequencies(int32_t rotary_dim, double base, int32_t sca
     if (scaling < GDN_ROTARY_NONE || scaling > GDN_ROTARY_YARN) return GDN_ERR_UNSUPPORTED;
     if (scaling != GDN_ROTARY_NONE && (!(factor >= 1.) || !isfinite(factor))) return GDN_ERR_INVALID_ARG;
     const double rot = rotary_dim;
-    double lo = 0., hi = 0.;
+    double lo = 0., hi = 0., slow = 0.;  // ends of the ramp; the pair that makes beta_slow turns
     if (scaling == GDN_ROTARY_NTK) {
         if (rotary_dim <= 2) return GDN_ERR_INVALID_ARG;
         base *= pow(factor, rot / (rot - 2.));
@@ -291,13 +291,15 @@ gdn_status_t gdn_rotary_frequencies(int32_t rotary_dim, double base, int32_t sca
         // The pair that makes `turns` turns over the original length.
         auto pair = [&](double turns) { return rot * log(static_cast<double>(original_length) / (turns * kTwoPi)) / (2. * log(base)); };
         lo = fmax(floor(pair(beta_fast)), 0.);
-        hi = fmin(ceil(pair(beta_slow)), rot - 1.);
+        slow = pair(beta_slow);
+        hi = fmin(ceil(slow), rot - 1.);
     }
     for (int32_t i = 0; i < rotary_dim / 2; ++i) {
         double f = pow(base, -2. * i / rot);
         if (scaling == GDN_ROTARY_LINEAR) f /= factor;
         if (scaling == GDN_ROTARY_YARN) {
-            const double ramp = fmin(fmax((i - lo) / fmax(hi - lo, 0.001), 0.), 1.);
+            // (slow < 0: all pairs turn less, pair 0 too, which the clamped ramp begins with)
+            const double ramp = slow < 0. ? 1. : fmin(fmax((i - lo) / fmax(hi - lo, 0.001), 0.), 1.);
             f = f * (1. - ramp) + f / factor * ramp;
         }
         out[i] = static_cast<uint64_t>(nearbyint(ldexp(f / kTwoPi, 64)));  // (at most a sixth of a turn)

@@ -51,3 +51,22 @@ def test_rotary_outputs_far_apart(gdn):  # noqa: F811
             (2, 65536, big, 1 << 25, INVALID)]:
         got = rotary(gdn, T=T, d=128, rot=64, k=side(gdn, heads=1 << 17), heads=heads, ot=ot, oh=oh)
         assert got == status, (T, heads, ot, oh)
+
+
+@pytest.mark.parametrize("rot", [2, 16, 128])
+@pytest.mark.parametrize("length,fast,slow", [(4, 32.0, 1.0), (1, 32.0, 1.0), (4096, 5000.0, 1000.0), (4096, 1000.0, 1000.0),
+                                              (6, 1.0, 1.0), (4096, 32.0, 1.0), (1 << 40, 0.001, 0.0001)])
+def test_yarn_pairs_outside_its_ramp(gdn, rot, length, fast, slow):  # noqa: F811
+    # a pair that turns less than `slow` times over the length is divided by the factor, one that turns more than `fast`
+    # times stays; what lies between is between
+    from math import pi
+    got = gdn.gdn_rotary_frequencies(rot, 1e4, "yarn", 8.0, length, fast, slow).tolist()
+    plain = gdn.gdn_rotary_frequencies(rot, 1e4).tolist()
+    for i, (f, p) in enumerate(zip(got, plain)):
+        turns = length * 1e4 ** (-2 * i / rot) / (2 * pi)
+        if turns < slow * (1 - 1e-9):
+            assert abs(f - p / 8) <= p / 8 * 2.0 ** -45 + 1, i
+        elif turns > fast * (1 + 1e-9):
+            assert abs(f - p) <= p * 2.0 ** -45 + 1, i
+        else:
+            assert p / 8 * (1 - 2.0 ** -45) - 1 <= f <= p * (1 + 2.0 ** -45) + 1, i
