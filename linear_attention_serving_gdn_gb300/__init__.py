@@ -840,23 +840,24 @@ def _rotary_side(x, out, name, dtype, T, d):
 
 def gdn_rotary(q, k, positions, frequencies, q_out=None, k_out=None, interleaved: bool = False,
                magnitude: float = 1.0, stream=None) -> None:
-    """Rotary positions of ``q`` ([T][h_q][d]) and ``k`` ([T][h_kv][d]; None: q
-    alone), into ``q_out`` and ``k_out`` or, where those are None, in place (see
+    """Rotary positions of ``q`` ([T][h_q][d]) and ``k`` ([T][h_kv][d]; None for
+    either: the other alone), into ``q_out`` and ``k_out`` or, where those are None, in place (see
     gdn.h).  The first 2 * len(frequencies) elements of each head turn, in
     halves or ``interleaved`` pairs; ``frequencies`` is the tensor of
     ``gdn_rotary_frequencies``, on the device.  Any strides with a contiguous
     last dimension."""
     lib = _lib or load_library()
-    dtype = getattr(q, "dtype", None)
+    some = k if q is None else q
+    dtype = getattr(some, "dtype", None)
     code = _PAGED_DTYPES.get(dtype)
     if code is None:
-        raise TypeError(f"q must be bfloat16 or float16, got {dtype}")
+        raise TypeError(f"{'k' if q is None else 'q'} must be bfloat16 or float16, got {dtype}")
     if not (positions.__class__ is frequencies.__class__ is _Tensor and positions.dtype is _i32 and frequencies.dtype is _i64
             and positions.is_cuda and frequencies.is_cuda and positions.stride() == frequencies.stride() == _one):
         _i32_vec(positions, "positions"), _words(frequencies, "frequencies")
-    T, d = positions.numel(), q.shape[-1]
+    T, d = positions.numel(), some.shape[-1]
     status = lib.gdn_rotary(code, T, d, 2 * frequencies.numel(), 1 if interleaved else 0, magnitude, positions.data_ptr(),
-                            frequencies.data_ptr(), _rotary_side(q, q_out, "q", dtype, T, d),
+                            frequencies.data_ptr(), None if q is None else _rotary_side(q, q_out, "q", dtype, T, d),
                             None if k is None else _rotary_side(k, k_out, "k", dtype, T, d),
                             _raw_stream(_current_device()) if stream is None and _raw_stream else _stream(stream))
     if status:

@@ -2,6 +2,7 @@
 import ctypes
 
 import pytest
+import torch
 
 from tests.test_paged_cpu import INVALID, UNSUPPORTED
 from tests.test_tree_cpu import attention, decode, gdn, maps, rotary, side  # noqa: F401
@@ -70,3 +71,13 @@ def test_yarn_pairs_outside_its_ramp(gdn, rot, length, fast, slow):  # noqa: F81
             assert abs(f - p) <= p * 2.0 ** -45 + 1, i
         else:
             assert p / 8 * (1 - 2.0 ** -45) - 1 <= f <= p * (1 + 2.0 ** -45) + 1, i
+
+
+def test_rotary_of_neither_side(gdn):  # noqa: F811
+    i, w = torch.zeros(1, dtype=torch.int32), torch.zeros(1, dtype=torch.int64)
+    with pytest.raises(TypeError, match="k must be"):
+        gdn.gdn_rotary(None, None, i, w)
+    with pytest.raises(TypeError, match="k must be"):
+        gdn.gdn_rotary(None, torch.zeros(1, 2, 64), i, w)
+    with pytest.raises(ValueError):  # (not on the device)
+        gdn.gdn_rotary(None, torch.zeros(1, 2, 64, dtype=torch.bfloat16), i, w)
