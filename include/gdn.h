@@ -584,8 +584,10 @@ gdn_status_t gdn_tree_attention(const gdn_paged_cache_t *cache, int32_t num_reqs
  * written).  GDN_DEV_BAD_SLOT (a slot >= num_slots) and GDN_DEV_BAD_LENGTH (more nodes than max_nodes): zero
  * outputs; GDN_DEV_BAD_LENGTH also for a row whose cu_seqlens run backwards or
  * past cu_seqlens[num_rows] or num_tokens: it is skipped.
- * A node's outputs depend on its path and the row's state alone, bit for bit:
- * not on its siblings, the batch or max_nodes.  A NaN or infinity in a node
+ * A node's outputs depend on its word, what the nodes named there hold and the
+ * row's state alone, bit for bit: not on what other nodes hold, the batch or
+ * max_nodes.  (Under other numbers a path's sums are taken in other groups, and
+ * may be rounded otherwise.)  A NaN or infinity in a node
  * shows in it and the nodes below it only.
  */
 gdn_status_t gdn_tree_decode(const gdn_dims_t *dims, int32_t num_rows, int32_t max_nodes, int64_t num_tokens,

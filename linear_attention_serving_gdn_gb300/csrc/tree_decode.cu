@@ -49,7 +49,8 @@
 // L2 65 / 91, the block's own state to L2 for up to 16 nodes 63, k and q by 8-byte
 // pieces 61 / 97.
 //
-// A node's bits depend on its own path and the state alone.  A value that is
+// A node's bits depend on its word, the nodes on its path and the state alone (on the
+// word, since the last product sums over node numbers, 16 at a time).  A value that is
 // not finite stays with the nodes whose path it is on: it is left out of the
 // last product and added to those alone.
 #include "gdn_internal.cuh"
