@@ -577,9 +577,9 @@ gdn_status_t gdn_tree_attention(const gdn_paged_cache_t *cache, int32_t num_reqs
  *   state        [num_slots][h_v][d_v][d_k] fp32, 32-byte aligned, read at
  *                src_slot[r]; a negative slot marks a padded row, whose outputs
  *                are zeros.
- * Products with the state take each of its values to within 2^-16 of it, and
- * those of a node's share with its factor are within 2^-15 of their values;
- * sums are fp32, o is rounded once.
+ * Products with the state take each of its values to within 2^-16 of it; what
+ * a node on the path adds to an output, a number times a vector, is within
+ * 2^-15 of that product; sums are fp32, o is rounded once.
  * Tokens from cu_seqlens[num_rows] on get zeros (with num_rows = 0 nothing is
  * written).  GDN_DEV_BAD_SLOT (a slot >= num_slots) and GDN_DEV_BAD_LENGTH (more nodes than max_nodes): zero
  * outputs; GDN_DEV_BAD_LENGTH also for a row whose cu_seqlens run backwards or

@@ -61,9 +61,9 @@
 // 64-bit word per token, looked at only in the last one or two key tiles, by the
 // softmax threads whose row it is; scheduling, splits and the join are the same.
 // 8 trees of 25 to 32 nodes over 60 to 100 thousand keys, 32/8 heads of 128: 2.87
-// GB in 442 to 449 us, 0.95 of the copy peak; 128 of up to 12 over 2000 to 8000,
+// GB in 442 to 454 us, 0.93 to 0.95 of the copy peak; 128 of up to 12 over 2000 to 8000,
 // 16/16 of 64: 2.55 GB in 418 to 423, 0.90; 64 of 16 to 64 over 500 to 8000, 16/2
-// of 256: 195 GF in 218 to 225 us, as gdn_paged_attention of the same lengths
+// of 256: 195 GF in 218 to 230 us, as gdn_paged_attention of the same lengths
 // (215): row tiles of 16 tokens a seventh empty, parts that a request alone would
 // need and the join of their 97 MB (the kernel itself 188 us, the tensor pipe 63 %
 // busy); 64 equal ones of 64 nodes over 8000 keys 1.19 PF/s.  One tree of 7 over

@@ -28,7 +28,7 @@
 //      that 2^-15 of a product is left at most.
 //
 // What bounds it.  Up to 16 nodes: the state's 64 KB per head.  256 requests of
-// 4 to 12 nodes, 16 heads: 303 MB in 53.3 us, 5.7 TB/s, 0.84 of the copy peak,
+// 4 to 12 nodes, 16 heads: 303 MB in 53.5 us, 5.7 TB/s, 0.83 of the copy peak,
 // the tensor pipe 30 % busy; what is missing are the loads that a block does not
 // have in flight while it walks.  With 33 to 64 nodes (64 requests, 32 heads:
 // 76 us) a block's phases: 9000 cycles until k and q are there, 4000 for their
@@ -36,13 +36,14 @@
 // 2500 for the rest of it, four blocks of an SM in turn: the tensor pipe is 46 %
 // busy (712 products a warp, 2 cycles each of the SM, are 36 us), the shared
 // memory's pipe 55 %, and neither is the bound alone.  One tree: 5.2 us, the
-// chain of these phases.
+// chain of these phases.  Heads of 64 (out of L2): 256 of 4 to 12 nodes 11 us with
+// 8/8 heads, 14 with 4/12; 64 of 33 to 64 nodes 14 and 17.
 //
 // Why mma.sync and not tcgen05.  Up to 16 nodes the products hide behind the
 // state.  A tcgen05 product takes the state as two bf16 operands out of shared
 // memory (64 KB a block) or TMEM: two blocks per SM instead of four to seven, and
-// one more trip of 64 KB, for a pipe that is not the bound; and with one
-// arithmetic for every size a request's bits do not depend on max_nodes.
+// one more trip of 64 KB, for a pipe that is not the bound (counted, not measured);
+// and with one arithmetic for every size a request's bits do not depend on max_nodes.
 //
 // Tried and worse (256 small trees / 64 large ones, us, at 61 / 91): blocks that
 // take several (request, head) in turn 65 / 98, the state of the next block to
@@ -617,6 +618,9 @@ cudaError_t launch(const TreeDecodeArgs &a, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
+// By the bound, which is all that the host knows of the rows: small rows beside a large one pay for its form (248 rows of 1
+// to 8 nodes, 16 heads: bound 8 48.9 us, 16 51.4, 32 58.3, 64 70.6; with 8 rows of 64 nodes among them 80.4, in two calls
+// with bounds of their own 64.2).
 template <int D>
 cudaError_t launch_d(const TreeDecodeArgs &a, cudaStream_t stream) {
     if (a.max_nodes <= 8) return launch<D, 1>(a, stream);

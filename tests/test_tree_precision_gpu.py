@@ -22,8 +22,8 @@ def test_products_of_the_nodes(gdn, m, max_nodes, d):
 
     Every number but b and 1 + y is held exactly in 8 bits (y, v0, the factors of 1 and -1), the sums are exact but for fp32's
     roundings.  So b (1 + y) is all that the splits take something of: each factor is the sum of two bf16, the upper one off
-    by 2^-8 of it at most, the rest by 2^-8 of that, less the product of the two rests: 2^-16 + 2 * 2^-17 = 2^-15 of it
-    (rests are half a step of the upper one at most: 2^-8, rounded to 2^-9 of that).  v0 takes nearly all of it away."""
+    by 2^-8 of it at most, the rest of that by 2^-17 of the factor (half a step of a number up to 2^-8), and the product of
+    the two rests is left out: 2^-16 + 2 * 2^-17 = 2^-15 of it.  v0 takes nearly all of it away."""
     h = 16
     gen = torch.Generator().manual_seed(m + d)
     b = 1 + torch.rand(h, generator=gen)                                   # any 24 bits
